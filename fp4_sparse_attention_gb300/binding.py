@@ -12,6 +12,10 @@ The functions keep the C names:
     fp4idx_logits_topk(problem, w, k, sorted=False, ...) -> (logits, indices, values, valid_count)
     fp4idx_topk_score / fp4idx_topk_merge(...)  -- the streaming plan's two phases
     fp4idx_topk_workspace_bytes(problem, k) -> int
+    fp4idx_latent_attention(attention, stream=None) -> (out [T, H, 512], lse [T, H])
+    fp4idx_paged_attention(attention, stream=None) -> (out [T, H, 128], lse [T, H])
+    fp4idx_store_latent / fp4idx_store_kv(...)  -- the 16-bit caches' writers
+    fp4idx_build_tables(...) -> (cu_seqlens_q, cu_seqlens_k, visible_len, slots, pages_taken)
     fp4idx_get_error(clear=True, stream=None) -> int
 """
 from __future__ import annotations
@@ -32,6 +36,7 @@ FP4IDX_TOPK_STREAMING = 0x2
 ERR_PAGE_RANGE = 0x1
 ERR_TIMEOUT = 0x2
 ERR_TOKEN_TABLE = 0x4
+ERR_LENGTHS = 0x8
 KV_SPLIT = 0
 KV_FUSED = 1
 
@@ -49,6 +54,12 @@ EXPORTED = (
     "fp4idx_topk_score",
     "fp4idx_topk_merge",
     "fp4idx_logits_topk",
+    "fp4idx_attention_workspace_bytes",
+    "fp4idx_latent_attention",
+    "fp4idx_paged_attention",
+    "fp4idx_store_latent",
+    "fp4idx_store_kv",
+    "fp4idx_build_tables",
     "fp4idx_get_error",
     "fp4idx_status_string",
     "fp4idx_last_error_message",
@@ -85,6 +96,42 @@ class CProblem(ctypes.Structure):
         ("kv_layout", ctypes.c_int32),
         ("cand_mask", ctypes.c_void_p),
         ("mask_ld", ctypes.c_int64),
+    ]
+
+
+class CAttention(ctypes.Structure):
+    """Mirror of fp4idx_attention_t."""
+
+    _fields_ = [
+        ("dtype", ctypes.c_int32),
+        ("num_seqs", ctypes.c_int32),
+        ("num_rows", ctypes.c_int32),
+        ("num_heads", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("num_pages", ctypes.c_int64),
+        ("table_stride", ctypes.c_int64),
+        ("max_seqlen_q", ctypes.c_int32),
+        ("max_seqlen_k", ctypes.c_int32),
+        ("q", ctypes.c_void_p),
+        ("q_row_stride", ctypes.c_int64),
+        ("q_head_stride", ctypes.c_int64),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("page_stride", ctypes.c_int64),
+        ("cu_seqlens_q", ctypes.c_void_p),
+        ("cu_seqlens_k", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p),
+        ("page_offsets", ctypes.c_void_p),
+        ("visible_len", ctypes.c_void_p),
+        ("qo_offset", ctypes.c_void_p),
+        ("causal", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("indices", ctypes.c_void_p),
+        ("num_indices", ctypes.c_int32),
+        ("out", ctypes.c_void_p),
+        ("out_row_stride", ctypes.c_int64),
+        ("lse", ctypes.c_void_p),
     ]
 
 
@@ -136,6 +183,19 @@ def load_library(path: str = LIB_PATH):
         lib.fp4idx_topk_score.restype = i32
         lib.fp4idx_topk_merge.argtypes = [P, i32, u32, vp, vp, vp, vp, sz, vp]
         lib.fp4idx_topk_merge.restype = i32
+        A = ctypes.POINTER(CAttention)
+        lib.fp4idx_attention_workspace_bytes.argtypes = [A]
+        lib.fp4idx_attention_workspace_bytes.restype = sz
+        lib.fp4idx_latent_attention.argtypes = [A, vp, sz, vp]
+        lib.fp4idx_latent_attention.restype = i32
+        lib.fp4idx_paged_attention.argtypes = [A, vp, sz, vp]
+        lib.fp4idx_paged_attention.restype = i32
+        lib.fp4idx_store_latent.argtypes = [vp, i64, vp, i64, vp, i32, i32, i64, i64, vp, vp]
+        lib.fp4idx_store_latent.restype = i32
+        lib.fp4idx_store_kv.argtypes = [vp, i64, vp, i64, vp, i32, i32, i32, i64, i64, vp, vp, vp]
+        lib.fp4idx_store_kv.restype = i32
+        lib.fp4idx_build_tables.argtypes = [vp, vp, i32, i32, i32, i64, vp, i32, vp, i64, vp, vp, vp, vp, vp, vp]
+        lib.fp4idx_build_tables.restype = i32
         lib.fp4idx_get_error.argtypes = [ctypes.POINTER(u32), i32, vp]
         lib.fp4idx_get_error.restype = i32
         lib.fp4idx_status_string.argtypes = [i32]
@@ -453,6 +513,163 @@ def fp4idx_topk_merge(problem: DeviceProblem, k: int, indices: torch.Tensor, val
     _check(lib.fp4idx_topk_merge(ctypes.byref(problem.c), int(k), flags, _ptr(indices), _ptr(values),
                                  _ptr(valid_count), _ptr(workspace), workspace.numel(), _stream(stream)),
            "fp4idx_topk_merge")
+
+
+class DeviceAttention:
+    """Device tensors of one attention call plus its fp4idx_attention_t.
+
+    Fields follow include/fp4idx.h.  Latent attention (v None): q [T,H,576], k the
+    cache [P,page,576].  Paged attention: q [T,H,128], k and v [P,Hkv,page,128].
+    cu_seqlens_q/k [B+1] i32, block_table [B,stride] (or flat with page_offsets
+    [B]), visible_len [T], causal, qo_offset [B]; indices [T,n] (latent) or
+    [Hkv,T,n] (paged) i32, or None for the whole prefix.  out, lse and the
+    workspace are allocated here unless given, and kept: a call writes the same
+    tensors again.  The object holds pointers: rebuild it when a tensor moves.
+    """
+
+    def __init__(self, *, q, k, cu_seqlens_q, cu_seqlens_k, block_table, max_seqlen_q: int, max_seqlen_k: int,
+                 scale: float, v=None, page_offsets=None, visible_len=None, causal: bool = False, qo_offset=None,
+                 indices=None, out=None, lse=None, workspace=None):
+        latent = v is None
+        if q.dtype not in (torch.bfloat16, torch.float16) or k.dtype != q.dtype or (v is not None and v.dtype != q.dtype):
+            raise ValueError("q and the caches must all be bfloat16 or all float16")
+        dk, dv = (576, 512) if latent else (128, 128)
+        if q.dim() != 3 or q.shape[2] != dk or q.stride(2) != 1:
+            raise ValueError(f"q must be [T, H, {dk}] with dense rows")
+        if k.dim() != (3 if latent else 4) or k.shape[-1] != dk or not k[0].is_contiguous():
+            raise ValueError("the cache must be [P, page, 576] (latent) or [P, Hkv, page, 128], dense inside a page")
+        if not latent and (v.shape != k.shape or v.stride() != k.stride()):
+            raise ValueError("k and v must have one shape and one set of strides")
+        T, H = q.shape[0], q.shape[1]
+        B = int(cu_seqlens_q.shape[0]) - 1
+        kv_heads = 1 if latent else int(k.shape[1])
+        for name, x, n in (("cu_seqlens_q", cu_seqlens_q, B + 1), ("cu_seqlens_k", cu_seqlens_k, B + 1),
+                           ("page_offsets", page_offsets, B), ("visible_len", visible_len, T), ("qo_offset", qo_offset, B)):
+            if x is not None and (x.dtype != torch.int32 or x.numel() < n or not x.is_contiguous()):
+                raise ValueError(f"{name} must be contiguous int32 with at least {n} entries")
+        if block_table.dtype != torch.int32 or block_table.stride(-1) != 1:
+            raise ValueError("block_table must be int32 with dense rows")
+        if block_table.dim() == 2 and block_table.shape[0] < B:
+            raise ValueError("block_table must have a row for every request")
+        if block_table.dim() != 2 and page_offsets is None:
+            raise ValueError("a flat block_table needs page_offsets")
+        if indices is not None and (indices.dtype != torch.int32 or not indices.is_contiguous()
+                                    or tuple(indices.shape[:-1]) != ((T,) if latent else (kv_heads, T))):
+            raise ValueError("indices must be contiguous int32 [T, n] (latent) or [Hkv, T, n] (paged)")
+        if out is None:
+            out = torch.empty((T, H, dv), dtype=q.dtype, device=q.device)
+        if lse is None:
+            lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+        if tuple(out.shape) != (T, H, dv) or out.dtype != q.dtype or out.stride(2) != 1 or out.stride(1) != dv:
+            raise ValueError(f"out must be [T, H, {dv}] of q's type with dense rows")
+        if tuple(lse.shape) != (T, H) or lse.dtype != torch.float32 or not lse.is_contiguous():
+            raise ValueError("lse must be a contiguous [T, H] float32 tensor")
+        self.q, self.k, self.v = q, k, v
+        self.cu_seqlens_q, self.cu_seqlens_k, self.block_table = cu_seqlens_q, cu_seqlens_k, block_table
+        self.page_offsets, self.visible_len, self.qo_offset = page_offsets, visible_len, qo_offset
+        self.indices, self.out, self.lse = indices, out, lse
+
+        def at(x):
+            return None if x is None else x.data_ptr()
+
+        self.c = CAttention(
+            dtype=0 if q.dtype == torch.bfloat16 else 1, num_seqs=B, num_rows=T, num_heads=H, num_kv_heads=kv_heads,
+            page_size=int(k.shape[-2]), num_pages=int(k.shape[0]),
+            table_stride=int(block_table.stride(0)) if block_table.dim() == 2 else 0, max_seqlen_q=int(max_seqlen_q),
+            max_seqlen_k=int(max_seqlen_k), q=at(q), q_row_stride=int(q.stride(0)), q_head_stride=int(q.stride(1)),
+            k=at(k), v=at(v), page_stride=int(k.stride(0)), cu_seqlens_q=at(cu_seqlens_q),
+            cu_seqlens_k=at(cu_seqlens_k), block_table=at(block_table), page_offsets=at(page_offsets),
+            visible_len=at(visible_len), qo_offset=at(qo_offset), causal=int(bool(causal)), scale=float(scale),
+            indices=at(indices), num_indices=0 if indices is None else int(indices.shape[-1]), out=at(out),
+            out_row_stride=int(out.stride(0)), lse=at(lse))
+        self._ref = ctypes.byref(self.c)
+        need = int(load_library().fp4idx_attention_workspace_bytes(self._ref))
+        if workspace is None:
+            workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=q.device)
+        self.workspace = workspace
+        self._ws = (ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size())
+
+
+def fp4idx_latent_attention(attention: DeviceAttention, stream=None):
+    """Absorbed latent attention of every row over its visible or selected keys: (out [T, H, 512], lse [T, H])."""
+    _check(load_library().fp4idx_latent_attention(attention._ref, *attention._ws, _stream(stream)),
+           "fp4idx_latent_attention")
+    return attention.out, attention.lse
+
+
+def fp4idx_paged_attention(attention: DeviceAttention, stream=None):
+    """Grouped-query attention of every row over its visible keys or selected blocks: (out [T, H, 128], lse [T, H])."""
+    _check(load_library().fp4idx_paged_attention(attention._ref, *attention._ws, _stream(stream)),
+           "fp4idx_paged_attention")
+    return attention.out, attention.lse
+
+
+def fp4idx_store_latent(latent: torch.Tensor, rope: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor,
+                        stream=None) -> None:
+    """Write latent [N, 512] and rope [N, 64] into the latent cache [P, page, 576] at token slots [N] int32."""
+    if latent.dtype not in (torch.bfloat16, torch.float16) or rope.dtype != latent.dtype or cache.dtype != latent.dtype:
+        raise ValueError("latent, rope and cache must all be bfloat16 or all float16")
+    N = latent.shape[0]
+    if tuple(latent.shape) != (N, 512) or tuple(rope.shape) != (N, 64) or latent.stride(1) != 1 or rope.stride(1) != 1:
+        raise ValueError("latent must be [N, 512] and rope [N, 64] with dense rows")
+    if slots.dtype != torch.int32 or slots.numel() != N or not slots.is_contiguous():
+        raise ValueError("slots must be a contiguous [N] int32 tensor")
+    if cache.dim() != 3 or cache.shape[2] != 576 or cache.stride(2) != 1 or cache.stride(1) != 576:
+        raise ValueError("cache must be [P, page, 576], dense inside a page")
+    _check(load_library().fp4idx_store_latent(latent.data_ptr(), latent.stride(0), rope.data_ptr(), rope.stride(0),
+                                              slots.data_ptr(), N, cache.shape[1], cache.shape[0], cache.stride(0),
+                                              cache.data_ptr(), _stream(stream)), "fp4idx_store_latent")
+
+
+def fp4idx_store_kv(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                    stream=None) -> None:
+    """Write k_new, v_new [N, Hkv, 128] into the caches k, v [P, Hkv, page, 128] at token slots [N] int32."""
+    if k_new.dtype not in (torch.bfloat16, torch.float16) or any(x.dtype != k_new.dtype for x in (v_new, k, v)):
+        raise ValueError("k_new, v_new, k and v must all be bfloat16 or all float16")
+    N, Hkv = k_new.shape[0], k_new.shape[1]
+    for x in (k_new, v_new):
+        if tuple(x.shape) != (N, Hkv, 128) or x.stride(2) != 1 or x.stride(1) != 128:
+            raise ValueError("k_new and v_new must be [N, Hkv, 128] with dense heads")
+    if slots.dtype != torch.int32 or slots.numel() != N or not slots.is_contiguous():
+        raise ValueError("slots must be a contiguous [N] int32 tensor")
+    page = k.shape[2]
+    if k.dim() != 4 or k.shape[1] != Hkv or k.shape[3] != 128 or k.shape != v.shape or k.stride() != v.stride() \
+            or k.stride()[1:] != (page * 128, 128, 1):
+        raise ValueError("k and v must be [P, Hkv, page, 128], dense inside a page, with one set of strides")
+    _check(load_library().fp4idx_store_kv(k_new.data_ptr(), k_new.stride(0), v_new.data_ptr(), v_new.stride(0),
+                                          slots.data_ptr(), N, Hkv, page, k.shape[0], k.stride(0), k.data_ptr(),
+                                          v.data_ptr(), _stream(stream)), "fp4idx_store_kv")
+
+
+def fp4idx_build_tables(cached_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.Tensor,
+                        free_pages: torch.Tensor, page_size: int, num_rows: int, num_pages: Optional[int] = None,
+                        out=None, stream=None):
+    """Metadata of one step from its request lengths: (cu_seqlens_q [B+1], cu_seqlens_k [B+1], visible_len [T],
+    slots [T], pages_taken [1]), int32 on the device; block_table [B, stride] gets its new pages in place from
+    free_pages [F].  ``num_pages`` bounds the page ids (default: any); ``out`` may give the five tensors."""
+    B = cached_len.shape[0]
+    for name, x in (("cached_len", cached_len), ("new_len", new_len), ("free_pages", free_pages)):
+        if x.dtype != torch.int32 or x.dim() != 1 or not x.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous 1-D int32 tensor")
+    if new_len.shape[0] != B or block_table.dim() != 2 or block_table.shape[0] != B \
+            or block_table.dtype != torch.int32 or block_table.stride(1) != 1:
+        raise ValueError("new_len must be [B] and block_table [B, stride] int32 with dense rows")
+    if out is None:
+        # one allocation; each array starts at a multiple of four entries
+        size = [(n + 3) // 4 * 4 for n in (B + 1, B + 1, num_rows, num_rows, 1)]
+        flat = torch.empty((sum(size),), dtype=torch.int32, device=cached_len.device).split(size)
+        out = (flat[0][:B + 1], flat[1][:B + 1], flat[2][:num_rows], flat[3][:num_rows], flat[4][:1])
+    cu_q, cu_k, visible, slots, taken = out
+    for x, n in ((cu_q, B + 1), (cu_k, B + 1), (visible, num_rows), (slots, num_rows), (taken, 1)):
+        if x.dtype != torch.int32 or x.numel() != n or not x.is_contiguous():
+            raise ValueError("out: cu_seqlens_q [B+1], cu_seqlens_k [B+1], visible_len [T], slots [T], pages_taken [1]")
+    pages = (2 ** 31 - 1) // page_size if num_pages is None and page_size > 0 else num_pages
+    _check(load_library().fp4idx_build_tables(cached_len.data_ptr(), new_len.data_ptr(), B, num_rows, page_size, pages,
+                                              free_pages.data_ptr(), free_pages.shape[0], block_table.data_ptr(),
+                                              block_table.stride(0), cu_q.data_ptr(), cu_k.data_ptr(),
+                                              visible.data_ptr(), slots.data_ptr(), taken.data_ptr(),
+                                              _stream(stream)), "fp4idx_build_tables")
+    return out
 
 
 def fp4idx_get_error(clear: bool = True, stream=None) -> int:

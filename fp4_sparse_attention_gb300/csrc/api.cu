@@ -6,6 +6,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "attention.h"
 #include "fp4idx.h"
 #include "internal.h"
 
@@ -287,6 +288,15 @@ TopkWorkspace topk_workspace(const fp4idx_problem_t* p, int32_t k, int sms) {
 }
 
 }  // namespace
+
+fp4idx_status_t call_device(int* sms, uint32_t** err) {
+  DeviceInfo* dev;
+  fp4idx_status_t s = device_info(&dev);
+  if (s != FP4IDX_OK) return s;
+  *sms = dev->sms;
+  *err = dev->err;
+  return FP4IDX_OK;
+}
 
 void set_last_error(const char* fmt, ...) {
   va_list ap;

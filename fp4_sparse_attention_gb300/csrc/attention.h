@@ -1,0 +1,123 @@
+// attention.h -- parameters shared by the attention host layer
+// (api_attention.cu) and its kernels.  Not part of the public ABI.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "fp4idx.h"
+
+namespace fp4idx {
+
+constexpr uint32_t kErrLengths = 0x8u;  // FP4IDX_ERR_LENGTHS
+
+constexpr int kLatentDim = 512;  // shared latent values of a token (keys and values)
+constexpr int kRopeDim = 64;     // rotary values of a token (keys only)
+constexpr int kPagedDim = 128;   // head size of the paged K/V cache
+constexpr int kSelectBlock = 128;  // keys of one selectable block
+
+struct AttnParams {
+  const uint16_t* q;
+  int64_t q_row_stride, q_head_stride;  // elements
+  const uint16_t* k;
+  const uint16_t* v;                    // paged; the latent cache holds both in k
+  int64_t page_stride;                  // elements
+  int64_t num_pages;
+  const int32_t* cu_seqlens_q;
+  const int32_t* cu_seqlens_k;
+  const int32_t* block_table;
+  const int32_t* page_offsets;
+  int64_t table_stride;
+  const int32_t* visible_len;
+  const int32_t* qo_offset;
+  int32_t causal;
+  int32_t page_size, page_shift;
+  int32_t num_seqs, num_rows, num_heads, num_kv_heads;
+  int32_t group;                        // num_heads / num_kv_heads
+  int32_t max_seqlen_q, max_seqlen_k;
+  const int32_t* indices;               // nullptr: whole prefix
+  int32_t num_indices;
+  float scale_log2;                     // scale * log2(e): scores in powers of two
+  uint16_t* out;
+  int64_t out_row_stride;
+  float* lse;
+  uint32_t* err;
+};
+
+// Rows copied into a paged cache by slot: up to two sources, each a run of
+// `units` 16-byte pieces per (token, head).
+struct StoreRowsPart {
+  const uint16_t* src;   // (token, head) at src + token*token_stride + head*head_stride (elements)
+  int64_t token_stride, head_stride;
+  uint16_t* dst;         // (page, head, offset) at dst + page*page_stride + head*dst_head_stride + offset*dst_row
+  int64_t dst_head_stride;
+  int32_t dst_row;       // elements
+  int32_t units;         // 16-byte pieces per (token, head)
+};
+struct StoreRowsParams {
+  StoreRowsPart part[2];
+  const int32_t* slots;
+  int32_t num_tokens, heads;
+  int32_t page_size, page_shift;
+  int64_t num_pages, page_stride;
+  uint32_t* err;
+};
+
+struct TablesParams {
+  const int32_t* cached_len;
+  const int32_t* new_len;
+  int32_t num_reqs, num_rows;
+  int32_t page_size, page_shift;
+  int64_t num_pages;
+  const int32_t* free_pages;
+  int32_t num_free;
+  int32_t* block_table;
+  int64_t table_stride;
+  int32_t* cu_seqlens_q;
+  int32_t* cu_seqlens_k;
+  int32_t* visible_len;
+  int32_t* slots;
+  int32_t* pages_taken;
+  int32_t reqs_per_cta;
+  uint32_t* err;
+};
+
+// SM count and error word of the current device (api.cu).
+fp4idx_status_t call_device(int* sms, uint32_t** err);
+
+cudaError_t launch_attention(const AttnParams& p, int dtype, cudaStream_t stream);
+cudaError_t launch_store_rows(const StoreRowsParams& p, cudaStream_t stream);
+cudaError_t launch_tables(TablesParams p, int sms, cudaStream_t stream);
+
+#ifdef __CUDACC__
+// ---------------------------------------------------------------- device helpers
+// Request of row t: the last b with cu_seqlens_q[b] <= t (num_seqs >= 1).
+__device__ __forceinline__ int attn_request(const AttnParams& p, int t) {
+  int lo = 0, hi = p.num_seqs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(p.cu_seqlens_q + mid) <= t) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+// Positions row t of request b sees: [0, the result).
+__device__ __forceinline__ int attn_visible(const AttnParams& p, int b, int t) {
+  const int k_len = min(max(0, __ldg(p.cu_seqlens_k + b + 1) - __ldg(p.cu_seqlens_k + b)), p.max_seqlen_k);
+  int64_t vis = k_len;
+  if (p.visible_len) {
+    vis = __ldg(p.visible_len + t);
+  } else if (p.causal) {
+    const int q0 = __ldg(p.cu_seqlens_q + b), q_len = __ldg(p.cu_seqlens_q + b + 1) - q0;
+    const int64_t off = p.qo_offset ? static_cast<int64_t>(__ldg(p.qo_offset + b))
+                                    : static_cast<int64_t>(k_len) - q_len;
+    vis = static_cast<int64_t>(t - q0) + off + 1;
+  }
+  vis = vis < 0 ? 0 : vis;
+  return static_cast<int>(vis > k_len ? k_len : vis);
+}
+__device__ __forceinline__ int64_t attn_table_base(const AttnParams& p, int b) {
+  return p.page_offsets ? static_cast<int64_t>(__ldg(p.page_offsets + b)) : static_cast<int64_t>(b) * p.table_stride;
+}
+#endif
+
+}  // namespace fp4idx

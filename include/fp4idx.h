@@ -15,7 +15,10 @@
  * 类型"), and the top-k positions of each row.  Around them: the top-k blocks
  * of a block-score tensor, the physical cache slots of selected positions
  * (the sparse-attention consumer's input) and the MXFP4 K-cache writer (the
- * producer of the cache).
+ * producer of the cache).  After them: the attention that consumes a
+ * selection (or a whole prefix) from 16-bit paged caches -- over one shared
+ * latent vector a token, or grouped-query -- with the caches' writers, and
+ * the request metadata and slots of a step from its request lengths.
  *
  * Formats (M3-indexer README, "FP4 和 scale layout"; SGLang PR 42861,
  * "Modifications"):
@@ -76,6 +79,9 @@ typedef enum fp4idx_status {
                                        request's slots is not one cache page in
                                        order, or the rows' requests are not
                                        non-decreasing                            */
+#define FP4IDX_ERR_LENGTHS 0x8u     /* fp4idx_build_tables: a negative length, more rows
+                                       than the caller's row count, a request longer than
+                                       its table row, or too few free pages         */
 
 /* Key-cache layouts (fp4idx_problem_t.kv_layout). */
 #define FP4IDX_KV_SPLIT 0  /* k [P][Hkv][page][64] and k_scale [P][Hkv][page][G]     */
@@ -411,6 +417,160 @@ fp4idx_status_t fp4idx_pages_from_token_table(const int32_t* req, int32_t num_ro
 fp4idx_status_t fp4idx_topk_slots(const fp4idx_problem_t* problem, const int32_t* indices,
                                   int32_t k, int32_t* slots, int32_t ncols,
                                   int32_t* offset_bits, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Attention over 16-bit paged caches, and what it needs around it.
+ * ---------------------------------------------------------------------- */
+
+/* Element type of q, the caches and the outputs (one type per call). */
+typedef enum fp4idx_dtype {
+  FP4IDX_BF16 = 0,
+  FP4IDX_FP16 = 1
+} fp4idx_dtype_t;
+
+/*
+ * One attention call.  For every query row t (request b) and head h
+ *
+ *     s(t,h,j) = scale * q[t,h] . k[j]                 j in keys(t)
+ *     out[t,h] = sum_j exp(s - lse(t,h)) * v[j]
+ *     lse(t,h) = log sum_j exp(s(t,h,j))
+ *
+ * in fp32 from 16-bit operands; the weights exp(s - m) are rounded to the
+ * operand type before they multiply v (the tensor cores take 16-bit operands),
+ * their sum is not.  A row without keys, or whose scores are all -inf, gets
+ * out = 0 and lse = -inf.
+ *
+ *   fp4idx_latent_attention  (absorbed latent attention) v == NULL; one cache
+ *       k [num_pages][page_size][576]: a token's 512 latent values, then its 64
+ *       rotary values; k[j] = all 576, v[j] = the first 512; num_kv_heads = 1,
+ *       any num_heads; q [T][H][576], out [T][H][512].
+ *       indices  NULL: keys(t) = the visible positions of row t;
+ *                [T][num_indices] int32: the listed logical positions
+ *                (fp4idx_topk's output) that are visible to row t.
+ *   fp4idx_paged_attention  k and v [num_pages][Hkv][page_size][128], head h
+ *       reads K/V head h / (H/Hkv); q [T][H][128], out [T][H][128].
+ *       indices  NULL: keys(t) = the visible positions of row t;
+ *                [Hkv][T][num_indices] int32: the visible positions of the
+ *                listed 128-key blocks (block i = positions 128i .. 128i+127;
+ *                fp4idx_block_topk's output for Hkv index heads).
+ *       An index that is negative or names nothing visible is no key (-1
+ *       padding); indices may come in any order; one listed twice counts twice.
+ *
+ * Visible positions are those of fp4idx_problem_t (visible_len; causal with
+ * qo_offset; all keys).  cu_seqlens_q/k, block_table, page_offsets,
+ * table_stride, max_seqlen_q/k as there.  A block-table entry outside
+ * [0, num_pages) under a visible position sets FP4IDX_ERR_PAGE_RANGE and its
+ * keys count as not visible.  Cache contents that no row of the call may see
+ * are never used and may hold anything (NaN included); a position that some
+ * row of a request sees must hold finite values for the others, too.
+ *
+ *   q           element (t,h,d) at q + t*q_row_stride + h*q_head_stride + d
+ *               (elements; strides multiples of 8, 16-byte aligned base).
+ *   k, v        page p at k + p*page_stride (elements; a multiple of 8, at
+ *               least one page's content; 16-byte aligned bases; a cache may
+ *               be one layer's slice of a larger allocation and exceed 2^31
+ *               elements).
+ *   out         [T][H][dv], row stride out_row_stride elements (>= H*dv, a
+ *               multiple of 8), 16-byte aligned; head stride dv.
+ *   lse         [T][H] fp32, natural logarithm, or NULL.
+ *   scale       finite.
+ *
+ * Workspace: fp4idx_attention_workspace_bytes() bytes of device memory,
+ * 16-byte aligned, uninitialised (0 for an invalid argument: the call then
+ * returns the matching status).  The result does not depend on its contents
+ * and is the same from call to call.  No allocation, no synchronisation;
+ * graph-capturable; replays see updated device metadata.
+ * Supported: page_size 64 or 128; num_indices <= 2^20; num_heads <= 1024.
+ */
+typedef struct fp4idx_attention {
+  int32_t dtype;            /* fp4idx_dtype_t */
+  int32_t num_seqs;
+  int32_t num_rows;
+  int32_t num_heads;
+  int32_t num_kv_heads;
+  int32_t page_size;
+  int64_t num_pages;
+  int64_t table_stride;
+  int32_t max_seqlen_q;
+  int32_t max_seqlen_k;
+  const void* q;
+  int64_t q_row_stride;
+  int64_t q_head_stride;
+  const void* k;
+  const void* v;
+  int64_t page_stride;
+  const int32_t* cu_seqlens_q;
+  const int32_t* cu_seqlens_k;
+  const int32_t* block_table;
+  const int32_t* page_offsets;
+  const int32_t* visible_len;
+  const int32_t* qo_offset;
+  int32_t causal;
+  float scale;
+  const int32_t* indices;
+  int32_t num_indices;
+  void* out;
+  int64_t out_row_stride;
+  float* lse;
+} fp4idx_attention_t;
+
+size_t fp4idx_attention_workspace_bytes(const fp4idx_attention_t* attention);
+fp4idx_status_t fp4idx_latent_attention(const fp4idx_attention_t* attention, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+fp4idx_status_t fp4idx_paged_attention(const fp4idx_attention_t* attention, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
+/*
+ * Write 16-bit rows into the caches of fp4idx_attention_t by slot (token i at
+ * page slots[i] / page_size, offset slots[i] % page_size; a negative slot is
+ * skipped, one past the cache is skipped and sets FP4IDX_ERR_PAGE_RANGE; two
+ * tokens with one slot: either may win).  The values are copied unchanged.
+ *   fp4idx_store_latent  latent [N][512] and rope [N][64] (element strides
+ *       latent_stride, rope_stride between tokens) into cache
+ *       [num_pages][page_size][576].
+ *   fp4idx_store_kv      k_new, v_new [N][Hkv][128] (token strides k_stride,
+ *       v_stride) into k, v [num_pages][Hkv][page_size][128].
+ * Strides and page_stride are multiples of 8 elements, bases 16-byte aligned.
+ * Graph-capturable, no workspace, one launch (none for num_tokens == 0).
+ */
+fp4idx_status_t fp4idx_store_latent(const void* latent, int64_t latent_stride, const void* rope,
+                                    int64_t rope_stride, const int32_t* slots, int32_t num_tokens,
+                                    int32_t page_size, int64_t num_pages, int64_t page_stride, void* cache,
+                                    void* stream);
+fp4idx_status_t fp4idx_store_kv(const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
+                                const int32_t* slots, int32_t num_tokens, int32_t num_kv_heads,
+                                int32_t page_size, int64_t num_pages, int64_t page_stride, void* k, void* v,
+                                void* stream);
+
+/*
+ * Metadata of one step from its request lengths, on the device.  Request b
+ * holds cached_len[b] tokens in its pages block_table[b][0 ..
+ * ceil(cached_len/page_size)) and gets new_len[b] (>= 0) more rows; pages it
+ * lacks are taken from free_pages in order, request 0's first.
+ *   cu_seqlens_q [B+1]  prefix sums of new_len.
+ *   cu_seqlens_k [B+1]  prefix sums of cached_len + new_len.
+ *   block_table  [B][table_stride] int32, in place: the new pages are entered
+ *                behind the held ones; other entries are not touched.  (A call
+ *                repeated with the same lengths enters the same pages again.)
+ *   visible_len  [T] row i of request b sees cached_len[b] + i + 1 positions.
+ *   slots        [T] page * page_size + offset of each row's token (input of the
+ *                store calls).
+ *   pages_taken  [1] the number of free pages used.
+ * T = num_rows is the host's row count; rows past the requests' sum get
+ * visible_len 0 and slot -1.  FP4IDX_ERR_LENGTHS: a negative length (counted
+ * as 0), a sum of new rows above num_rows (the rows past it are not written),
+ * a request that needs more than table_stride pages or a free list that is too
+ * short (the page is entered as -1 where the row has room, its rows' slots are
+ * -1).  A held page outside [0, num_pages) gives slots -1 and
+ * FP4IDX_ERR_PAGE_RANGE.  One launch, no workspace, graph-capturable.
+ * Supported: page_size 64 or 128, num_pages * page_size < 2^31, and key
+ * counts that sum to less than 2^31.
+ */
+fp4idx_status_t fp4idx_build_tables(const int32_t* cached_len, const int32_t* new_len, int32_t num_reqs,
+                                    int32_t num_rows, int32_t page_size, int64_t num_pages,
+                                    const int32_t* free_pages, int32_t num_free, int32_t* block_table,
+                                    int64_t table_stride, int32_t* cu_seqlens_q, int32_t* cu_seqlens_k,
+                                    int32_t* visible_len, int32_t* slots, int32_t* pages_taken, void* stream);
 
 /*
  * Device error word of the current device (FP4IDX_ERR_* bits).  Synchronises
