@@ -118,7 +118,12 @@ fp4idx_status_t attention_any(const fp4idx_attention_t* a, bool latent, void* wo
   AttnParams p = attention_params(a);
   int sms = 0;
   if ((s = call_device(&sms, &p.err)) != FP4IDX_OK) return s;
-  return cuda_status(launch_attention(p, a->dtype, static_cast<cudaStream_t>(stream)), "attention launch");
+  if (!plan_attention(&p, sms)) FAIL(FP4IDX_EUNSUPPORTED, "more than 2^31 work items");
+  const size_t need = attention_workspace(p);
+  if (!workspace || workspace_bytes < need)
+    FAIL(FP4IDX_EWORKSPACE, "workspace of %zu bytes is smaller than %zu", workspace ? workspace_bytes : size_t{0}, need);
+  if (!aligned(workspace, 16)) FAIL(FP4IDX_EINVAL, "workspace must be 16-byte aligned");
+  return cuda_status(launch_attention(p, a->dtype, workspace, static_cast<cudaStream_t>(stream)), "attention launch");
 }
 
 // Arguments that both cache writers share.
@@ -167,8 +172,11 @@ extern "C" {
 
 size_t fp4idx_attention_workspace_bytes(const fp4idx_attention_t* attention) {
   set_last_error("%s", "");
-  if (!attention || check_attention(attention, attention->v == nullptr) != FP4IDX_OK) return 0;
-  return 0;
+  if (check_attention(attention, attention && attention->v == nullptr) != FP4IDX_OK) return 0;
+  AttnParams p = attention_params(attention);
+  int sms = 0;
+  if (attention->num_rows == 0 || call_device(&sms, &p.err) != FP4IDX_OK || !plan_attention(&p, sms)) return 0;
+  return attention_workspace(p);
 }
 
 fp4idx_status_t fp4idx_latent_attention(const fp4idx_attention_t* attention, void* workspace, size_t workspace_bytes,

@@ -1,22 +1,196 @@
-// attention.cu -- attention over the 16-bit paged caches (fp4idx_latent_attention,
-// fp4idx_paged_attention): one CTA per (row, head), one key per thread for the
-// scores and one or four output dimensions per thread for the weighted sum, with a
-// running maximum and sum over tiles of 128 keys.
+// attention.cu -- attention over the 16-bit paged caches for sm_103a
+// (fp4idx_latent_attention, fp4idx_paged_attention).
+//
+//   s(r, j) = scale * q[r] . k[j],   out[r] = sum_j exp(s - lse) v[j]
+//
+// One CTA owns up to 64 query rows that share their keys -- the (row, head)
+// pairs of one request and K/V head, or of one row when every row has its own
+// selection -- and walks the keys in tiles, with a running maximum and sum:
+//
+//   S   [64 rows x TK keys]  = Q K^T     tcgen05, M = 64 rows, N = TK keys
+//   P   = 2^(S - m)                      registers, rounded to 16 bits once
+//   O^T [dv x 64 rows]      += V^T P^T   tcgen05, M = 128 of dv, N = rows
+//
+// The second product is transposed so that M is the value dimension: 64 rows
+// on M would use half of the tensor pipe, and O^T of 512 values x 64 rows
+// takes 256 TMEM columns where O would take all 512.  Both operands of both
+// products come from one copy of the keys in shared memory: a key's row lies
+// in 128-byte swizzled pieces of 64 values, which is the K-major layout Q K^T
+// wants and, read along the other axis, the MN-major layout V^T wants; for
+// the latent cache K and V are even the same bytes.
+//
+// Roles (13 warps, one CTA per SM):
+//   warps 0-3   softmax: TMEM S as row fragments (four lanes per row), mask,
+//               running maximum, 2^x, P to shared memory; rescale of O^T when
+//               a row's maximum grew by more than 2^8 (until then the older
+//               maximum serves as the reference: weights stay below 2^8 and
+//               the result is the same up to rounding); the output.
+//   warp 4      MMA issuer: whichever of the next tile's Q K^T and this
+//               tile's V^T P^T is ready.
+//   warps 5-12  loaders: page lookup or selection, 16-byte asynchronous copies
+//               (zeros for keys that do not exist), key positions.
+//
+// Work split: the tiles of all items (request or row, K/V head, row chunk)
+// are concatenated and cut into equal runs, one per CTA group, so long and
+// short requests balance; the `members` CTAs of a group walk the same keys
+// for different row chunks, close enough in time for the L2 to serve the
+// second reader.  An item cut by a boundary leaves partial sums that
+// join_kernel adds in a fixed order.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cstring>
+
 #include "attention.h"
-#include "ptx.cuh"
+#include "attn_ptx.cuh"
 
 namespace fp4idx {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kSoftmaxWarps = 4, kMmaWarp = 4, kLoadWarps = 8;
+constexpr int kThreads = 32 * (kSoftmaxWarps + 1 + kLoadWarps);
+constexpr int kLoadThreads = 32 * kLoadWarps;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kMaxMembers = 8;
+// A row's reference maximum is raised only when the true one is 2^8 above it.
+constexpr float kRaise = 8.0f;
+
+template <bool LATENT>
+struct Cfg {
+  static constexpr int kDk = LATENT ? kLatentDim + kRopeDim : kPagedDim;
+  static constexpr int kDv = LATENT ? kLatentDim : kPagedDim;
+  static constexpr int kTk = LATENT ? 64 : 128;                 // keys per tile
+  static constexpr int kStages = LATENT ? 2 : 3;
+  static constexpr int kKc = kDk / 64;                          // 128-byte pieces of a key
+  static constexpr int kVc = LATENT ? 0 : kDv / 64;             // pieces of a separate value row
+  static constexpr uint32_t kPiece = kTk * 128;                 // one piece of every key of a tile
+  static constexpr uint32_t kStage = (kKc + kVc) * kPiece;
+  static constexpr uint32_t kV = LATENT ? 0 : kKc * kPiece;     // values inside a stage
+  static constexpr uint32_t kQ = kKc * kChunkRows * 128;
+  static constexpr uint32_t kP = kTk / 64 * kChunkRows * 128;
+  static constexpr uint32_t kOff_Q = kStages * kStage;
+  static constexpr uint32_t kOff_P = kOff_Q + kQ;
+  static constexpr uint32_t kOff_Ctl = kOff_P + kP;
+  static constexpr uint32_t kOCols = kDv / 128 * kChunkRows;    // O^T: 64 columns per 128 values
+};
+
+template <bool LATENT>
+struct Control {
+  uint64_t kfull[Cfg<LATENT>::kStages], kempty[Cfg<LATENT>::kStages];
+  uint64_t sfull[2], sempty[2], pfull, pvdone, qfull, qempty, oempty, drain;
+  int64_t row_off[kChunkRows];                                 // output element of each row
+  int64_t plan[4];                                             // first item, its first tile, lo, hi
+  int32_t key_pos[Cfg<LATENT>::kStages][Cfg<LATENT>::kTk];     // logical position, -1: no key
+  float factor[kChunkRows], row_m[kChunkRows], row_l[kChunkRows];
+  uint32_t tmem;
+  int abort;
+};
+
+template <bool LATENT>
+constexpr uint32_t smem_bytes() {
+  return Cfg<LATENT>::kOff_Ctl + sizeof(Control<LATENT>);
+}
+static_assert(smem_bytes<true>() <= 232448 && smem_bytes<false>() <= 232448, "227 KB per CTA");
+
+// ---------------------------------------------------------------- items
+struct Item {
+  int b, hk;
+  int q0;        // first row of the request (or the row of a selection)
+  int rows;      // (row, head) pairs: rows of the request x group
+  int c0;        // first pair of the chunk group
+};
+
+__device__ __forceinline__ Item item_of(const AttnParams& p, int item) {
+  Item it;
+  const int cg = item % p.chunk_groups, x = item / p.chunk_groups;
+  it.hk = x % p.num_kv_heads;
+  const int u = x / p.num_kv_heads;
+  if (p.indices) {
+    it.q0 = u;
+    it.b = attn_request(p, u);
+    it.rows = p.group;
+  } else {
+    it.b = u;
+    it.q0 = __ldg(p.cu_seqlens_q + u);
+    it.rows = max(0, min(__ldg(p.cu_seqlens_q + u + 1), p.num_rows) - it.q0) * p.group;
+  }
+  it.c0 = cg * p.members * kChunkRows;
+  return it;
+}
+
+// Largest visible length of the rows that pairs [c, c + n) belong to; called
+// by `step` threads with lane = 0..step-1, each giving its share.
+__device__ __forceinline__ int pairs_max_visible(const AttnParams& p, const Item& it, int c, int n, int lane, int step) {
+  const int first = it.q0 + c / p.group, last = it.q0 + (c + n - 1) / p.group;
+  if (!p.visible_len) return attn_visible(p, it.b, last);  // grows with the row
+  int v = 0;
+  for (int t = first + lane; t <= last; t += step) v = max(v, attn_visible(p, it.b, t));
+  return v;
+}
+
+// Key tiles of an item (0 without rows; at least one otherwise, so that a row
+// without keys is written too).
+template <int TK>
+__device__ __forceinline__ int item_tiles(const AttnParams& p, const Item& it, int lane, int step) {
+  const int n = min(it.rows - it.c0, p.members * kChunkRows);
+  if (n <= 0) return 0;
+  if (p.indices) return p.list_tiles;
+  int v = pairs_max_visible(p, it, it.c0, n, lane, step);
+  if (step > 1) v = __reduce_max_sync(0xffffffffu, v);
+  return max(1, (v + TK - 1) / TK);
+}
+
+__device__ __forceinline__ int64_t run_start(int64_t total, int group, int groups) {
+  return static_cast<int64_t>(static_cast<uint64_t>(total) * group / groups);
+}
+__device__ __forceinline__ int used_groups(const AttnParams& p, int64_t total) {
+  return total < p.groups ? static_cast<int>(total) : p.groups;
+}
+
+// The part of an item that one CTA computes.
+struct Segment {
+  Item it;
+  int c, rows;       // its pairs [c, c + rows) of the request
+  int max_vis;       // largest visible length among them
+  int lo, hi, tiles; // key tiles [lo, hi) of the item's `tiles`
+};
+
+// Calls f(segment) for every segment of this CTA, in order; whole warps.
+template <int TK, class F>
+__device__ __forceinline__ void for_segments(const AttnParams& p, const int64_t* plan, int member, F&& f) {
+  const int lane = threadIdx.x & 31;
+  int item = static_cast<int>(plan[0]);
+  int64_t start = plan[1], pos = plan[2];
+  const int64_t hi = plan[3];
+  while (pos < hi) {
+    Segment s;
+    s.it = item_of(p, item);
+    s.tiles = item_tiles<TK>(p, s.it, lane, 32);
+    const int64_t end = min(hi, start + s.tiles);
+    if (end > pos) {
+      s.c = s.it.c0 + member * kChunkRows;
+      s.rows = min(kChunkRows, s.it.rows - s.c);
+      s.lo = static_cast<int>(pos - start);
+      s.hi = static_cast<int>(end - start);
+      if (s.rows > 0) {
+        s.max_vis = __reduce_max_sync(0xffffffffu, pairs_max_visible(p, s.it, s.c, s.rows, lane, 32));
+        f(s);
+      }
+      pos = end;
+    }
+    start += s.tiles;
+    ++item;
+  }
+}
 
 template <int DTYPE>
-__device__ __forceinline__ float to_float(uint16_t w) {
-  if constexpr (DTYPE == FP4IDX_BF16) return __uint_as_float(static_cast<uint32_t>(w) << 16);
-  return __half2float(__ushort_as_half(w));
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if constexpr (DTYPE == FP4IDX_BF16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 template <int DTYPE>
 __device__ __forceinline__ uint16_t from_float(float x) {
@@ -24,98 +198,612 @@ __device__ __forceinline__ uint16_t from_float(float x) {
   return __half_as_ushort(__float2half_rn(x));
 }
 
-__device__ __forceinline__ float block_reduce(float v, bool is_max, float* red) {
+// ln(sum) of a row with reference maximum m (in powers of two) and sum l.
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
+}
+
+// ---------------------------------------------------------------- kernel
+template <int DTYPE, bool LATENT>
+__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ AttnParams p) {
+  using C = Cfg<LATENT>;
+  constexpr int TK = C::kTk;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Control<LATENT>& ctl = *reinterpret_cast<Control<LATENT>*>(smem + C::kOff_Ctl);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t base = smem_u32(smem);
+  volatile int* abort_flag = &ctl.abort;
+
+  if (base & 1023u) {  // the swizzled layouts need it; the runtime places the window there
+    if (tid == 0) {
+      p.info[3] = 0;
+      atomicOr(p.err, kErrTimeout);
+    }
+    return;
+  }
+  if (tid == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(smem_u32(&ctl.kfull[s]), kLoadThreads + kLoadThreads / 8);
+      mbar_init(smem_u32(&ctl.kempty[s]), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&ctl.sfull[s]), 1);
+      mbar_init(smem_u32(&ctl.sempty[s]), kSoftmaxWarps);
+    }
+    mbar_init(smem_u32(&ctl.pfull), kSoftmaxWarps);
+    mbar_init(smem_u32(&ctl.pvdone), 1);
+    mbar_init(smem_u32(&ctl.qfull), kLoadThreads);
+    mbar_init(smem_u32(&ctl.qempty), 1);
+    mbar_init(smem_u32(&ctl.oempty), kSoftmaxWarps);
+    mbar_init(smem_u32(&ctl.drain), 1);
+    ctl.abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) tmem_alloc<kTmemCols>(smem_u32(&ctl.tmem));
+  pdl_wait();  // everything below reads what earlier kernels wrote
+
+  // ---- the run of tiles of this CTA's group
+  const int group = blockIdx.x / p.members, member = blockIdx.x - group * p.members;
+  if (p.indices) {
+    if (tid == 0) {
+      const int64_t total = static_cast<int64_t>(p.items) * p.list_tiles;
+      const int used = used_groups(p, total);
+      const int64_t lo = group < used ? run_start(total, group, used) : total;
+      const int64_t item = group < used ? lo / p.list_tiles : 0;
+      ctl.plan[0] = item;
+      ctl.plan[1] = item * p.list_tiles;
+      ctl.plan[2] = lo;
+      ctl.plan[3] = group < used ? run_start(total, group + 1, used) : total;
+      if (member == 0) {
+        int64_t* info = p.info + 4 * group;
+        info[0] = item;
+        info[1] = item * p.list_tiles;
+        info[2] = p.list_tiles;
+        info[3] = total;
+      }
+    }
+  } else {
+    // every thread sums a run of items; then the thread whose run holds this
+    // group's first tile finds the item (the key ring is not in use yet)
+    int64_t* warp_sum = reinterpret_cast<int64_t*>(smem);
+    const int per = (p.items + kThreads - 1) / kThreads;
+    const int first = min(p.items, tid * per), last = min(p.items, first + per);
+    int64_t mine = 0;
+    for (int i = first; i < last; ++i) mine += item_tiles<TK>(p, item_of(p, i), 0, 1);
+    int64_t incl = mine;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const float w = __shfl_xor_sync(0xffffffffu, v, o);
-    v = is_max ? fmaxf(v, w) : v + w;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int64_t before = incl - mine, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      before += w < warp ? warp_sum[w] : 0;
+      total += warp_sum[w];
+    }
+    const int used = used_groups(p, total);
+    const int64_t lo = group < used ? run_start(total, group, used) : total;
+    if (tid == 0) {
+      ctl.plan[2] = lo;
+      ctl.plan[3] = group < used ? run_start(total, group + 1, used) : total;
+      if (member == 0) p.info[4 * group + 3] = total;
+    }
+    if (group < used && before <= lo && lo < before + mine) {
+      int i = first;
+      int n = item_tiles<TK>(p, item_of(p, i), 0, 1);
+      while (before + n <= lo) {
+        before += n;
+        ++i;
+        n = item_tiles<TK>(p, item_of(p, i), 0, 1);
+      }
+      ctl.plan[0] = i;
+      ctl.plan[1] = before;
+      if (member == 0) {
+        int64_t* info = p.info + 4 * group;
+        info[0] = i;
+        info[1] = before;
+        info[2] = n;
+      }
+    }
   }
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  tc_fence_after();
+  const uint32_t tmem = ctl.tmem;
+  const uint32_t s_col = C::kOCols;  // two score buffers behind O^T
+
+  if (warp >= kMmaWarp + 1) {
+    // ================================================================ loaders
+    const int lt = tid - 32 * (kMmaWarp + 1);
+    const int u = lt & 7;                                   // 16-byte unit of a 128-byte piece
+    constexpr int kPasses = TK / (kLoadThreads / 8);
+    uint32_t g = 0, seg = 0;
+    bool ok = true;
+    for_segments<TK>(p, ctl.plan, member, [&](const Segment& s) {
+      if (!ok) return;
+      const int64_t table = attn_table_base(p, s.it.b);
+      const int32_t* list = nullptr;
+      if (p.indices)
+        list = p.indices + (LATENT ? static_cast<int64_t>(s.it.q0)
+                                   : static_cast<int64_t>(s.it.hk) * p.num_rows + s.it.q0) * p.num_indices;
+      // position and cache element of this thread's keys of tile i
+      int32_t pos[kPasses];
+      int64_t at[kPasses];
+      auto locate = [&](int i) {
+#pragma unroll
+        for (int n = 0; n < kPasses; ++n) {
+          const int64_t j = static_cast<int64_t>(i) * TK + n * (kLoadThreads / 8) + (lt >> 3);
+          int32_t q = -1;
+          if (!list) {
+            if (j < s.max_vis) q = static_cast<int32_t>(j);
+          } else if (LATENT) {
+            if (j < p.num_indices) q = __ldg(list + j);
+          } else {  // a tile is one listed block
+            const int32_t blk = __ldg(list + i);
+            if (blk >= 0 && blk <= (INT32_MAX - kSelectBlock) / kSelectBlock) q = blk * kSelectBlock + static_cast<int32_t>(j % kSelectBlock);
+          }
+          if (q >= s.max_vis) q = -1;
+          pos[n] = q;
+          at[n] = 0;
+          if (q >= 0) {
+            const int64_t page = __ldg(p.block_table + table + (q >> p.page_shift));
+            if (page < 0 || page >= p.num_pages) {
+              if (u == 0) atomicOr(p.err, kErrPageRange);
+              pos[n] = -1;
+            } else {
+              at[n] = page * p.page_stride +
+                      (static_cast<int64_t>(s.it.hk) * p.page_size + (q & (p.page_size - 1))) * C::kDk;
+            }
+          }
+        }
+      };
+      locate(s.lo);
+      // queries of the segment, once the previous segment's products are done
+      ok = warp_wait(smem_u32(&ctl.qempty), (seg & 1) ^ 1, abort_flag, p.err);
+      if (!ok) return;
+#pragma unroll
+      for (int n = 0; n < kChunkRows / (kLoadThreads / 8); ++n) {
+        const int r = n * (kLoadThreads / 8) + (lt >> 3);
+        const bool have = r < s.rows;
+        const int t = s.it.q0 + (s.c + (have ? r : 0)) / p.group, h = s.it.hk * p.group + (s.c + (have ? r : 0)) % p.group;
+        const uint16_t* src = p.q + t * p.q_row_stride + h * p.q_head_stride + u * 8;
+        const uint32_t dst = base + C::kOff_Q + r * 128 + ((u ^ (r & 7)) << 4);
+#pragma unroll
+        for (int c = 0; c < C::kKc; ++c) cp_async_16_or_zero(dst + c * (kChunkRows * 128), src + c * 64, have);
+      }
+      cp_async_arrive(smem_u32(&ctl.qfull));
+      for (int i = s.lo; i < s.hi; ++i, ++g) {
+        const uint32_t st = g % C::kStages;
+        ok = warp_wait(smem_u32(&ctl.kempty[st]), ((g / C::kStages) & 1) ^ 1, abort_flag, p.err);
+        if (!ok) return;
+#pragma unroll
+        for (int n = 0; n < kPasses; ++n) {
+          const int key = n * (kLoadThreads / 8) + (lt >> 3);
+          const bool have = pos[n] >= 0;
+          const uint32_t dst = base + st * C::kStage + key * 128 + ((u ^ (key & 7)) << 4);
+          const uint16_t* src = p.k + at[n] + u * 8;
+#pragma unroll
+          for (int c = 0; c < C::kKc; ++c) cp_async_16_or_zero(dst + c * C::kPiece, src + c * 64, have);
+          if constexpr (!LATENT) {
+            const uint16_t* vsrc = p.v + at[n] + u * 8;
+#pragma unroll
+            for (int c = 0; c < C::kVc; ++c) cp_async_16_or_zero(dst + C::kV + c * C::kPiece, vsrc + c * 64, have);
+          }
+          if (u == 0) ctl.key_pos[st][key] = pos[n];
+        }
+        cp_async_arrive(smem_u32(&ctl.kfull[st]));
+        if (u == 0) mbar_arrive(smem_u32(&ctl.kfull[st]));
+        if (i + 1 < s.hi) locate(i + 1);
+      }
+      ++seg;
+    });
+    cp_async_wait_all();  // this thread's copies land before it exits
+  } else if (warp == kMmaWarp) {
+    // ================================================================ MMA issuer
+    uint32_t g = 0, seg = 0;
+    bool ok = true;
+    for_segments<TK>(p, ctl.plan, member, [&](const Segment& s) {
+      if (!ok) return;
+      if (lane == 0) {
+        const uint32_t qk_desc = idesc_f16(64, TK, DTYPE == FP4IDX_BF16, false);
+        const uint32_t pv_desc = idesc_f16(128, (s.rows + 15) & ~15, DTYPE == FP4IDX_BF16, true);
+        const uint32_t n = s.hi - s.lo;
+        uint32_t qk = 0, pv = 0, spins = 0;
+        uint64_t t0 = 0;
+        ok = mbar_wait(smem_u32(&ctl.qfull), seg & 1, abort_flag, p.err);
+        while (ok && pv < n) {
+          bool moved = false;
+          if (qk < n && qk - pv < 2) {
+            const uint32_t x = g + qk, st = x % C::kStages, buf = x & 1;
+            if (mbar_test_wait(smem_u32(&ctl.kfull[st]), (x / C::kStages) & 1) &&
+                mbar_test_wait(smem_u32(&ctl.sempty[buf]), ((x >> 1) & 1) ^ 1)) {
+              tc_fence_after();
+              fence_proxy_async_smem();  // the copies were written by cp.async (generic proxy)
+              const uint32_t kb = base + st * C::kStage;
+#pragma unroll
+              for (int c = 0; c < C::kKc; ++c)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  tc_mma_f16(tmem + s_col + buf * TK, desc_sw128(base + C::kOff_Q + c * (kChunkRows * 128) + k * 32, 16),
+                             desc_sw128(kb + c * C::kPiece + k * 32, 16), qk_desc, (c | k) != 0);
+              tc_commit(smem_u32(&ctl.sfull[buf]));
+              if (++qk == n) tc_commit(smem_u32(&ctl.qempty));
+              moved = true;
+            }
+          }
+          if (!moved && pv < qk) {
+            const uint32_t x = g + pv, st = x % C::kStages;
+            if (mbar_test_wait(smem_u32(&ctl.pfull), x & 1) &&
+                (pv > 0 || mbar_test_wait(smem_u32(&ctl.oempty), (seg & 1) ^ 1))) {
+              tc_fence_after();
+              const uint32_t vb = base + st * C::kStage + C::kV;
+#pragma unroll
+              for (int d = 0; d < C::kDv / 128; ++d)
+#pragma unroll
+                for (int k = 0; k < TK / 16; ++k)
+                  tc_mma_f16(tmem + d * kChunkRows, desc_sw128(vb + d * 2 * C::kPiece + k * 2048, C::kPiece),
+                             desc_sw128(base + C::kOff_P + (k >> 2) * (kChunkRows * 128) + (k & 3) * 32, 16), pv_desc,
+                             pv > 0 || k > 0);
+              tc_commit(smem_u32(&ctl.kempty[st]));
+              tc_commit(smem_u32(&ctl.pvdone));
+              ++pv;
+              moved = true;
+            }
+          }
+          if (moved) {
+            spins = 0;
+          } else if ((++spins & 1023u) == 0) {  // every wait ends
+            if (spins == 1024u) t0 = globaltimer();
+            if (*abort_flag) ok = false;
+            if (globaltimer() - t0 > kWaitLimitNs) {
+              atomicOr(p.err, kErrTimeout);
+              *abort_flag = 1;
+              ok = false;
+            }
+          }
+        }
+        g += n;
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      ++seg;
+    });
+    if (lane == 0) {  // no product is in flight when TMEM is freed
+      int never = 0;
+      tc_commit(smem_u32(&ctl.drain));
+      mbar_wait(smem_u32(&ctl.drain), 0, &never, p.err);
+    }
+    __syncwarp();
+  } else {
+    // ================================================================ softmax
+    // After a failed wait the loop runs on without waiting, so that the
+    // named barriers below still meet; nothing is written then.
+    uint32_t g = 0;
+    bool ok = true;
+    const int r0 = 16 * warp + (lane >> 2);                 // this thread's rows: r0 and r0 + 8
+    const uint32_t quarter = static_cast<uint32_t>(warp) << 21;  // TMEM lanes 32 * warp
+    for_segments<TK>(p, ctl.plan, member, [&](const Segment& s) {
+      int vis[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = r0 + 8 * i;
+        vis[i] = r < s.rows ? attn_visible(p, s.it.b, s.it.q0 + (s.c + r) / p.group) : 0;
+      }
+      const bool active = 16 * warp < s.rows;
+      const int cols = (s.rows + 15) & ~15;                  // O^T columns in use
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+      for (int i = s.lo; i < s.hi; ++i, ++g) {
+        const uint32_t buf = g & 1, st = g % C::kStages;
+        float x[TK / 2];
+        bool raise = false;
+        float f[2] = {1.0f, 1.0f};
+        if (active) {
+          if (ok) ok = warp_wait(smem_u32(&ctl.sfull[buf]), (g >> 1) & 1, abort_flag, p.err);
+          if (ok) ok = warp_wait(smem_u32(&ctl.kfull[st]), (g / C::kStages) & 1, abort_flag, p.err);
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < TK / 64; ++c) {
+            uint32_t r[32];
+            tmem_ld_16x256b_x8(tmem + quarter + s_col + buf * TK + c * 64, r);
+            tmem_wait_ld();
+            reg_fence(r);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[c * 32 + e] = __uint_as_float(r[e]) * p.scale_log2;
+          }
+          tc_fence_before();
+          float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int j = 0; j < TK / 8; ++j) {
+            const int2 kp = *reinterpret_cast<const int2*>(&ctl.key_pos[st][8 * j + 2 * (lane & 3)]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              // -1 (no key) is the largest unsigned value
+              const bool seen = static_cast<uint32_t>(e & 1 ? kp.y : kp.x) < static_cast<uint32_t>(vis[e >> 1]);
+              x[4 * j + e] = seen ? x[4 * j + e] : -INFINITY;
+              top[e >> 1] = fmaxf(top[e >> 1], x[4 * j + e]);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
+            top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+            if (top[e] > m[e] + kRaise) {
+              f[e] = ex2(m[e] - top[e]);
+              m[e] = top[e];
+              raise = true;
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl.sempty[buf]));
+        const bool any = bar_red_or(1, 32 * kSoftmaxWarps, raise);
+        // the previous product has read P and updated O^T
+        if (ok && g > 0) ok = warp_wait(smem_u32(&ctl.pvdone), (g - 1) & 1, abort_flag, p.err);
+        if (any && i > s.lo) {
+          if ((lane & 3) == 0) {
+            ctl.factor[r0] = f[0];
+            ctl.factor[r0 + 8] = f[1];
+          }
+          bar_sync(2, 32 * kSoftmaxWarps);
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < C::kDv / 128 * cols; c += 16) {
+            const int d = c / cols, col = c - d * cols;
+            const uint32_t at = tmem + quarter + d * kChunkRows + col;
+            uint32_t r[16];
+            tmem_ld(at, r);
+            tmem_wait_ld();
+            reg_fence(r);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * ctl.factor[col + e]);
+            tmem_st_x16(at, r);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        if (active) {
+          // weights, their sum in fp32, and P in 16 bits (the MMA's operand
+          // type: each weight is rounded once, the sum is of unrounded ones)
+          const float ref[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
+          l[0] *= f[0];
+          l[1] *= f[1];
+          uint8_t* prow = smem + C::kOff_P + r0 * 128 + (lane & 3) * 4;
+#pragma unroll
+          for (int j = 0; j < TK / 8; ++j) {
+            const float a = ex2(x[4 * j] - ref[0]), b = ex2(x[4 * j + 1] - ref[0]);
+            const float c = ex2(x[4 * j + 2] - ref[1]), d = ex2(x[4 * j + 3] - ref[1]);
+            l[0] += a + b;
+            l[1] += c + d;
+            uint8_t* at = prow + (j >> 3) * (kChunkRows * 128) + (((j & 7) ^ (r0 & 7)) << 4);
+            *reinterpret_cast<uint32_t*>(at) = pack2<DTYPE>(a, b);
+            *reinterpret_cast<uint32_t*>(at + 8 * 128) = pack2<DTYPE>(c, d);
+          }
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl.pfull));
+      }
+      // ---- output of the segment
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+      }
+      const bool whole = s.lo == 0 && s.hi == s.tiles;
+      const int64_t slot = (static_cast<int64_t>(group) * 2 + (s.lo == 0)) * p.members + member;
+      if ((lane & 3) == 0) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = r0 + 8 * e;
+          const int t = s.it.q0 + (s.c + r) / p.group, h = s.it.hk * p.group + (s.c + r) % p.group;
+          ctl.row_l[r] = l[e];
+          ctl.row_off[r] = t * p.out_row_stride + static_cast<int64_t>(h) * C::kDv;
+          if (r < s.rows && ok) {
+            if (!whole)
+              p.stats[slot * kChunkRows + r] = make_float2(m[e], l[e]);
+            else if (p.lse)
+              p.lse[static_cast<int64_t>(t) * p.num_heads + h] = row_lse(m[e], l[e]);
+          }
+        }
+      }
+      if (ok) ok = warp_wait(smem_u32(&ctl.pvdone), (g - 1) & 1, abort_flag, p.err);
+      bar_sync(2, 32 * kSoftmaxWarps);
+      tc_fence_after();
+#pragma unroll 1
+      for (int d = 0; d < C::kDv / 128; ++d) {
+        const int dv = d * 128 + tid;  // this thread's value dimension (tid < 128)
+#pragma unroll 1
+        for (int c = 0; c < cols; c += 16) {
+          uint32_t r[16];
+          tmem_ld(tmem + quarter + d * kChunkRows + c, r);
+          tmem_wait_ld();
+          reg_fence(r);
+          if (!ok) continue;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            if (c + e >= s.rows) break;
+            const float o = __uint_as_float(r[e]);
+            if (whole) {
+              const float sum = ctl.row_l[c + e];
+              p.out[ctl.row_off[c + e] + dv] = from_float<DTYPE>(sum == 0.0f ? 0.0f : o / sum);
+            } else {
+              p.partial[(slot * kChunkRows + c + e) * C::kDv + dv] = o;
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      bar_sync(2, 32 * kSoftmaxWarps);  // row_l and row_off are read before the next segment writes them
+      if (lane == 0) mbar_arrive(smem_u32(&ctl.oempty));
+    });
+    tc_fence_before();
+  }
   __syncthreads();
-  float r = red[0];
-  for (int i = 1; i < kThreads / 32; ++i) r = is_max ? fmaxf(r, red[i]) : r + red[i];
-  return r;
+  pdl_launch_dependents();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc<kTmemCols>(tmem);
+  }
+}
+
+// ---------------------------------------------------------------- join
+// out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over the partial sums of
+// an item that crosses run boundaries, in the order of its keys.  A CTA
+// takes kJoinRows rows of one (boundary, member); the boundary that is the
+// first inside its item does the work.  With few partials a warp takes a
+// row, with many the eight warps share a row's partials.
+constexpr int kJoinThreads = 256, kJoinRows = 8;
+
+template <int DTYPE, bool LATENT>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnParams p) {
+  using C = Cfg<LATENT>;
+  constexpr int kVec = C::kDv / 128;  // float4s per lane
+  __shared__ float sum[kJoinThreads / 32][C::kDv];
+  __shared__ float2 ml[kJoinThreads / 32];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int group = blockIdx.x + 1, member = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t total = p.info[3];
+  const int used = used_groups(p, total);
+  if (group >= used) return;
+  const int64_t* info = p.info + 4 * group;
+  const int64_t start = info[1], end = start + info[2];
+  if (start >= run_start(total, group, used) || run_start(total, group - 1, used) > start) return;
+  const Item it = item_of(p, static_cast<int>(info[0]));
+  const int c = it.c0 + member * kChunkRows;
+  const int rows = min(kChunkRows, it.rows - c);
+  const int row_lo = blockIdx.z * kJoinRows;
+  if (row_lo >= rows) return;
+  const int row_hi = min(rows, row_lo + kJoinRows);
+  int parts = 1;
+  while (group + parts - 1 < used && run_start(total, group + parts - 1, used) < end) ++parts;
+  // part i: group - 1 + i; the first one is its group's last segment, the others their groups' first
+  auto slot_row = [&](int i, int r) {
+    return ((static_cast<int64_t>(group - 1 + i) * 2 + (i == 0)) * p.members + member) * kChunkRows + r;
+  };
+  const bool share = parts > 4;
+  for (int r = share ? row_lo : row_lo + warp; r < row_hi; r += share ? 1 : kJoinThreads / 32) {
+    const int i0 = share ? warp : 0, step = share ? kJoinThreads / 32 : 1;
+    float M = -INFINITY;
+    for (int i = lane; i < parts; i += 32) M = fmaxf(M, p.stats[slot_row(i, r)].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float ref = M == -INFINITY ? 0.0f : M;
+    float4 acc[kVec] = {};
+    float l = 0.0f;
+#pragma unroll 4
+    for (int i = i0; i < parts; i += step) {
+      const int64_t row = slot_row(i, r);
+      const float2 s = p.stats[row];
+      const float w = ex2(s.x - ref);
+      l = fmaf(w, s.y, l);
+#pragma unroll
+      for (int v = 0; v < kVec; ++v) {
+        const float4 o = reinterpret_cast<const float4*>(p.partial + row * C::kDv)[v * 32 + lane];
+        acc[v].x = fmaf(w, o.x, acc[v].x);
+        acc[v].y = fmaf(w, o.y, acc[v].y);
+        acc[v].z = fmaf(w, o.z, acc[v].z);
+        acc[v].w = fmaf(w, o.w, acc[v].w);
+      }
+    }
+    if (share) {
+#pragma unroll
+      for (int v = 0; v < kVec; ++v) reinterpret_cast<float4*>(sum[warp])[v * 32 + lane] = acc[v];
+      if (lane == 0) ml[warp] = make_float2(M, l);
+      __syncthreads();
+      if (warp == 0) {
+        for (int w = 1; w < kJoinThreads / 32; ++w) {
+          l += ml[w].y;
+#pragma unroll
+          for (int v = 0; v < kVec; ++v) {
+            const float4 o = reinterpret_cast<const float4*>(sum[w])[v * 32 + lane];
+            acc[v].x += o.x;
+            acc[v].y += o.y;
+            acc[v].z += o.z;
+            acc[v].w += o.w;
+          }
+        }
+      }
+    }
+    if (!share || warp == 0) {
+      const int t = it.q0 + (c + r) / p.group, h = it.hk * p.group + (c + r) % p.group;
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      uint2* out = reinterpret_cast<uint2*>(p.out + t * p.out_row_stride + static_cast<int64_t>(h) * C::kDv);
+#pragma unroll
+      for (int v = 0; v < kVec; ++v)
+        out[v * 32 + lane] = make_uint2(pack2<DTYPE>(acc[v].x * inv, acc[v].y * inv), pack2<DTYPE>(acc[v].z * inv, acc[v].w * inv));
+      if (p.lse && lane == 0) p.lse[static_cast<int64_t>(t) * p.num_heads + h] = row_lse(M, l);
+    }
+    if (share) __syncthreads();
+  }
 }
 
 template <int DTYPE, bool LATENT>
-__global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p) {
-  constexpr int DK = LATENT ? kLatentDim + kRopeDim : kPagedDim;
-  constexpr int DV = LATENT ? kLatentDim : kPagedDim;
-  __shared__ float q[DK];
-  __shared__ float weight[kThreads];
-  __shared__ int64_t row_at[kThreads];
-  __shared__ float red[kThreads / 32];
-  const int t = blockIdx.x, h = blockIdx.y, hk = h / p.group, tid = threadIdx.x;
-  const int b = attn_request(p, t);
-  const int vis = attn_visible(p, b, t);
-  const int64_t base = attn_table_base(p, b);
-  for (int d = tid; d < DK; d += kThreads)
-    q[d] = to_float<DTYPE>(p.q[t * p.q_row_stride + h * p.q_head_stride + d]);
-  __syncthreads();
-  int64_t n = vis;
-  const int32_t* list = nullptr;
-  if (p.indices) {
-    n = static_cast<int64_t>(p.num_indices) * (LATENT ? 1 : kSelectBlock);
-    list = p.indices + (LATENT ? static_cast<int64_t>(t) : static_cast<int64_t>(hk) * p.num_rows + t) * p.num_indices;
-  }
-  float m = -INFINITY, l = 0.0f, acc[DV / kThreads] = {};
-  for (int64_t j0 = 0; j0 < n; j0 += kThreads) {
-    const int64_t j = j0 + tid;
-    int64_t pos = -1;
-    if (j < n) pos = !list ? j : LATENT ? __ldg(list + j) : static_cast<int64_t>(__ldg(list + j / kSelectBlock)) * kSelectBlock + j % kSelectBlock;
-    int64_t at = -1;
-    if (pos >= 0 && pos < vis) {
-      const int64_t page = __ldg(p.block_table + base + (pos >> p.page_shift));
-      if (page >= 0 && page < p.num_pages)
-        at = page * p.page_stride +
-             (static_cast<int64_t>(LATENT ? 0 : hk) * p.page_size + (pos & (p.page_size - 1))) * DK;
-      else
-        atomicOr(p.err, kErrPageRange);
-    }
-    float s = -INFINITY;
-    if (at >= 0) {
-      s = 0.0f;
-      for (int d = 0; d < DK; ++d) s = fmaf(q[d], to_float<DTYPE>(p.k[at + d]), s);
-      s *= p.scale_log2;
-    }
-    const float top = fmaxf(m, block_reduce(s, true, red));
-    const float ref = top == -INFINITY ? 0.0f : top;
-    const float w = exp2f(s - ref), keep = exp2f(m - ref);
-    l = l * keep + block_reduce(w, false, red);
-    m = top;
-    weight[tid] = w;
-    row_at[tid] = at;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < DV / kThreads; ++i) acc[i] *= keep;
-    for (int u = 0; u < kThreads; ++u) {
-      if (row_at[u] < 0) continue;
-      const uint16_t* row = (LATENT ? p.k : p.v) + row_at[u];
-#pragma unroll
-      for (int i = 0; i < DV / kThreads; ++i) acc[i] = fmaf(weight[u], to_float<DTYPE>(row[i * kThreads + tid]), acc[i]);
-    }
-    __syncthreads();
-  }
-  const float inv = l > 0.0f ? 1.0f / l : l;  // no keys: 0; NaN stays
-  for (int i = 0; i < DV / kThreads; ++i)
-    p.out[t * p.out_row_stride + static_cast<int64_t>(h) * DV + i * kThreads + tid] = from_float<DTYPE>(l == 0.0f ? 0.0f : acc[i] * inv);
-  if (p.lse && tid == 0)
-    p.lse[static_cast<int64_t>(t) * p.num_heads + h] = (m + log2f(l)) * 0.693147180559945309f;
+cudaError_t launch(const AttnParams& p, cudaStream_t stream) {
+  cudaError_t e = cudaFuncSetAttribute(attention_kernel<DTYPE, LATENT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       smem_bytes<LATENT>());
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(static_cast<unsigned>(p.groups * p.members));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_bytes<LATENT>();
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, attention_kernel<DTYPE, LATENT>, p)) != cudaSuccess) return e;
+  if (p.groups < 2) return cudaSuccess;
+  cfg.gridDim = dim3(static_cast<unsigned>(p.groups - 1), static_cast<unsigned>(p.members), kChunkRows / kJoinRows);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, join_kernel<DTYPE, LATENT>, p);
 }
+
+int64_t round16(int64_t n) { return (n + 15) & ~int64_t{15}; }
 
 }  // namespace
 
-cudaError_t launch_attention(const AttnParams& p, int dtype, cudaStream_t stream) {
-  const dim3 grid(p.num_rows, p.num_heads);
+bool plan_attention(AttnParams* p, int sms) {
+  const bool latent = p->v == nullptr;
+  const int64_t pairs = (p->indices ? 1 : static_cast<int64_t>(p->max_seqlen_q)) * p->group;
+  const int64_t chunks = (pairs + kChunkRows - 1) / kChunkRows;
+  p->members = static_cast<int32_t>(chunks < kMaxMembers ? chunks : kMaxMembers);
+  const int64_t cg = (chunks + p->members - 1) / p->members;
+  const int64_t items = static_cast<int64_t>(p->indices ? p->num_rows : p->num_seqs) * p->num_kv_heads * cg;
+  if (items > INT32_MAX) return false;
+  p->chunk_groups = static_cast<int32_t>(cg);
+  p->items = static_cast<int32_t>(items);
+  const int tk = latent ? Cfg<true>::kTk : Cfg<false>::kTk;
+  p->list_tiles = p->indices ? static_cast<int32_t>((static_cast<int64_t>(p->num_indices) * (latent ? 1 : kSelectBlock) + tk - 1) / tk) : 0;
+  // no more groups than tiles can exist
+  const int64_t per_item = p->indices ? p->list_tiles : (static_cast<int64_t>(p->max_seqlen_k) + tk - 1) / tk;
+  const int64_t most = items * (per_item < 1 ? 1 : per_item);
+  const int64_t groups = sms / p->members;
+  p->groups = static_cast<int32_t>(most < groups ? most : groups);
+  return true;
+}
+
+size_t attention_workspace(const AttnParams& p) {
+  const int64_t rows = static_cast<int64_t>(p.groups) * 2 * p.members * kChunkRows;
+  const int64_t dv = p.v == nullptr ? kLatentDim : kPagedDim;
+  return static_cast<size_t>(round16(p.groups * 4 * 8) + round16(rows * 8) + rows * dv * 4);
+}
+
+cudaError_t launch_attention(AttnParams p, int dtype, void* workspace, cudaStream_t stream) {
+  const int64_t rows = static_cast<int64_t>(p.groups) * 2 * p.members * kChunkRows;
+  char* w = static_cast<char*>(workspace);
+  p.info = reinterpret_cast<int64_t*>(w);
+  w += round16(p.groups * 4 * 8);
+  p.stats = reinterpret_cast<float2*>(w);
+  w += round16(rows * 8);
+  p.partial = reinterpret_cast<float*>(w);
   const bool latent = p.v == nullptr;
   if (dtype == FP4IDX_BF16)
-    latent ? attention_kernel<FP4IDX_BF16, true><<<grid, kThreads, 0, stream>>>(p)
-           : attention_kernel<FP4IDX_BF16, false><<<grid, kThreads, 0, stream>>>(p);
-  else
-    latent ? attention_kernel<FP4IDX_FP16, true><<<grid, kThreads, 0, stream>>>(p)
-           : attention_kernel<FP4IDX_FP16, false><<<grid, kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+    return latent ? launch<FP4IDX_BF16, true>(p, stream) : launch<FP4IDX_BF16, false>(p, stream);
+  return latent ? launch<FP4IDX_FP16, true>(p, stream) : launch<FP4IDX_FP16, false>(p, stream);
 }
 
 }  // namespace fp4idx

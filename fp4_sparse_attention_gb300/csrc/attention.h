@@ -42,7 +42,19 @@ struct AttnParams {
   int64_t out_row_stride;
   float* lse;
   uint32_t* err;
+  // work split (plan_attention)
+  int32_t members;      // CTAs of a group: they share an item's keys and split its query rows
+  int32_t chunk_groups; // row-chunk groups of one (request, K/V head)
+  int32_t groups;       // CTA groups of the grid
+  int32_t items;        // (request or row) x K/V head x chunk group
+  int32_t list_tiles;   // key tiles of an item with a selection (0: whole prefix)
+  // workspace
+  int64_t* info;        // [groups][4]: first item, its first tile, its tiles, all tiles
+  float2* stats;        // [groups][2][members][64]: reference maximum and sum of a partial row
+  float* partial;       // [groups][2][members][64][dv]: its unnormalised output
 };
+
+constexpr int kChunkRows = 64;  // query rows ((row, head) pairs) of one CTA
 
 // Rows copied into a paged cache by slot: up to two sources, each a run of
 // `units` 16-byte pieces per (token, head).
@@ -85,7 +97,10 @@ struct TablesParams {
 // SM count and error word of the current device (api.cu).
 fp4idx_status_t call_device(int* sms, uint32_t** err);
 
-cudaError_t launch_attention(const AttnParams& p, int dtype, cudaStream_t stream);
+// Fills the work split of p; false if it does not fit the counters.
+bool plan_attention(AttnParams* p, int sms);
+size_t attention_workspace(const AttnParams& p);
+cudaError_t launch_attention(AttnParams p, int dtype, void* workspace, cudaStream_t stream);
 cudaError_t launch_store_rows(const StoreRowsParams& p, cudaStream_t stream);
 cudaError_t launch_tables(TablesParams p, int sms, cudaStream_t stream);
 

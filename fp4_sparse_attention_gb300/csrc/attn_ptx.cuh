@@ -1,0 +1,93 @@
+// attn_ptx.cuh -- inline-PTX building blocks of the attention kernels beyond
+// ptx.cuh: 16-bit tcgen05 MMAs, their descriptors, TMEM loads in the
+// row-fragment shape and TMEM stores, zero-filling asynchronous copies.
+#pragma once
+
+#include "ptx.cuh"
+
+namespace fp4idx {
+
+// D[tmem] (+)= A[smem] * B[smem]^T, 16-bit operands, fp32 accumulator.
+__device__ __forceinline__ void tc_mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor of kind::f16 with an fp32 accumulator; both operands
+// fp16 (bf16 false) or both bf16.  a_mn: A is stored with M contiguous.
+__host__ __device__ constexpr uint32_t idesc_f16(int m, int n, bool bf16, bool a_mn) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (a_mn ? 1u << 15 : 0u) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// Operand in 128-byte rows, 128-byte swizzle (1,024-byte atoms of 8 rows).
+//   K-major: a row holds 64 consecutive k of one m/n; 8-row groups every
+//   1,024 B; a 16-wide k step inside the row advances the address by 32 B.
+//   MN-major: a row holds 64 consecutive m of one k; groups of 8 k every
+//   1,024 B, the next 64 m every `mn_stride` bytes.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t mn_stride) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(mn_stride >> 4) << 16;  // leading byte offset (unused when K-major)
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;       // stride byte offset
+  d |= static_cast<uint64_t>(1) << 46;               // descriptor version (tcgen05)
+  d |= static_cast<uint64_t>(2) << 61;               // 128-byte swizzle
+  return d;
+}
+
+// 16 lanes x 64 columns as the four warps' row fragments: thread i receives
+// columns 8j + 2(i%4) + {0,1} of lane i/4 in r[4j], r[4j+1] and of lane i/4 + 8
+// in r[4j+2], r[4j+3].
+#define FP4IDX_R8(i) "=r"(r[i + 0]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), \
+                     "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
+__device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : FP4IDX_R8(0), FP4IDX_R8(8), FP4IDX_R8(16), FP4IDX_R8(24)
+      : "r"(taddr));
+}
+#undef FP4IDX_R8
+
+// 32 lanes x 16 columns: thread i of the warp writes its lane's columns.
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 16-byte asynchronous copy, or 16 zero bytes (src is not read).
+__device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void* src, bool copy) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(copy ? 16 : 0) : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Named barrier of `count` threads that also ORs a predicate over them.
+__device__ __forceinline__ bool bar_red_or(uint32_t id, uint32_t count, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %3, 0;\n barrier.cta.red.or.pred q, %1, %2, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(id), "r"(count), "r"(static_cast<uint32_t>(v))
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void bar_sync(uint32_t id, uint32_t count) {
+  asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
+}  // namespace fp4idx

@@ -267,6 +267,24 @@ def test_another_stream_and_graph_replay(kv):
     check(c, (a.out, a.lse))
 
 
+@pytest.mark.parametrize("kv", [None, 4])
+def test_workspace_too_small_is_refused(kv):
+    c = R.make_case(23, [1], [9000], heads=16, kv_heads=kv, device="cuda")
+    a = build(c)
+    need = a.workspace.numel()
+    a.out.fill_(5)
+    a._ws = (a._ws[0], need - 1)
+    with pytest.raises(B.Fp4idxError) as e:
+        call(a)
+    assert e.value.status == 3
+    a._ws = (None, need)
+    with pytest.raises(B.Fp4idxError) as e:
+        call(a)
+    assert e.value.status == 3
+    torch.cuda.synchronize()
+    assert bool((a.out == 5).all())
+
+
 def test_lse_is_optional():
     c = R.make_case(24, [2], [300], heads=16, device="cuda")
     a = build(c)
