@@ -36,9 +36,6 @@
 // for different row chunks, close enough in time for the L2 to serve the
 // second reader.  An item cut by a boundary leaves partial sums that
 // join_kernel adds in a fixed order.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include <cstring>
 
 #include "attention.h"
@@ -52,6 +49,7 @@ constexpr int kThreads = 32 * (kSoftmaxWarps + 1 + kLoadWarps);
 constexpr int kLoadThreads = 32 * kLoadWarps;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxMembers = 8;
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 // A row's reference maximum is raised only when the true one is 2^8 above it.
 constexpr float kRaise = 8.0f;
 
@@ -81,7 +79,7 @@ struct Control {
   int64_t row_off[kChunkRows];                                 // output element of each row
   int64_t plan[4];                                             // first item, its first tile, lo, hi
   int32_t key_pos[Cfg<LATENT>::kStages][Cfg<LATENT>::kTk];     // logical position, -1: no key
-  float factor[kChunkRows], row_m[kChunkRows], row_l[kChunkRows];
+  float factor[kChunkRows], row_inv[kChunkRows];
   uint32_t tmem;
   int abort;
 };
@@ -192,12 +190,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-template <int DTYPE>
-__device__ __forceinline__ uint16_t from_float(float x) {
-  if constexpr (DTYPE == FP4IDX_BF16) return __bfloat16_as_ushort(__float2bfloat16_rn(x));
-  return __half_as_ushort(__float2half_rn(x));
-}
-
 // ln(sum) of a row with reference maximum m (in powers of two) and sum l.
 __device__ __forceinline__ float row_lse(float m, float l) {
   return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
@@ -401,76 +393,80 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     cp_async_wait_all();  // this thread's copies land before it exits
   } else if (warp == kMmaWarp) {
     // ================================================================ MMA issuer
+    // The whole warp runs this loop; one elected lane issues.
     uint32_t g = 0, seg = 0;
     bool ok = true;
+    const uint32_t tm = uniform(tmem);
+    const uint32_t qk_idesc = idesc_f16(64, TK, DTYPE == FP4IDX_BF16, false);
+    const uint64_t q_desc = desc_sw128(base + C::kOff_Q, 16), p_desc = desc_sw128(base + C::kOff_P, 16);
+    auto ready = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_test_wait(smem_u32(bar), parity));
+    };
     for_segments<TK>(p, ctl.plan, member, [&](const Segment& s) {
       if (!ok) return;
-      if (lane == 0) {
-        const uint32_t qk_desc = idesc_f16(64, TK, DTYPE == FP4IDX_BF16, false);
-        const uint32_t pv_desc = idesc_f16(128, (s.rows + 15) & ~15, DTYPE == FP4IDX_BF16, true);
-        const uint32_t n = s.hi - s.lo;
-        uint32_t qk = 0, pv = 0, spins = 0;
-        uint64_t t0 = 0;
-        ok = mbar_wait(smem_u32(&ctl.qfull), seg & 1, abort_flag, p.err);
-        while (ok && pv < n) {
-          bool moved = false;
-          if (qk < n && qk - pv < 2) {
-            const uint32_t x = g + qk, st = x % C::kStages, buf = x & 1;
-            if (mbar_test_wait(smem_u32(&ctl.kfull[st]), (x / C::kStages) & 1) &&
-                mbar_test_wait(smem_u32(&ctl.sempty[buf]), ((x >> 1) & 1) ^ 1)) {
-              tc_fence_after();
-              fence_proxy_async_smem();  // the copies were written by cp.async (generic proxy)
-              const uint32_t kb = base + st * C::kStage;
+      const uint32_t pv_idesc = uniform(idesc_f16(128, (s.rows + 15) & ~15, DTYPE == FP4IDX_BF16, true));
+      const uint32_t n = uniform(s.hi - s.lo);
+      uint32_t qk = 0, pv = 0, spins = 0;
+      uint64_t t0 = 0;
+      ok = warp_wait(smem_u32(&ctl.qfull), seg & 1, abort_flag, p.err);
+      while (ok && pv < n) {
+        bool moved = false;
+        if (qk < n && qk - pv < 2) {
+          const uint32_t x = g + qk, st = uniform(x % C::kStages), buf = x & 1;
+          if (ready(&ctl.kfull[st], (x / C::kStages) & 1) && ready(&ctl.sempty[buf], ((x >> 1) & 1) ^ 1)) {
+            tc_fence_after();
+            fence_proxy_async_smem();  // the copies were written by cp.async (generic proxy)
+            const uint64_t k_desc = desc_sw128(base + st * C::kStage, 16);
+            const uint32_t d = tm + s_col + buf * TK;
 #pragma unroll
-              for (int c = 0; c < C::kKc; ++c)
+            for (int c = 0; c < C::kKc; ++c)
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  tc_mma_f16(tmem + s_col + buf * TK, desc_sw128(base + C::kOff_Q + c * (kChunkRows * 128) + k * 32, 16),
-                             desc_sw128(kb + c * C::kPiece + k * 32, 16), qk_desc, (c | k) != 0);
-              tc_commit(smem_u32(&ctl.sfull[buf]));
-              if (++qk == n) tc_commit(smem_u32(&ctl.qempty));
-              moved = true;
-            }
-          }
-          if (!moved && pv < qk) {
-            const uint32_t x = g + pv, st = x % C::kStages;
-            if (mbar_test_wait(smem_u32(&ctl.pfull), x & 1) &&
-                (pv > 0 || mbar_test_wait(smem_u32(&ctl.oempty), (seg & 1) ^ 1))) {
-              tc_fence_after();
-              const uint32_t vb = base + st * C::kStage + C::kV;
-#pragma unroll
-              for (int d = 0; d < C::kDv / 128; ++d)
-#pragma unroll
-                for (int k = 0; k < TK / 16; ++k)
-                  tc_mma_f16(tmem + d * kChunkRows, desc_sw128(vb + d * 2 * C::kPiece + k * 2048, C::kPiece),
-                             desc_sw128(base + C::kOff_P + (k >> 2) * (kChunkRows * 128) + (k & 3) * 32, 16), pv_desc,
-                             pv > 0 || k > 0);
-              tc_commit(smem_u32(&ctl.kempty[st]));
-              tc_commit(smem_u32(&ctl.pvdone));
-              ++pv;
-              moved = true;
-            }
-          }
-          if (moved) {
-            spins = 0;
-          } else if ((++spins & 1023u) == 0) {  // every wait ends
-            if (spins == 1024u) t0 = globaltimer();
-            if (*abort_flag) ok = false;
-            if (globaltimer() - t0 > kWaitLimitNs) {
-              atomicOr(p.err, kErrTimeout);
-              *abort_flag = 1;
-              ok = false;
-            }
+              for (int k = 0; k < 4; ++k)  // descriptor addresses count 16 bytes
+                tc_mma_f16(d, q_desc + c * (kChunkRows * 8) + k * 2, k_desc + c * (C::kPiece >> 4) + k * 2, qk_idesc,
+                           (c | k) != 0);
+            tc_commit_elected(smem_u32(&ctl.sfull[buf]));
+            if (++qk == n) tc_commit_elected(smem_u32(&ctl.qempty));
+            moved = true;
           }
         }
-        g += n;
+        if (!moved && pv < qk) {
+          const uint32_t x = g + pv, st = uniform(x % C::kStages);
+          if (ready(&ctl.pfull, x & 1) && (pv > 0 || ready(&ctl.oempty, (seg & 1) ^ 1))) {
+            tc_fence_after();
+            const uint64_t v_desc = desc_sw128(base + st * C::kStage + C::kV, C::kPiece);
+            const uint32_t more = pv > 0;
+#pragma unroll
+            for (int d = 0; d < C::kDv / 128; ++d)
+#pragma unroll
+              for (int k = 0; k < TK / 16; ++k)
+                tc_mma_f16(tm + d * kChunkRows, v_desc + d * (2 * C::kPiece >> 4) + k * 128,
+                           p_desc + (k >> 2) * (kChunkRows * 8) + (k & 3) * 2, pv_idesc, k > 0 ? 1u : more);
+            tc_commit_elected(smem_u32(&ctl.kempty[st]));
+            tc_commit_elected(smem_u32(&ctl.pvdone));
+            ++pv;
+            moved = true;
+          }
+        }
+        if (moved) {
+          spins = 0;
+        } else if ((++spins & 1023u) == 0) {  // every wait ends
+          if (spins == 1024u) t0 = globaltimer();
+          bool stop = *abort_flag != 0;
+          if (globaltimer() - t0 > kWaitLimitNs) {
+            if (lane == 0) atomicOr(p.err, kErrTimeout);
+            *abort_flag = 1;
+            stop = true;
+          }
+          ok = !__any_sync(0xffffffffu, stop);
+        }
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
+      g += n;
       ++seg;
     });
-    if (lane == 0) {  // no product is in flight when TMEM is freed
+    // no product is in flight when TMEM is freed
+    tc_commit_elected(smem_u32(&ctl.drain));
+    if (lane == 0) {
       int never = 0;
-      tc_commit(smem_u32(&ctl.drain));
       mbar_wait(smem_u32(&ctl.drain), 0, &never, p.err);
     }
     __syncwarp();
@@ -537,8 +533,35 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ctl.sempty[buf]));
         const bool any = bar_red_or(1, 32 * kSoftmaxWarps, raise);
+        uint32_t w[TK / 4];
+        if (active) {
+          // weights, their sum in fp32, and P in 16 bits (the MMA's operand
+          // type: each weight is rounded once, the sum is of unrounded ones)
+          const float ref[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
+          l[0] *= f[0];
+          l[1] *= f[1];
+#pragma unroll
+          for (int j = 0; j < TK / 8; ++j) {
+            const float a = ex2(x[4 * j] - ref[0]), b = ex2(x[4 * j + 1] - ref[0]);
+            const float c = ex2(x[4 * j + 2] - ref[1]), d = ex2(x[4 * j + 3] - ref[1]);
+            l[0] += a + b;
+            l[1] += c + d;
+            w[2 * j] = pack2<DTYPE>(a, b);
+            w[2 * j + 1] = pack2<DTYPE>(c, d);
+          }
+        }
         // the previous product has read P and updated O^T
         if (ok && g > 0) ok = warp_wait(smem_u32(&ctl.pvdone), (g - 1) & 1, abort_flag, p.err);
+        if (active) {
+          uint8_t* prow = smem + C::kOff_P + r0 * 128 + (lane & 3) * 4;
+#pragma unroll
+          for (int j = 0; j < TK / 8; ++j) {
+            uint8_t* at = prow + (j >> 3) * (kChunkRows * 128) + (((j & 7) ^ (r0 & 7)) << 4);
+            *reinterpret_cast<uint32_t*>(at) = w[2 * j];
+            *reinterpret_cast<uint32_t*>(at + 8 * 128) = w[2 * j + 1];
+          }
+          fence_proxy_async_smem();
+        }
         if (any && i > s.lo) {
           if ((lane & 3) == 0) {
             ctl.factor[r0] = f[0];
@@ -561,25 +584,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           tmem_wait_st();
           tc_fence_before();
         }
-        if (active) {
-          // weights, their sum in fp32, and P in 16 bits (the MMA's operand
-          // type: each weight is rounded once, the sum is of unrounded ones)
-          const float ref[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
-          l[0] *= f[0];
-          l[1] *= f[1];
-          uint8_t* prow = smem + C::kOff_P + r0 * 128 + (lane & 3) * 4;
-#pragma unroll
-          for (int j = 0; j < TK / 8; ++j) {
-            const float a = ex2(x[4 * j] - ref[0]), b = ex2(x[4 * j + 1] - ref[0]);
-            const float c = ex2(x[4 * j + 2] - ref[1]), d = ex2(x[4 * j + 3] - ref[1]);
-            l[0] += a + b;
-            l[1] += c + d;
-            uint8_t* at = prow + (j >> 3) * (kChunkRows * 128) + (((j & 7) ^ (r0 & 7)) << 4);
-            *reinterpret_cast<uint32_t*>(at) = pack2<DTYPE>(a, b);
-            *reinterpret_cast<uint32_t*>(at + 8 * 128) = pack2<DTYPE>(c, d);
-          }
-          fence_proxy_async_smem();
-        }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ctl.pfull));
       }
@@ -596,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         for (int e = 0; e < 2; ++e) {
           const int r = r0 + 8 * e;
           const int t = s.it.q0 + (s.c + r) / p.group, h = s.it.hk * p.group + (s.c + r) % p.group;
-          ctl.row_l[r] = l[e];
+          ctl.row_inv[r] = l[e] == 0.0f ? 0.0f : 1.0f / l[e];
           ctl.row_off[r] = t * p.out_row_stride + static_cast<int64_t>(h) * C::kDv;
           if (r < s.rows && ok) {
             if (!whole)
@@ -610,30 +614,34 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       bar_sync(2, 32 * kSoftmaxWarps);
       tc_fence_after();
 #pragma unroll 1
-      for (int d = 0; d < C::kDv / 128; ++d) {
+      for (int c = 0; c < C::kDv / 128 * cols; c += 16) {
+        const int d = c / cols, col = c - d * cols;
         const int dv = d * 128 + tid;  // this thread's value dimension (tid < 128)
-#pragma unroll 1
-        for (int c = 0; c < cols; c += 16) {
-          uint32_t r[16];
-          tmem_ld(tmem + quarter + d * kChunkRows + c, r);
-          tmem_wait_ld();
-          reg_fence(r);
-          if (!ok) continue;
+        uint32_t r[16];
+        tmem_ld(tmem + quarter + d * kChunkRows + col, r);
+        tmem_wait_ld();
+        reg_fence(r);
+        if (!ok) continue;
+        if (whole) {
+          // neighbouring lanes swap rows so that each stores two values of one row
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            if (c + e >= s.rows) break;
-            const float o = __uint_as_float(r[e]);
-            if (whole) {
-              const float sum = ctl.row_l[c + e];
-              p.out[ctl.row_off[c + e] + dv] = from_float<DTYPE>(sum == 0.0f ? 0.0f : o / sum);
-            } else {
-              p.partial[(slot * kChunkRows + c + e) * C::kDv + dv] = o;
-            }
+          for (int e = 0; e < 16; e += 2) {
+            const int row = col + e + (lane & 1);
+            const float a = __uint_as_float(r[e]) * ctl.row_inv[col + e];
+            const float b = __uint_as_float(r[e + 1]) * ctl.row_inv[col + e + 1];
+            const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : b, 1);
+            const uint32_t v = lane & 1 ? pack2<DTYPE>(other, b) : pack2<DTYPE>(a, other);
+            if (row < s.rows) *reinterpret_cast<uint32_t*>(p.out + ctl.row_off[row] + (dv & ~1)) = v;
           }
+        } else {
+          float* o = p.partial + (slot * kChunkRows + col) * C::kDv + dv;
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (col + e < s.rows) o[e * C::kDv] = __uint_as_float(r[e]);
         }
       }
       tc_fence_before();
-      bar_sync(2, 32 * kSoftmaxWarps);  // row_l and row_off are read before the next segment writes them
+      bar_sync(2, 32 * kSoftmaxWarps);  // row_inv and row_off are read before the next segment writes them
       if (lane == 0) mbar_arrive(smem_u32(&ctl.oempty));
     });
     tc_fence_before();
@@ -648,52 +656,53 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 
 // ---------------------------------------------------------------- join
 // out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over the partial sums of
-// an item that crosses run boundaries, in the order of its keys.  A CTA
-// takes kJoinRows rows of one (boundary, member); the boundary that is the
-// first inside its item does the work.  With few partials a warp takes a
-// row, with many the eight warps share a row's partials.
-constexpr int kJoinThreads = 256, kJoinRows = 8;
+// an item that crosses run boundaries, in the order of its keys.  The eight
+// warps of a CTA take a row each when an item has few partials (BY_ITEM
+// false: blockIdx.x counts run boundaries, the first boundary inside an item
+// does its work), and share one row's partials when there are fewer items
+// than groups, so that many partials meet (BY_ITEM: blockIdx.x is the item).
 
-template <int DTYPE, bool LATENT>
+template <int DTYPE, bool LATENT, bool BY_ITEM>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnParams p) {
   using C = Cfg<LATENT>;
   constexpr int kVec = C::kDv / 128;  // float4s per lane
-  __shared__ float sum[kJoinThreads / 32][C::kDv];
-  __shared__ float2 ml[kJoinThreads / 32];
+  __shared__ float4 sum[BY_ITEM ? kJoinWarps : 1][C::kDv / 4];
+  __shared__ float part_l[kJoinWarps];
+  __shared__ int first_group;
   pdl_wait();
   pdl_launch_dependents();
-  const int group = blockIdx.x + 1, member = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tid = threadIdx.x, member = blockIdx.y, warp = tid >> 5, lane = tid & 31;
   const int64_t total = p.info[3];
   const int used = used_groups(p, total);
-  if (group >= used) return;
-  const int64_t* info = p.info + 4 * group;
-  const int64_t start = info[1], end = start + info[2];
-  if (start >= run_start(total, group, used) || run_start(total, group - 1, used) > start) return;
-  const Item it = item_of(p, static_cast<int>(info[0]));
+  // the groups whose run begins inside the item: consecutive ones
+  const int item = BY_ITEM ? blockIdx.x : static_cast<int>(blockIdx.x) + 1 < used ? static_cast<int>(p.info[4 * (blockIdx.x + 1)]) : -1;
+  const bool inside = tid > 0 && tid < used && p.info[4 * tid] == item && p.info[4 * tid + 1] < run_start(total, tid, used);
+  if (tid == 0) first_group = INT32_MAX;
+  const int parts = 1 + __syncthreads_count(inside);
+  if (inside) atomicMin(&first_group, tid);
+  __syncthreads();
+  const int group = first_group;  // the first boundary; the part before it is the previous group's
+  if (parts == 1 || (!BY_ITEM && group != static_cast<int>(blockIdx.x) + 1)) return;
+  const Item it = item_of(p, item);
   const int c = it.c0 + member * kChunkRows;
-  const int rows = min(kChunkRows, it.rows - c);
-  const int row_lo = blockIdx.z * kJoinRows;
-  if (row_lo >= rows) return;
-  const int row_hi = min(rows, row_lo + kJoinRows);
-  int parts = 1;
-  while (group + parts - 1 < used && run_start(total, group + parts - 1, used) < end) ++parts;
-  // part i: group - 1 + i; the first one is its group's last segment, the others their groups' first
-  auto slot_row = [&](int i, int r) {
-    return ((static_cast<int64_t>(group - 1 + i) * 2 + (i == 0)) * p.members + member) * kChunkRows + r;
-  };
-  const bool share = parts > 4;
-  for (int r = share ? row_lo : row_lo + warp; r < row_hi; r += share ? 1 : kJoinThreads / 32) {
-    const int i0 = share ? warp : 0, step = share ? kJoinThreads / 32 : 1;
+  const int r = BY_ITEM ? blockIdx.z : blockIdx.z * kJoinWarps + warp;
+  const bool have = r < min(kChunkRows, it.rows - c);
+  if (BY_ITEM && !have) return;
+  if (have) {
+    // part i: group - 1 + i; the first one is its group's last segment, the others their groups' first
+    const auto row_of = [&](int i) {
+      return ((static_cast<int64_t>(group - 1 + i) * 2 + (i == 0)) * p.members + member) * kChunkRows + r;
+    };
     float M = -INFINITY;
-    for (int i = lane; i < parts; i += 32) M = fmaxf(M, p.stats[slot_row(i, r)].x);
+    for (int i = lane; i < parts; i += 32) M = fmaxf(M, p.stats[row_of(i)].x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     const float ref = M == -INFINITY ? 0.0f : M;
     float4 acc[kVec] = {};
     float l = 0.0f;
 #pragma unroll 4
-    for (int i = i0; i < parts; i += step) {
-      const int64_t row = slot_row(i, r);
+    for (int i = BY_ITEM ? warp : 0; i < parts; i += BY_ITEM ? kJoinWarps : 1) {
+      const int64_t row = row_of(i);
       const float2 s = p.stats[row];
       const float w = ex2(s.x - ref);
       l = fmaf(w, s.y, l);
@@ -706,35 +715,34 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         acc[v].w = fmaf(w, o.w, acc[v].w);
       }
     }
-    if (share) {
+    if constexpr (BY_ITEM) {
 #pragma unroll
-      for (int v = 0; v < kVec; ++v) reinterpret_cast<float4*>(sum[warp])[v * 32 + lane] = acc[v];
-      if (lane == 0) ml[warp] = make_float2(M, l);
+      for (int v = 0; v < kVec; ++v) sum[warp][v * 32 + lane] = acc[v];
+      if (lane == 0) part_l[warp] = l;
       __syncthreads();
-      if (warp == 0) {
-        for (int w = 1; w < kJoinThreads / 32; ++w) {
-          l += ml[w].y;
+      if (warp >= kVec) return;
+      // warp v adds the warps' shares of its 128 values
+      l = part_l[0];
+      acc[0] = sum[0][warp * 32 + lane];
 #pragma unroll
-          for (int v = 0; v < kVec; ++v) {
-            const float4 o = reinterpret_cast<const float4*>(sum[w])[v * 32 + lane];
-            acc[v].x += o.x;
-            acc[v].y += o.y;
-            acc[v].z += o.z;
-            acc[v].w += o.w;
-          }
-        }
+      for (int w = 1; w < kJoinWarps; ++w) {
+        const float4 o = sum[w][warp * 32 + lane];
+        l += part_l[w];
+        acc[0].x += o.x;
+        acc[0].y += o.y;
+        acc[0].z += o.z;
+        acc[0].w += o.w;
       }
     }
-    if (!share || warp == 0) {
-      const int t = it.q0 + (c + r) / p.group, h = it.hk * p.group + (c + r) % p.group;
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      uint2* out = reinterpret_cast<uint2*>(p.out + t * p.out_row_stride + static_cast<int64_t>(h) * C::kDv);
+    const int t = it.q0 + (c + r) / p.group, h = it.hk * p.group + (c + r) % p.group;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint2* out = reinterpret_cast<uint2*>(p.out + t * p.out_row_stride + static_cast<int64_t>(h) * C::kDv);
 #pragma unroll
-      for (int v = 0; v < kVec; ++v)
-        out[v * 32 + lane] = make_uint2(pack2<DTYPE>(acc[v].x * inv, acc[v].y * inv), pack2<DTYPE>(acc[v].z * inv, acc[v].w * inv));
-      if (p.lse && lane == 0) p.lse[static_cast<int64_t>(t) * p.num_heads + h] = row_lse(M, l);
-    }
-    if (share) __syncthreads();
+    for (int v = 0; v < (BY_ITEM ? 1 : kVec); ++v)
+      out[(BY_ITEM ? warp : v) * 32 + lane] =
+          make_uint2(pack2<DTYPE>(acc[v].x * inv, acc[v].y * inv), pack2<DTYPE>(acc[v].z * inv, acc[v].w * inv));
+    if (p.lse && lane == 0 && (!BY_ITEM || warp == 0))
+      p.lse[static_cast<int64_t>(t) * p.num_heads + h] = row_lse(M, l);
   }
 }
 
@@ -756,10 +764,17 @@ cudaError_t launch(const AttnParams& p, cudaStream_t stream) {
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, attention_kernel<DTYPE, LATENT>, p)) != cudaSuccess) return e;
   if (p.groups < 2) return cudaSuccess;
-  cfg.gridDim = dim3(static_cast<unsigned>(p.groups - 1), static_cast<unsigned>(p.members), kChunkRows / kJoinRows);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, join_kernel<DTYPE, LATENT>, p);
+  // rows that a CTA of the first kernel can hold
+  const int64_t pairs = (p.indices ? 1 : static_cast<int64_t>(p.max_seqlen_q)) * p.group;
+  const unsigned rows = static_cast<unsigned>(pairs < kChunkRows ? pairs : kChunkRows);
+  if (p.items < p.groups) {
+    cfg.gridDim = dim3(static_cast<unsigned>(p.items), static_cast<unsigned>(p.members), rows);
+    return cudaLaunchKernelEx(&cfg, join_kernel<DTYPE, LATENT, true>, p);
+  }
+  cfg.gridDim = dim3(static_cast<unsigned>(p.groups - 1), static_cast<unsigned>(p.members), (rows + kJoinWarps - 1) / kJoinWarps);
+  return cudaLaunchKernelEx(&cfg, join_kernel<DTYPE, LATENT, false>, p);
 }
 
 int64_t round16(int64_t n) { return (n + 15) & ~int64_t{15}; }
@@ -781,7 +796,8 @@ bool plan_attention(AttnParams* p, int sms) {
   // no more groups than tiles can exist
   const int64_t per_item = p->indices ? p->list_tiles : (static_cast<int64_t>(p->max_seqlen_k) + tk - 1) / tk;
   const int64_t most = items * (per_item < 1 ? 1 : per_item);
-  const int64_t groups = sms / p->members;
+  int64_t groups = sms / p->members;
+  if (groups > kJoinThreads) groups = kJoinThreads;  // the join looks at one group per thread
   p->groups = static_cast<int32_t>(most < groups ? most : groups);
   return true;
 }

@@ -7,15 +7,27 @@
 
 namespace fp4idx {
 
-// D[tmem] (+)= A[smem] * B[smem]^T, 16-bit operands, fp32 accumulator.
+// D[tmem] (+)= A[smem] * B[smem]^T, 16-bit operands, fp32 accumulator, issued
+// by one elected lane of a converged warp.  The whole warp executes the call
+// so that the operands stay in uniform registers: issued from a single
+// thread's branch each MMA cost 56 cycles of register moves, which is more
+// than a 64x64x16 or 128x64x16 MMA takes (31 and 45 cycles, measured).
 __device__ __forceinline__ void tc_mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                            uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// tc_commit by the same elected lane (a commit covers its own thread's MMAs).
+__device__ __forceinline__ void tc_commit_elected(uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // Instruction descriptor of kind::f16 with an fp32 accumulator; both operands
 // fp16 (bf16 false) or both bf16.  a_mn: A is stored with M contiguous.
