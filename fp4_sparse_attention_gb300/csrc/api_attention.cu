@@ -1,6 +1,7 @@
 // api_attention.cu -- the C ABI of the attention calls, the 16-bit cache
 // writers and the step tables (include/fp4idx.h): host-side argument checks
 // and launches.  Nothing here reads device memory or synchronises.
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 
@@ -16,6 +17,8 @@ namespace {
     set_last_error(__VA_ARGS__); \
     return status;               \
   } while (0)
+
+constexpr float kLog2e = 1.44269504088896341f;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -67,7 +70,7 @@ fp4idx_status_t check_attention(const fp4idx_attention_t* a, bool latent) {
            static_cast<long long>(need));
   }
   if (a->qo_offset && !a->causal) FAIL(FP4IDX_EINVAL, "qo_offset is only allowed with causal != 0");
-  if (!std::isfinite(a->scale)) FAIL(FP4IDX_EINVAL, "scale must be finite");
+  if (!std::isfinite(a->scale * kLog2e)) FAIL(FP4IDX_EINVAL, "scale must be finite");
   if (a->indices && a->num_indices < 1) FAIL(FP4IDX_EINVAL, "num_indices must be >= 1 with indices");
   if (a->indices && a->num_indices > (1 << 20)) FAIL(FP4IDX_EUNSUPPORTED, "num_indices %d: up to 2^20", a->num_indices);
   return FP4IDX_OK;
@@ -102,7 +105,10 @@ AttnParams attention_params(const fp4idx_attention_t* a) {
   p.max_seqlen_k = a->max_seqlen_k;
   p.indices = a->indices;
   p.num_indices = a->indices ? a->num_indices : 0;
-  p.scale_log2 = a->scale * 1.44269504088896341f;
+  // scale 0 becomes the smallest normal number: every finite score still is 0
+  // to fp32, and a masked one stays -inf (not 0 * -inf)
+  p.scale_log2 = std::fmax(std::fabs(a->scale) * kLog2e, FLT_MIN);
+  p.negate = a->scale < 0.0f;
   p.out = static_cast<uint16_t*>(a->out);
   p.out_row_stride = a->out_row_stride;
   p.lse = a->lse;

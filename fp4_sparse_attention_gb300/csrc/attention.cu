@@ -79,6 +79,7 @@ struct Control {
   int64_t row_off[kChunkRows];                                 // output element of each row
   int64_t plan[4];                                             // first item, its first tile, lo, hi
   int32_t key_pos[Cfg<LATENT>::kStages][Cfg<LATENT>::kTk];     // logical position, -1: no key
+  alignas(8) uint8_t holes[Cfg<LATENT>::kStages][kLoadWarps];             // a loader warp found a key that does not exist
   float factor[kChunkRows], row_inv[kChunkRows];
   uint32_t tmem;
   int abort;
@@ -369,6 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         const uint32_t st = g % C::kStages;
         ok = warp_wait(smem_u32(&ctl.kempty[st]), ((g / C::kStages) & 1) ^ 1, abort_flag, p.err);
         if (!ok) return;
+        bool hole = false;
 #pragma unroll
         for (int n = 0; n < kPasses; ++n) {
           const int key = n * (kLoadThreads / 8) + (lt >> 3);
@@ -383,7 +385,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             for (int c = 0; c < C::kVc; ++c) cp_async_16_or_zero(dst + C::kV + c * C::kPiece, vsrc + c * 64, have);
           }
           if (u == 0) ctl.key_pos[st][key] = pos[n];
+          hole |= !have;
         }
+        hole = __any_sync(0xffffffffu, hole);
+        if (lane == 0) ctl.holes[st][lt >> 5] = hole;
         cp_async_arrive(smem_u32(&ctl.kfull[st]));
         if (u == 0) mbar_arrive(smem_u32(&ctl.kfull[st]));
         if (i + 1 < s.hi) locate(i + 1);
@@ -397,14 +402,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     uint32_t g = 0, seg = 0;
     bool ok = true;
     const uint32_t tm = uniform(tmem);
-    const uint32_t qk_idesc = idesc_f16(64, TK, DTYPE == FP4IDX_BF16, false);
+    const uint32_t qk_idesc = uniform(idesc_f16(64, TK, DTYPE == FP4IDX_BF16, false, p.negate != 0));
     const uint64_t q_desc = desc_sw128(base + C::kOff_Q, 16), p_desc = desc_sw128(base + C::kOff_P, 16);
     auto ready = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_test_wait(smem_u32(bar), parity));
     };
     for_segments<TK>(p, ctl.plan, member, [&](const Segment& s) {
       if (!ok) return;
-      const uint32_t pv_idesc = uniform(idesc_f16(128, (s.rows + 15) & ~15, DTYPE == FP4IDX_BF16, true));
+      const uint32_t pv_idesc = uniform(idesc_f16(128, (s.rows + 15) & ~15, DTYPE == FP4IDX_BF16, true, false));
       const uint32_t n = uniform(s.hi - s.lo);
       uint32_t qk = 0, pv = 0, spins = 0;
       uint64_t t0 = 0;
@@ -479,15 +484,19 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const int r0 = 16 * warp + (lane >> 2);                 // this thread's rows: r0 and r0 + 8
     const uint32_t quarter = static_cast<uint32_t>(warp) << 21;  // TMEM lanes 32 * warp
     for_segments<TK>(p, ctl.plan, member, [&](const Segment& s) {
+      // rows past the chunk's end have zero queries: their scores are harmless
       int vis[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = r0 + 8 * i;
-        vis[i] = r < s.rows ? attn_visible(p, s.it.b, s.it.q0 + (s.c + r) / p.group) : 0;
+        vis[i] = r < s.rows ? attn_visible(p, s.it.b, s.it.q0 + (s.c + r) / p.group) : INT32_MAX;
       }
+      // tiles that all of the warp's rows see whole (a selection's keys are all visible or holes)
+      const int full_tiles = p.indices ? INT32_MAX : __reduce_min_sync(0xffffffffu, min(vis[0], vis[1])) / TK;
       const bool active = 16 * warp < s.rows;
       const int cols = (s.rows + 15) & ~15;                  // O^T columns in use
-      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+      float m[2] = {-INFINITY, -INFINITY};                   // reference maximum, in powers of two
+      float2 l[2] = {};                                      // this thread's share of the sums
       for (int i = s.lo; i < s.hi; ++i, ++g) {
         const uint32_t buf = g & 1, st = g % C::kStages;
         float x[TK / 2];
@@ -497,6 +506,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           if (ok) ok = warp_wait(smem_u32(&ctl.sfull[buf]), (g >> 1) & 1, abort_flag, p.err);
           if (ok) ok = warp_wait(smem_u32(&ctl.kfull[st]), (g / C::kStages) & 1, abort_flag, p.err);
           tc_fence_after();
+          static_assert(kLoadWarps == 8, "holes of a stage are read as one word");
+          const bool mask = i >= full_tiles || *reinterpret_cast<const uint64_t*>(ctl.holes[st]) != 0;
 #pragma unroll
           for (int c = 0; c < TK / 64; ++c) {
             uint32_t r[32];
@@ -504,25 +515,28 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             tmem_wait_ld();
             reg_fence(r);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[c * 32 + e] = __uint_as_float(r[e]) * p.scale_log2;
+            for (int e = 0; e < 32; ++e) x[c * 32 + e] = __uint_as_float(r[e]);
           }
           tc_fence_before();
+          if (mask) {
+#pragma unroll
+            for (int j = 0; j < TK / 8; ++j) {
+              const int2 kp = *reinterpret_cast<const int2*>(&ctl.key_pos[st][8 * j + 2 * (lane & 3)]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e)  // -1 (no key) is the largest unsigned value
+                if (static_cast<uint32_t>(e & 1 ? kp.y : kp.x) >= static_cast<uint32_t>(vis[e >> 1])) x[4 * j + e] = -INFINITY;
+            }
+          }
           float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
           for (int j = 0; j < TK / 8; ++j) {
-            const int2 kp = *reinterpret_cast<const int2*>(&ctl.key_pos[st][8 * j + 2 * (lane & 3)]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              // -1 (no key) is the largest unsigned value
-              const bool seen = static_cast<uint32_t>(e & 1 ? kp.y : kp.x) < static_cast<uint32_t>(vis[e >> 1]);
-              x[4 * j + e] = seen ? x[4 * j + e] : -INFINITY;
-              top[e >> 1] = fmaxf(top[e >> 1], x[4 * j + e]);
-            }
+            top[0] = fmaxf(top[0], fmaxf(x[4 * j], x[4 * j + 1]));
+            top[1] = fmaxf(top[1], fmaxf(x[4 * j + 2], x[4 * j + 3]));
           }
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
-            top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+            top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2)) * p.scale_log2;
             if (top[e] > m[e] + kRaise) {
               f[e] = ex2(m[e] - top[e]);
               m[e] = top[e];
@@ -537,17 +551,23 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         if (active) {
           // weights, their sum in fp32, and P in 16 bits (the MMA's operand
           // type: each weight is rounded once, the sum is of unrounded ones)
-          const float ref[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
-          l[0] *= f[0];
-          l[1] *= f[1];
+          const float2 scale = make_float2(p.scale_log2, p.scale_log2);
+          const float2 ref0 = m[0] == -INFINITY ? make_float2(0.0f, 0.0f) : make_float2(-m[0], -m[0]);
+          const float2 ref1 = m[1] == -INFINITY ? make_float2(0.0f, 0.0f) : make_float2(-m[1], -m[1]);
+          l[0].x *= f[0];
+          l[0].y *= f[0];
+          l[1].x *= f[1];
+          l[1].y *= f[1];
 #pragma unroll
           for (int j = 0; j < TK / 8; ++j) {
-            const float a = ex2(x[4 * j] - ref[0]), b = ex2(x[4 * j + 1] - ref[0]);
-            const float c = ex2(x[4 * j + 2] - ref[1]), d = ex2(x[4 * j + 3] - ref[1]);
-            l[0] += a + b;
-            l[1] += c + d;
-            w[2 * j] = pack2<DTYPE>(a, b);
-            w[2 * j + 1] = pack2<DTYPE>(c, d);
+            float2 a = fma2(make_float2(x[4 * j], x[4 * j + 1]), scale, ref0);
+            float2 b = fma2(make_float2(x[4 * j + 2], x[4 * j + 3]), scale, ref1);
+            a = make_float2(ex2(a.x), ex2(a.y));
+            b = make_float2(ex2(b.x), ex2(b.y));
+            l[0] = add2(l[0], a);
+            l[1] = add2(l[1], b);
+            w[2 * j] = pack2<DTYPE>(a.x, a.y);
+            w[2 * j + 1] = pack2<DTYPE>(b.x, b.y);
           }
         }
         // the previous product has read P and updated O^T
@@ -588,10 +608,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         if (lane == 0) mbar_arrive(smem_u32(&ctl.pfull));
       }
       // ---- output of the segment
+      float sum[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+        sum[e] = l[e].x + l[e].y;
+        sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
+        sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
       }
       const bool whole = s.lo == 0 && s.hi == s.tiles;
       const int64_t slot = (static_cast<int64_t>(group) * 2 + (s.lo == 0)) * p.members + member;
@@ -600,13 +622,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         for (int e = 0; e < 2; ++e) {
           const int r = r0 + 8 * e;
           const int t = s.it.q0 + (s.c + r) / p.group, h = s.it.hk * p.group + (s.c + r) % p.group;
-          ctl.row_inv[r] = l[e] == 0.0f ? 0.0f : 1.0f / l[e];
+          ctl.row_inv[r] = sum[e] == 0.0f ? 0.0f : 1.0f / sum[e];
           ctl.row_off[r] = t * p.out_row_stride + static_cast<int64_t>(h) * C::kDv;
           if (r < s.rows && ok) {
             if (!whole)
-              p.stats[slot * kChunkRows + r] = make_float2(m[e], l[e]);
+              p.stats[slot * kChunkRows + r] = make_float2(m[e], sum[e]);
             else if (p.lse)
-              p.lse[static_cast<int64_t>(t) * p.num_heads + h] = row_lse(m[e], l[e]);
+              p.lse[static_cast<int64_t>(t) * p.num_heads + h] = row_lse(m[e], sum[e]);
           }
         }
       }

@@ -37,7 +37,8 @@ struct AttnParams {
   int32_t max_seqlen_q, max_seqlen_k;
   const int32_t* indices;               // nullptr: whole prefix
   int32_t num_indices;
-  float scale_log2;                     // scale * log2(e): scores in powers of two
+  float scale_log2;                     // |scale| * log2(e): scores in powers of two
+  int32_t negate;                       // scale < 0: the product is of -q
   uint16_t* out;
   int64_t out_row_stride;
   float* lse;
