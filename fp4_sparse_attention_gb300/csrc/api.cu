@@ -298,6 +298,19 @@ fp4idx_status_t call_device(int* sms, uint32_t** err) {
   return FP4IDX_OK;
 }
 
+fp4idx_status_t call_tensor_map16(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
+                                  const cuuint64_t* strides, const cuuint32_t* box) {
+  EncodeTiledFn fn;
+  fp4idx_status_t s = encode_fn(&fn);
+  if (s != FP4IDX_OK) return s;
+  cuuint32_t elem[4] = {1, 1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, rank, const_cast<void*>(base), dims, strides, box, elem,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(FP4IDX_EINVAL, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return FP4IDX_OK;
+}
+
 void set_last_error(const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);

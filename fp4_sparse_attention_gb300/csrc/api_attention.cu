@@ -43,6 +43,9 @@ fp4idx_status_t check_attention(const fp4idx_attention_t* a, bool latent) {
   if (a->page_size != 64 && a->page_size != 128)
     FAIL(FP4IDX_EUNSUPPORTED, "page_size %d: only 64 and 128 are supported", a->page_size);
   if (a->num_pages < 1) FAIL(FP4IDX_EINVAL, "num_pages must be >= 1");
+  if (a->num_pages >= INT32_MAX || a->page_stride >= int64_t{1} << 39 ||
+      static_cast<int64_t>(a->num_kv_heads) * a->page_size > INT32_MAX)
+    FAIL(FP4IDX_EUNSUPPORTED, "num_pages below 2^31 - 1 and page_stride below 2^39 are supported");
   if (a->max_seqlen_q < 1 || a->max_seqlen_k < 0)
     FAIL(FP4IDX_EINVAL, "max_seqlen_q >= 1 and max_seqlen_k >= 0 required");
   if (!a->q || !a->k || (!latent && !a->v) || !a->cu_seqlens_q || !a->cu_seqlens_k || !a->block_table || !a->out)
@@ -115,6 +118,20 @@ AttnParams attention_params(const fp4idx_attention_t* a) {
   return p;
 }
 
+// Tensor maps of the caches (selected latent rows are copied without one).
+fp4idx_status_t cache_maps(const fp4idx_attention_t* a, bool latent, AttnMaps* maps) {
+  std::memset(maps, 0, sizeof(*maps));
+  if (latent && a->indices) return FP4IDX_OK;
+  const cuuint64_t dk = latent ? kLatentDim + kRopeDim : kPagedDim;
+  const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(a->num_kv_heads) * a->page_size, dk / 64,
+                              static_cast<cuuint64_t>(a->num_pages)};
+  const cuuint64_t strides[3] = {dk * 2, 128, static_cast<cuuint64_t>(a->page_stride) * 2};
+  const cuuint32_t box[4] = {64, 64, static_cast<cuuint32_t>(latent ? kLatentBoxPieces : kPagedBoxPieces), 1};
+  fp4idx_status_t s = call_tensor_map16(&maps->k, a->k, 4, dims, strides, box);
+  if (s != FP4IDX_OK || latent) return s;
+  return call_tensor_map16(&maps->v, a->v, 4, dims, strides, box);
+}
+
 fp4idx_status_t attention_any(const fp4idx_attention_t* a, bool latent, void* workspace, size_t workspace_bytes,
                               void* stream) {
   set_last_error("%s", "");
@@ -129,7 +146,9 @@ fp4idx_status_t attention_any(const fp4idx_attention_t* a, bool latent, void* wo
   if (!workspace || workspace_bytes < need)
     FAIL(FP4IDX_EWORKSPACE, "workspace of %zu bytes is smaller than %zu", workspace ? workspace_bytes : size_t{0}, need);
   if (!aligned(workspace, 16)) FAIL(FP4IDX_EINVAL, "workspace must be 16-byte aligned");
-  return cuda_status(launch_attention(p, a->dtype, workspace, static_cast<cudaStream_t>(stream)), "attention launch");
+  AttnMaps maps;
+  if ((s = cache_maps(a, latent, &maps)) != FP4IDX_OK) return s;
+  return cuda_status(launch_attention(p, maps, a->dtype, workspace, static_cast<cudaStream_t>(stream)), "attention launch");
 }
 
 // Arguments that both cache writers share.

@@ -19,7 +19,7 @@
 // wants and, read along the other axis, the MN-major layout V^T wants; for
 // the latent cache K and V are even the same bytes.
 //
-// Roles (13 warps, one CTA per SM):
+// Roles (one CTA per SM):
 //   warps 0-3   softmax: TMEM S as row fragments (four lanes per row), mask,
 //               running maximum, 2^x, P to shared memory; rescale of O^T when
 //               a row's maximum grew by more than 2^8 (until then the older
@@ -27,8 +27,17 @@
 //               the result is the same up to rounding); the output.
 //   warp 4      MMA issuer: whichever of the next tile's Q K^T and this
 //               tile's V^T P^T is ready.
-//   warps 5-12  loaders: page lookup or selection, 16-byte asynchronous copies
-//               (zeros for keys that do not exist), key positions.
+//   warps 5-    loaders: a 64-key run of one page by TMA; listed keys, and a
+//               run that a request ends in, by 16-byte asynchronous copies
+//               (zeros for keys that do not exist); key positions.  A gather
+//               of four rows by TMA (tile::gather4) moves 512 bytes an
+//               instruction and reached 6.7-8.7 TB/s from L2 where the copies
+//               reach 20.
+// A tile arrives and leaves in parts (latent: three times 192 of the 576
+// values; paged: keys, values): the score product starts with the first part
+// and a part is loaded again as soon as its last product is done, which is
+// what two 74 KB stages of latent keys beside 74 KB of queries need to
+// overlap loads with products.
 //
 // Work split: the tiles of all items (request or row, K/V head, row chunk)
 // are concatenated and cut into equal runs, one per CTA group, so long and
@@ -44,9 +53,8 @@
 namespace fp4idx {
 namespace {
 
-constexpr int kSoftmaxWarps = 4, kMmaWarp = 4, kLoadWarps = 8;
-constexpr int kThreads = 32 * (kSoftmaxWarps + 1 + kLoadWarps);
-constexpr int kLoadThreads = 32 * kLoadWarps;
+constexpr int kSoftmaxWarps = 4, kMmaWarp = 4;
+constexpr int kTeamWarps = 4, kTeamThreads = 32 * kTeamWarps;  // loader teams take tiles in turn
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxMembers = 8;
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
@@ -58,12 +66,18 @@ struct Cfg {
   static constexpr int kDk = LATENT ? kLatentDim + kRopeDim : kPagedDim;
   static constexpr int kDv = LATENT ? kLatentDim : kPagedDim;
   static constexpr int kTk = LATENT ? 64 : 128;                 // keys per tile
+  static constexpr int kRuns = kTk / 64;                        // 64-key runs of a tile: each inside one page
   static constexpr int kStages = LATENT ? 2 : 3;
+  static constexpr int kParts = LATENT ? 3 : 2;                 // parts of a stage that arrive and leave alone
+  static constexpr int kPosPart = LATENT ? 0 : 1;               // the part whose barriers guard the positions: it leaves after the softmax
+  static constexpr int kTeams = LATENT ? 2 : 1;
+  static constexpr int kThreads = 32 * (kSoftmaxWarps + 1 + kTeams * kTeamWarps);
   static constexpr int kKc = kDk / 64;                          // 128-byte pieces of a key
-  static constexpr int kVc = LATENT ? 0 : kDv / 64;             // pieces of a separate value row
-  static constexpr uint32_t kPiece = kTk * 128;                 // one piece of every key of a tile
-  static constexpr uint32_t kStage = (kKc + kVc) * kPiece;
-  static constexpr uint32_t kV = LATENT ? 0 : kKc * kPiece;     // values inside a stage
+  static constexpr int kPartPieces = LATENT ? kLatentBoxPieces : kPagedBoxPieces;  // pieces of a part, per run
+  static constexpr uint32_t kPiece = 64 * 128;                  // one piece of a run's keys
+  static constexpr uint32_t kPart = kRuns * kPartPieces * kPiece;
+  static constexpr uint32_t kStage = kParts * kPart;
+  static constexpr uint32_t kV = LATENT ? 0 : kPart;            // values inside a stage
   static constexpr uint32_t kQ = kKc * kChunkRows * 128;
   static constexpr uint32_t kP = kTk / 64 * kChunkRows * 128;
   static constexpr uint32_t kOff_Q = kStages * kStage;
@@ -74,12 +88,12 @@ struct Cfg {
 
 template <bool LATENT>
 struct Control {
-  uint64_t kfull[Cfg<LATENT>::kStages], kempty[Cfg<LATENT>::kStages];
+  uint64_t kfull[Cfg<LATENT>::kStages][Cfg<LATENT>::kParts], kempty[Cfg<LATENT>::kStages][Cfg<LATENT>::kParts];
   uint64_t sfull[2], sempty[2], pfull, pvdone, qfull, qempty, oempty, drain;
   int64_t row_off[kChunkRows];                                 // output element of each row
   int64_t plan[4];                                             // first item, its first tile, lo, hi
   int32_t key_pos[Cfg<LATENT>::kStages][Cfg<LATENT>::kTk];     // logical position, -1: no key
-  alignas(8) uint8_t holes[Cfg<LATENT>::kStages][kLoadWarps];             // a loader warp found a key that does not exist
+  alignas(4) uint8_t holes[Cfg<LATENT>::kStages][kTeamWarps];  // a loader warp found a key that does not exist
   float factor[kChunkRows], row_inv[kChunkRows];
   uint32_t tmem;
   int abort;
@@ -198,7 +212,8 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 
 // ---------------------------------------------------------------- kernel
 template <int DTYPE, bool LATENT>
-__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(const __grid_constant__ AttnParams p,
+                                                                const __grid_constant__ AttnMaps maps) {
   using C = Cfg<LATENT>;
   constexpr int TK = C::kTk;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -216,8 +231,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   }
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(smem_u32(&ctl.kfull[s]), kLoadThreads + kLoadThreads / 8);
-      mbar_init(smem_u32(&ctl.kempty[s]), 1);
+      for (int j = 0; j < C::kParts; ++j) {
+        mbar_init(smem_u32(&ctl.kfull[s][j]), kTeamWarps);
+        mbar_init(smem_u32(&ctl.kempty[s][j]), 1);
+      }
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_u32(&ctl.sfull[s]), 1);
@@ -225,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     }
     mbar_init(smem_u32(&ctl.pfull), kSoftmaxWarps);
     mbar_init(smem_u32(&ctl.pvdone), 1);
-    mbar_init(smem_u32(&ctl.qfull), kLoadThreads);
+    mbar_init(smem_u32(&ctl.qfull), C::kTeams * kTeamWarps);
     mbar_init(smem_u32(&ctl.qempty), 1);
     mbar_init(smem_u32(&ctl.oempty), kSoftmaxWarps);
     mbar_init(smem_u32(&ctl.drain), 1);
@@ -259,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     // every thread sums a run of items; then the thread whose run holds this
     // group's first tile finds the item (the key ring is not in use yet)
     int64_t* warp_sum = reinterpret_cast<int64_t*>(smem);
-    const int per = (p.items + kThreads - 1) / kThreads;
+    const int per = (p.items + C::kThreads - 1) / C::kThreads;
     const int first = min(p.items, tid * per), last = min(p.items, first + per);
     int64_t mine = 0;
     for (int i = first; i < last; ++i) mine += item_tiles<TK>(p, item_of(p, i), 0, 1);
@@ -272,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
     int64_t before = incl - mine, total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
+    for (int w = 0; w < C::kThreads / 32; ++w) {
       before += w < warp ? warp_sum[w] : 0;
       total += warp_sum[w];
     }
@@ -308,10 +325,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 
   if (warp >= kMmaWarp + 1) {
     // ================================================================ loaders
-    const int lt = tid - 32 * (kMmaWarp + 1);
-    const int u = lt & 7;                                   // 16-byte unit of a 128-byte piece
-    constexpr int kPasses = TK / (kLoadThreads / 8);
-    uint32_t g = 0, seg = 0;
+    // Every warp of a team arrives once per part, after its share is issued
+    // (TMA, whose bytes the barrier counts) or has landed (copies).
+    const int lw = warp - (kMmaWarp + 1), team = lw / kTeamWarps, tw = lw % kTeamWarps;
+    const int lt = tid - 32 * (kMmaWarp + 1) - team * kTeamThreads;
+    const int u = lt & 7, key0 = lt >> 3;                   // 16-byte unit of a 128-byte piece; first key
+    constexpr int kPass = kTeamThreads / 8;                 // keys the team copies at a time
+    constexpr int kFind = LATENT ? 64 / kPass : C::kRuns;   // positions a thread looks up: runs, or its listed keys
+    uint32_t g = 0, seg = 0;                                // tiles and segments before this one
+    uint32_t issued = 0;                                    // this team's last tile, counted from 1
     bool ok = true;
     for_segments<TK>(p, ctl.plan, member, [&](const Segment& s) {
       if (!ok) return;
@@ -320,91 +342,194 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       if (p.indices)
         list = p.indices + (LATENT ? static_cast<int64_t>(s.it.q0)
                                    : static_cast<int64_t>(s.it.hk) * p.num_rows + s.it.q0) * p.num_indices;
-      // position and cache element of this thread's keys of tile i
-      int32_t pos[kPasses];
-      int64_t at[kPasses];
-      auto locate = [&](int i) {
-#pragma unroll
-        for (int n = 0; n < kPasses; ++n) {
-          const int64_t j = static_cast<int64_t>(i) * TK + n * (kLoadThreads / 8) + (lt >> 3);
-          int32_t q = -1;
-          if (!list) {
-            if (j < s.max_vis) q = static_cast<int32_t>(j);
-          } else if (LATENT) {
-            if (j < p.num_indices) q = __ldg(list + j);
-          } else {  // a tile is one listed block
-            const int32_t blk = __ldg(list + i);
-            if (blk >= 0 && blk <= (INT32_MAX - kSelectBlock) / kSelectBlock) q = blk * kSelectBlock + static_cast<int32_t>(j % kSelectBlock);
-          }
-          if (q >= s.max_vis) q = -1;
-          pos[n] = q;
-          at[n] = 0;
-          if (q >= 0) {
-            const int64_t page = __ldg(p.block_table + table + (q >> p.page_shift));
-            if (page < 0 || page >= p.num_pages) {
-              if (u == 0) atomicOr(p.err, kErrPageRange);
-              pos[n] = -1;
-            } else {
-              at[n] = page * p.page_stride +
-                      (static_cast<int64_t>(s.it.hk) * p.page_size + (q & (p.page_size - 1))) * C::kDk;
-            }
-          }
+      const bool rows_listed = LATENT && list;              // keys are single rows, not runs
+      // position n of tile i, -1 for none; loaded two tiles ahead
+      const auto find = [&](int i, int n) -> int32_t {
+        if (i >= s.hi) return -1;
+        int32_t q = -1;
+        if (rows_listed) {
+          const int64_t j = static_cast<int64_t>(i) * TK + n * kPass + key0;
+          q = j < p.num_indices ? __ldg(list + j) : -1;
+        } else if (n >= C::kRuns) {
+        } else if (list) {  // a tile is one listed block
+          const int32_t blk = __ldg(list + i);
+          q = blk >= 0 && blk <= (INT32_MAX - kSelectBlock) / kSelectBlock ? blk * kSelectBlock + 64 * n : -1;
+        } else {
+          q = i * TK + 64 * n;
         }
+        return q;
       };
-      locate(s.lo);
-      // queries of the segment, once the previous segment's products are done
-      ok = warp_wait(smem_u32(&ctl.qempty), (seg & 1) ^ 1, abort_flag, p.err);
-      if (!ok) return;
+      // its block-table entry; loaded one tile ahead
+      const auto entry = [&](int32_t q) -> int32_t {
+        return q >= 0 && q < s.max_vis ? __ldg(p.block_table + table + (q >> p.page_shift)) : -1;
+      };
+      int i = s.lo + static_cast<int>((team + C::kTeams - g % C::kTeams) % C::kTeams);  // the team's first tile
+      int32_t now[kFind], page[kFind], next[kFind];
 #pragma unroll
-      for (int n = 0; n < kChunkRows / (kLoadThreads / 8); ++n) {
-        const int r = n * (kLoadThreads / 8) + (lt >> 3);
+      for (int n = 0; n < kFind; ++n) {
+        now[n] = find(i, n);
+        next[n] = find(i + C::kTeams, n);
+      }
+#pragma unroll
+      for (int n = 0; n < kFind; ++n) page[n] = entry(now[n]);
+      // queries of the segment, once the previous segment's products are done
+      ok = warp_try(smem_u32(&ctl.qempty), (seg & 1) ^ 1, abort_flag, p.err);
+      if (!ok) return;
+#pragma unroll 1
+      for (int r = team * kPass + key0; r < kChunkRows; r += C::kTeams * kPass) {
         const bool have = r < s.rows;
-        const int t = s.it.q0 + (s.c + (have ? r : 0)) / p.group, h = s.it.hk * p.group + (s.c + (have ? r : 0)) % p.group;
+        const int x = s.c + (have ? r : 0), t = s.it.q0 + x / p.group, h = s.it.hk * p.group + x % p.group;
         const uint16_t* src = p.q + t * p.q_row_stride + h * p.q_head_stride + u * 8;
         const uint32_t dst = base + C::kOff_Q + r * 128 + ((u ^ (r & 7)) << 4);
 #pragma unroll
         for (int c = 0; c < C::kKc; ++c) cp_async_16_or_zero(dst + c * (kChunkRows * 128), src + c * 64, have);
       }
-      cp_async_arrive(smem_u32(&ctl.qfull));
-      for (int i = s.lo; i < s.hi; ++i, ++g) {
-        const uint32_t st = g % C::kStages;
-        ok = warp_wait(smem_u32(&ctl.kempty[st]), ((g / C::kStages) & 1) ^ 1, abort_flag, p.err);
-        if (!ok) return;
-        bool hole = false;
+      cp_async_commit();
+      bool q_landed = false;
+      const auto queries_landed = [&] {  // called once this warp's copies so far have landed
+        if (lane == 0 && !q_landed) mbar_arrive(smem_u32(&ctl.qfull));
+        q_landed = true;
+      };
+      for (; i < s.hi; i += C::kTeams) {
+        const uint32_t x = g + (i - s.lo), st = x % C::kStages, ph = ((x / C::kStages) & 1) ^ 1;
+        const uint32_t stage = base + st * C::kStage;
+        // what the table says: pages outside the cache hold no keys
+        int32_t pos[kFind];
+        bool hole = false, ends = false;                    // a key missing; a run that ends inside
 #pragma unroll
-        for (int n = 0; n < kPasses; ++n) {
-          const int key = n * (kLoadThreads / 8) + (lt >> 3);
-          const bool have = pos[n] >= 0;
-          const uint32_t dst = base + st * C::kStage + key * 128 + ((u ^ (key & 7)) << 4);
-          const uint16_t* src = p.k + at[n] + u * 8;
-#pragma unroll
-          for (int c = 0; c < C::kKc; ++c) cp_async_16_or_zero(dst + c * C::kPiece, src + c * 64, have);
-          if constexpr (!LATENT) {
-            const uint16_t* vsrc = p.v + at[n] + u * 8;
-#pragma unroll
-            for (int c = 0; c < C::kVc; ++c) cp_async_16_or_zero(dst + C::kV + c * C::kPiece, vsrc + c * 64, have);
+        for (int n = 0; n < kFind; ++n) {
+          pos[n] = now[n] < s.max_vis ? now[n] : -1;
+          if (pos[n] >= 0 && (page[n] < 0 || page[n] >= p.num_pages)) {
+            if (rows_listed ? u == 0 : lt == 0) atomicOr(p.err, kErrPageRange);
+            pos[n] = -1;
           }
-          if (u == 0) ctl.key_pos[st][key] = pos[n];
-          hole |= !have;
+          hole |= pos[n] < 0 && (rows_listed || n < C::kRuns);
+          if (!rows_listed) ends |= pos[n] >= 0 && s.max_vis - pos[n] < 64;
         }
-        hole = __any_sync(0xffffffffu, hole);
-        if (lane == 0) ctl.holes[st][lt >> 5] = hole;
-        cp_async_arrive(smem_u32(&ctl.kfull[st]));
-        if (u == 0) mbar_arrive(smem_u32(&ctl.kfull[st]));
-        if (i + 1 < s.hi) locate(i + 1);
+        const bool boxes = !rows_listed && !ends, issuer = boxes && tw == 0;
+        hole = __any_sync(0xffffffffu, hole || ends);
+        if (issuer) {
+          // the bytes can be announced before the part is free, once its last load is complete
+#pragma unroll
+          for (int j = 0; j < C::kParts; ++j) {
+            const uint32_t bar = smem_u32(&ctl.kfull[st][j]);
+            const bool over = x < C::kStages || warp_try(bar, ph, abort_flag, p.err);
+            if (over && lane == 0) mbar_arrive_expect_tx(bar, C::kPart);
+          }
+        }
+        __syncwarp();
+        int64_t from[TK / kPass];                           // cache element of this thread's keys, -1: zeros
+        if (!boxes) {
+#pragma unroll
+          for (int n = 0; n < TK / kPass; ++n) {
+            const int f = rows_listed ? n % kFind : n * kPass / 64;
+            int32_t q = pos[f];
+            if (!rows_listed && q >= 0) {
+              q += (n * kPass + key0) & 63;
+              if (q >= s.max_vis) q = -1;
+            }
+            from[n] = q < 0 ? -1
+                            : page[f] * p.page_stride + (static_cast<int64_t>(s.it.hk) * p.page_size +
+                                                         (q & (p.page_size - 1))) * C::kDk + u * 8;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < C::kParts; ++j) {
+          ok = warp_try(smem_u32(&ctl.kempty[st][j]), ph, abort_flag, p.err);
+          if (!ok) return;
+          if (j == C::kPosPart && !issuer) {                // positions for the masks
+            if (rows_listed) {
+#pragma unroll
+              for (int n = 0; n < kFind; ++n)
+                if (u == 0) ctl.key_pos[st][n * kPass + key0] = pos[n];
+            } else if (lt >= 32 && lt < 96) {
+#pragma unroll
+              for (int n = 0; n < C::kRuns; ++n) {
+                const int k = lt - 32;
+                ctl.key_pos[st][64 * n + k] = pos[n] >= 0 && pos[n] + k < s.max_vis ? pos[n] + k : -1;
+              }
+            }
+            if (lane == 0) {
+              if (!boxes) ctl.holes[st][tw] = hole;
+              else if (tw == 1) *reinterpret_cast<uint32_t*>(ctl.holes[st]) = hole;
+            }
+            __syncwarp();
+          }
+          if (issuer) {
+            issued = x + 1;
+            if (lane < C::kRuns) {
+              const int32_t q = C::kRuns == 2 && lane ? pos[kFind - 1] : pos[0];
+              const int32_t pg = C::kRuns == 2 && lane ? page[kFind - 1] : page[0];
+              tma_load_4d(stage + j * C::kPart + lane * C::kPartPieces * C::kPiece, !LATENT && j ? &maps.v : &maps.k, 0,
+                          s.it.hk * p.page_size + (q & (p.page_size - 1)), LATENT ? j * C::kPartPieces : 0,
+                          q < 0 ? static_cast<int32_t>(p.num_pages) : pg, smem_u32(&ctl.kfull[st][j]));  // past the cache: zeros
+            }
+          } else if (boxes) {
+            if (lane == 0) mbar_arrive(smem_u32(&ctl.kfull[st][j]));
+          } else {
+            const uint16_t* cache = !LATENT && j ? p.v : p.k + (LATENT ? j * C::kPartPieces * 64 : 0);
+#pragma unroll
+            for (int n = 0; n < TK / kPass; ++n) {
+              const int key = (n * kPass + key0) & 63, run = n * kPass / 64;
+              const uint32_t dst = stage + j * C::kPart + run * C::kPartPieces * C::kPiece + key * 128 + ((u ^ (key & 7)) << 4);
+              const uint16_t* src = cache + (from[n] < 0 ? 0 : from[n]);
+#pragma unroll
+              for (int c = 0; c < C::kPartPieces; ++c) cp_async_16_or_zero(dst + c * C::kPiece, src + c * 64, from[n] >= 0);
+            }
+            cp_async_commit();
+          }
+        }
+        // look ahead while the loads are under way
+#pragma unroll
+        for (int n = 0; n < kFind; ++n) {
+          now[n] = next[n];
+          page[n] = entry(now[n]);
+          next[n] = find(i + 2 * C::kTeams, n);
+        }
+        if (!boxes) {
+#pragma unroll
+          for (int j = 0; j < C::kParts; ++j) {
+            if (C::kParts - 1 - j == 2) cp_async_wait_group<2>();
+            else if (C::kParts - 1 - j == 1) cp_async_wait_group<1>();
+            else cp_async_wait_group<0>();
+            fence_proxy_async_smem();  // the products read the copies through the async proxy
+            __syncwarp();
+            queries_landed();
+            if (lane == 0) mbar_arrive(smem_u32(&ctl.kfull[st][j]));
+          }
+        } else if (!q_landed) {
+          cp_async_wait_group<0>();
+          fence_proxy_async_smem();
+          __syncwarp();
+          queries_landed();
+        }
       }
+      if (!q_landed) {  // no tile of this segment was the team's
+        cp_async_wait_group<0>();
+        fence_proxy_async_smem();
+        __syncwarp();
+        queries_landed();
+      }
+      g += s.hi - s.lo;
       ++seg;
     });
-    cp_async_wait_all();  // this thread's copies land before it exits
+    // after a time-out: this warp's copies land before the CTA can exit
+    cp_async_wait_all();
+    if (!ok && lane == 0 && issued > 0) {
+      int never = 0;
+      for (int j = 0; j < C::kParts; ++j)
+        mbar_wait(smem_u32(&ctl.kfull[(issued - 1) % C::kStages][j]), ((issued - 1) / C::kStages) & 1, &never, p.err);
+    }
+    __syncwarp();
   } else if (warp == kMmaWarp) {
     // ================================================================ MMA issuer
     // The whole warp runs this loop; one elected lane issues.
     uint32_t g = 0, seg = 0;
     bool ok = true;
     const uint32_t tm = uniform(tmem);
-    const uint32_t qk_idesc = uniform(idesc_f16(64, TK, DTYPE == FP4IDX_BF16, false, p.negate != 0));
+    const uint32_t qk_idesc = uniform(idesc_f16(64, 64, DTYPE == FP4IDX_BF16, false, p.negate != 0));
     const uint64_t q_desc = desc_sw128(base + C::kOff_Q, 16), p_desc = desc_sw128(base + C::kOff_P, 16);
-    auto ready = [&](uint64_t* bar, uint32_t parity) {
+    const auto done = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_test_wait(smem_u32(bar), parity));
     };
     for_segments<TK>(p, ctl.plan, member, [&](const Segment& s) {
@@ -413,46 +538,66 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       const uint32_t n = uniform(s.hi - s.lo);
       uint32_t qk = 0, pv = 0, spins = 0;
       uint64_t t0 = 0;
-      ok = warp_wait(smem_u32(&ctl.qfull), seg & 1, abort_flag, p.err);
+      ok = warp_try(smem_u32(&ctl.qfull), seg & 1, abort_flag, p.err);
       while (ok && pv < n) {
-        bool moved = false;
-        if (qk < n && qk - pv < 2) {
-          const uint32_t x = g + qk, st = uniform(x % C::kStages), buf = x & 1;
-          if (ready(&ctl.kfull[st], (x / C::kStages) & 1) && ready(&ctl.sempty[buf], ((x >> 1) & 1) ^ 1)) {
-            tc_fence_after();
-            fence_proxy_async_smem();  // the copies were written by cp.async (generic proxy)
-            const uint64_t k_desc = desc_sw128(base + st * C::kStage, 16);
-            const uint32_t d = tm + s_col + buf * TK;
-#pragma unroll
-            for (int c = 0; c < C::kKc; ++c)
-#pragma unroll
-              for (int k = 0; k < 4; ++k)  // descriptor addresses count 16 bytes
-                tc_mma_f16(d, q_desc + c * (kChunkRows * 8) + k * 2, k_desc + c * (C::kPiece >> 4) + k * 2, qk_idesc,
-                           (c | k) != 0);
-            tc_commit_elected(smem_u32(&ctl.sfull[buf]));
-            if (++qk == n) tc_commit_elected(smem_u32(&ctl.qempty));
-            moved = true;
-          }
+        // what can be issued: 1 the next score product (its first part is there), 2 the oldest value product
+        int act = 0;
+        {
+          const uint32_t x = g + qk, y = g + pv;
+          if (pv < qk && done(&ctl.pfull, y & 1) && (pv > 0 || done(&ctl.oempty, (seg & 1) ^ 1)) &&
+              (LATENT || done(&ctl.kfull[y % C::kStages][1], (y / C::kStages) & 1)))
+            act = 2;
+          else if (qk < n && qk - pv < 2 && done(&ctl.kfull[x % C::kStages][0], (x / C::kStages) & 1) &&
+                   done(&ctl.sempty[x & 1], ((x >> 1) & 1) ^ 1))
+            act = 1;
         }
-        if (!moved && pv < qk) {
+        if (act == 1) {
+          const uint32_t x = g + qk, st = uniform(x % C::kStages), buf = x & 1;
+          tc_fence_after();
+          const uint32_t d = tm + s_col + buf * TK;
+          const uint64_t k_desc = desc_sw128(base + st * C::kStage, 16);
+#pragma unroll
+          for (int j = 0; j < (LATENT ? C::kParts : 1); ++j) {
+            if (j > 0) {  // the other parts follow at once
+              ok = warp_try(smem_u32(&ctl.kfull[st][j]), (x / C::kStages) & 1, abort_flag, p.err);
+              if (!ok) break;
+              tc_fence_after();
+            }
+#pragma unroll
+            for (int r = 0; r < C::kRuns; ++r)
+#pragma unroll
+              for (int c = 0; c < C::kPartPieces; ++c)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)  // descriptor addresses count 16 bytes
+                  tc_mma_f16(d + r * 64, q_desc + (j * C::kPartPieces + c) * (kChunkRows * 8) + k * 2,
+                             k_desc + (j * C::kPart >> 4) + (r * C::kPartPieces + c) * (C::kPiece >> 4) + k * 2, qk_idesc,
+                             j + c + k > 0);
+          }
+          if constexpr (!LATENT) tc_commit_elected(smem_u32(&ctl.kempty[st][0]));  // the keys' last reader
+          tc_commit_elected(smem_u32(&ctl.sfull[buf]));
+          if (++qk == n) tc_commit_elected(smem_u32(&ctl.qempty));
+        }
+        if (act == 2) {
           const uint32_t x = g + pv, st = uniform(x % C::kStages);
-          if (ready(&ctl.pfull, x & 1) && (pv > 0 || ready(&ctl.oempty, (seg & 1) ^ 1))) {
+          {
             tc_fence_after();
             const uint64_t v_desc = desc_sw128(base + st * C::kStage + C::kV, C::kPiece);
             const uint32_t more = pv > 0;
 #pragma unroll
-            for (int d = 0; d < C::kDv / 128; ++d)
+            for (int d = 0; d < C::kDv / 128; ++d) {
 #pragma unroll
               for (int k = 0; k < TK / 16; ++k)
-                tc_mma_f16(tm + d * kChunkRows, v_desc + d * (2 * C::kPiece >> 4) + k * 128,
+                tc_mma_f16(tm + d * kChunkRows, v_desc + (d * 2 + (k >> 2) * C::kPartPieces) * (C::kPiece >> 4) + (k & 3) * 128,
                            p_desc + (k >> 2) * (kChunkRows * 8) + (k & 3) * 2, pv_idesc, k > 0 ? 1u : more);
-            tc_commit_elected(smem_u32(&ctl.kempty[st]));
+              // 128 values are pieces 2d and 2d+1; part j of a latent tile is pieces 3j .. 3j+2
+              if (LATENT && d > 0) tc_commit_elected(smem_u32(&ctl.kempty[st][d - 1]));
+            }
+            if constexpr (!LATENT) tc_commit_elected(smem_u32(&ctl.kempty[st][1]));
             tc_commit_elected(smem_u32(&ctl.pvdone));
             ++pv;
-            moved = true;
           }
         }
-        if (moved) {
+        if (act != 0) {
           spins = 0;
         } else if ((++spins & 1023u) == 0) {  // every wait ends
           if (spins == 1024u) t0 = globaltimer();
@@ -503,11 +648,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         bool raise = false;
         float f[2] = {1.0f, 1.0f};
         if (active) {
-          if (ok) ok = warp_wait(smem_u32(&ctl.sfull[buf]), (g >> 1) & 1, abort_flag, p.err);
-          if (ok) ok = warp_wait(smem_u32(&ctl.kfull[st]), (g / C::kStages) & 1, abort_flag, p.err);
+          if (ok) ok = warp_try(smem_u32(&ctl.sfull[buf]), (g >> 1) & 1, abort_flag, p.err);
+          if (ok) ok = warp_try(smem_u32(&ctl.kfull[st][C::kPosPart]), (g / C::kStages) & 1, abort_flag, p.err);
           tc_fence_after();
-          static_assert(kLoadWarps == 8, "holes of a stage are read as one word");
-          const bool mask = i >= full_tiles || *reinterpret_cast<const uint64_t*>(ctl.holes[st]) != 0;
+          static_assert(kTeamWarps == 4, "holes of a stage are read as one word");
+          const bool mask = i >= full_tiles || *reinterpret_cast<const uint32_t*>(ctl.holes[st]) != 0;
 #pragma unroll
           for (int c = 0; c < TK / 64; ++c) {
             uint32_t r[32];
@@ -571,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           }
         }
         // the previous product has read P and updated O^T
-        if (ok && g > 0) ok = warp_wait(smem_u32(&ctl.pvdone), (g - 1) & 1, abort_flag, p.err);
+        if (ok && g > 0) ok = warp_try(smem_u32(&ctl.pvdone), (g - 1) & 1, abort_flag, p.err);
         if (active) {
           uint8_t* prow = smem + C::kOff_P + r0 * 128 + (lane & 3) * 4;
 #pragma unroll
@@ -632,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           }
         }
       }
-      if (ok) ok = warp_wait(smem_u32(&ctl.pvdone), (g - 1) & 1, abort_flag, p.err);
+      if (ok) ok = warp_try(smem_u32(&ctl.pvdone), (g - 1) & 1, abort_flag, p.err);
       bar_sync(2, 32 * kSoftmaxWarps);
       tc_fence_after();
 #pragma unroll 1
@@ -769,14 +914,14 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 }
 
 template <int DTYPE, bool LATENT>
-cudaError_t launch(const AttnParams& p, cudaStream_t stream) {
+cudaError_t launch(const AttnParams& p, const AttnMaps& maps, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(attention_kernel<DTYPE, LATENT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        smem_bytes<LATENT>());
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3(static_cast<unsigned>(p.groups * p.members));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Cfg<LATENT>::kThreads);
   cfg.dynamicSmemBytes = smem_bytes<LATENT>();
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -784,7 +929,7 @@ cudaError_t launch(const AttnParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, attention_kernel<DTYPE, LATENT>, p)) != cudaSuccess) return e;
+  if ((e = cudaLaunchKernelEx(&cfg, attention_kernel<DTYPE, LATENT>, p, maps)) != cudaSuccess) return e;
   if (p.groups < 2) return cudaSuccess;
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
@@ -830,7 +975,7 @@ size_t attention_workspace(const AttnParams& p) {
   return static_cast<size_t>(round16(p.groups * 4 * 8) + round16(rows * 8) + rows * dv * 4);
 }
 
-cudaError_t launch_attention(AttnParams p, int dtype, void* workspace, cudaStream_t stream) {
+cudaError_t launch_attention(AttnParams p, const AttnMaps& maps, int dtype, void* workspace, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(p.groups) * 2 * p.members * kChunkRows;
   char* w = static_cast<char*>(workspace);
   p.info = reinterpret_cast<int64_t*>(w);
@@ -840,8 +985,8 @@ cudaError_t launch_attention(AttnParams p, int dtype, void* workspace, cudaStrea
   p.partial = reinterpret_cast<float*>(w);
   const bool latent = p.v == nullptr;
   if (dtype == FP4IDX_BF16)
-    return latent ? launch<FP4IDX_BF16, true>(p, stream) : launch<FP4IDX_BF16, false>(p, stream);
-  return latent ? launch<FP4IDX_FP16, true>(p, stream) : launch<FP4IDX_FP16, false>(p, stream);
+    return latent ? launch<FP4IDX_BF16, true>(p, maps, stream) : launch<FP4IDX_BF16, false>(p, maps, stream);
+  return latent ? launch<FP4IDX_FP16, true>(p, maps, stream) : launch<FP4IDX_FP16, false>(p, maps, stream);
 }
 
 }  // namespace fp4idx

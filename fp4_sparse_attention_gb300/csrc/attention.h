@@ -2,6 +2,7 @@
 // (api_attention.cu) and its kernels.  Not part of the public ABI.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -55,6 +56,13 @@ struct AttnParams {
   float* partial;       // [groups][2][members][64][dv]: its unnormalised output
 };
 
+// 128-byte-swizzled tensor maps {64 values, (K/V head, offset), piece of 64
+// values, page}: boxes of 64 keys of one page and kBoxPieces pieces.
+struct AttnMaps {
+  CUtensorMap k, v;
+};
+constexpr int kLatentBoxPieces = 3, kPagedBoxPieces = 2;
+
 constexpr int kChunkRows = 64;  // query rows ((row, head) pairs) of one CTA
 
 // Rows copied into a paged cache by slot: up to two sources, each a run of
@@ -97,11 +105,15 @@ struct TablesParams {
 
 // SM count and error word of the current device (api.cu).
 fp4idx_status_t call_device(int* sms, uint32_t** err);
+// Tensor map of 16-bit elements, innermost box of 64 (128 bytes, 128-byte
+// swizzle), zeros outside (api.cu).  strides in bytes.
+fp4idx_status_t call_tensor_map16(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
+                                  const cuuint64_t* strides, const cuuint32_t* box);
 
 // Fills the work split of p; false if it does not fit the counters.
 bool plan_attention(AttnParams* p, int sms);
 size_t attention_workspace(const AttnParams& p);
-cudaError_t launch_attention(AttnParams p, int dtype, void* workspace, cudaStream_t stream);
+cudaError_t launch_attention(AttnParams p, const AttnMaps& maps, int dtype, void* workspace, cudaStream_t stream);
 cudaError_t launch_store_rows(const StoreRowsParams& p, cudaStream_t stream);
 cudaError_t launch_tables(TablesParams p, int sms, cudaStream_t stream);
 

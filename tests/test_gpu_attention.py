@@ -213,12 +213,28 @@ def test_strided_tensors_and_flat_tables(kv):
     assert bool((out[:, H] == 0).all())  # nothing past the call's heads is written
 
 
+@pytest.mark.parametrize("select", [0, 100])
+@pytest.mark.parametrize("gap", [576, 8])
+def test_latent_pages_any_distance_apart(gap, select):
+    # pages a whole number of rows apart, or not (selected rows cannot be gathered by row number then)
+    c = R.make_case(25, [2, 1], [400, 200], heads=8, select=select, device="cuda")
+    P, page, dk = c["k"].shape
+    wide = torch.full((P, page * dk + gap), math.nan, dtype=BF16, device="cuda")
+    wide[:, :page * dk] = c["k"].reshape(P, -1)
+    check(c, call(build(c, k=wide.as_strided((P, page, dk), (page * dk + gap, dk, 1)))))
+
+
 def test_cache_beyond_two_to_the_31_elements():
     # 64-bit offsets: the pages used lie at both ends of a cache of more than 2^31 elements
     free = torch.cuda.mem_get_info()[0]
     if free < 12 << 30:
         pytest.skip("needs 12 GB")
-    c = R.make_case(20, [2], [300], heads=8, device="cuda")
+    for select in (0, 100):
+        far_pages(select)
+
+
+def far_pages(select):
+    c = R.make_case(20, [2], [300], heads=8, select=select, device="cuda")
     big = torch.empty((2 ** 31 // (64 * 576) + 40, 64, 576), dtype=BF16, device="cuda")
     move = {p: (i if i % 2 else big.shape[0] - 1 - i) for i, p in enumerate(c["pages"][0])}
     for p, to in move.items():
