@@ -148,6 +148,8 @@ class Fp4idxError(RuntimeError):
 def load_library(path: str = LIB_PATH):
     """Load libfp4idx.so and declare its signatures (raises if it is missing)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -218,10 +220,18 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+# The current device and its current stream's handle without building a
+# torch.cuda.Stream (3 us a call on Grace, more than a kernel launch).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None or _raw_device is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(_raw_device())
 
 
 class DeviceProblem:
@@ -515,6 +525,9 @@ def fp4idx_topk_merge(problem: DeviceProblem, k: int, indices: torch.Tensor, val
            "fp4idx_topk_merge")
 
 
+_HALF = (torch.bfloat16, torch.float16)
+
+
 class DeviceAttention:
     """Device tensors of one attention call plus its fp4idx_attention_t.
 
@@ -531,7 +544,7 @@ class DeviceAttention:
                  scale: float, v=None, page_offsets=None, visible_len=None, causal: bool = False, qo_offset=None,
                  indices=None, out=None, lse=None, workspace=None):
         latent = v is None
-        if q.dtype not in (torch.bfloat16, torch.float16) or k.dtype != q.dtype or (v is not None and v.dtype != q.dtype):
+        if q.dtype not in _HALF or k.dtype != q.dtype or (v is not None and v.dtype != q.dtype):
             raise ValueError("q and the caches must all be bfloat16 or all float16")
         dk, dv = (576, 512) if latent else (128, 128)
         if q.dim() != 3 or q.shape[2] != dk or q.stride(2) != 1:
@@ -587,58 +600,68 @@ class DeviceAttention:
         if workspace is None:
             workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=q.device)
         self.workspace = workspace
-        self._ws = (ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size())
+        self._ws = (workspace.data_ptr(), workspace.numel() * workspace.element_size())
 
 
 def fp4idx_latent_attention(attention: DeviceAttention, stream=None):
     """Absorbed latent attention of every row over its visible or selected keys: (out [T, H, 512], lse [T, H])."""
-    _check(load_library().fp4idx_latent_attention(attention._ref, *attention._ws, _stream(stream)),
-           "fp4idx_latent_attention")
+    ws, size = attention._ws
+    status = load_library().fp4idx_latent_attention(attention._ref, ws, size, _stream(stream))
+    if status:
+        _check(status, "fp4idx_latent_attention")
     return attention.out, attention.lse
 
 
 def fp4idx_paged_attention(attention: DeviceAttention, stream=None):
     """Grouped-query attention of every row over its visible keys or selected blocks: (out [T, H, 128], lse [T, H])."""
-    _check(load_library().fp4idx_paged_attention(attention._ref, *attention._ws, _stream(stream)),
-           "fp4idx_paged_attention")
+    ws, size = attention._ws
+    status = load_library().fp4idx_paged_attention(attention._ref, ws, size, _stream(stream))
+    if status:
+        _check(status, "fp4idx_paged_attention")
     return attention.out, attention.lse
 
 
 def fp4idx_store_latent(latent: torch.Tensor, rope: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor,
                         stream=None) -> None:
     """Write latent [N, 512] and rope [N, 64] into the latent cache [P, page, 576] at token slots [N] int32."""
-    if latent.dtype not in (torch.bfloat16, torch.float16) or rope.dtype != latent.dtype or cache.dtype != latent.dtype:
+    dtype = latent.dtype
+    if dtype not in _HALF or rope.dtype != dtype or cache.dtype != dtype:
         raise ValueError("latent, rope and cache must all be bfloat16 or all float16")
     N = latent.shape[0]
-    if tuple(latent.shape) != (N, 512) or tuple(rope.shape) != (N, 64) or latent.stride(1) != 1 or rope.stride(1) != 1:
+    (ls, l1), (rs, r1) = latent.stride(), rope.stride()
+    if latent.shape != (N, 512) or rope.shape != (N, 64) or l1 != 1 or r1 != 1:
         raise ValueError("latent must be [N, 512] and rope [N, 64] with dense rows")
     if slots.dtype != torch.int32 or slots.numel() != N or not slots.is_contiguous():
         raise ValueError("slots must be a contiguous [N] int32 tensor")
-    if cache.dim() != 3 or cache.shape[2] != 576 or cache.stride(2) != 1 or cache.stride(1) != 576:
+    if cache.dim() != 3 or cache.shape[2] != 576 or cache.stride()[1:] != (576, 1):
         raise ValueError("cache must be [P, page, 576], dense inside a page")
-    _check(load_library().fp4idx_store_latent(latent.data_ptr(), latent.stride(0), rope.data_ptr(), rope.stride(0),
-                                              slots.data_ptr(), N, cache.shape[1], cache.shape[0], cache.stride(0),
-                                              cache.data_ptr(), _stream(stream)), "fp4idx_store_latent")
+    status = load_library().fp4idx_store_latent(latent.data_ptr(), ls, rope.data_ptr(), rs, slots.data_ptr(), N,
+                                                cache.shape[1], cache.shape[0], cache.stride(0), cache.data_ptr(),
+                                                _stream(stream))
+    if status:
+        _check(status, "fp4idx_store_latent")
 
 
 def fp4idx_store_kv(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                     stream=None) -> None:
     """Write k_new, v_new [N, Hkv, 128] into the caches k, v [P, Hkv, page, 128] at token slots [N] int32."""
-    if k_new.dtype not in (torch.bfloat16, torch.float16) or any(x.dtype != k_new.dtype for x in (v_new, k, v)):
+    dtype = k_new.dtype
+    if dtype not in _HALF or v_new.dtype != dtype or k.dtype != dtype or v.dtype != dtype:
         raise ValueError("k_new, v_new, k and v must all be bfloat16 or all float16")
     N, Hkv = k_new.shape[0], k_new.shape[1]
-    for x in (k_new, v_new):
-        if tuple(x.shape) != (N, Hkv, 128) or x.stride(2) != 1 or x.stride(1) != 128:
-            raise ValueError("k_new and v_new must be [N, Hkv, 128] with dense heads")
+    if k_new.shape != (N, Hkv, 128) or v_new.shape != (N, Hkv, 128) or k_new.stride()[1:] != (128, 1) \
+            or v_new.stride()[1:] != (128, 1):
+        raise ValueError("k_new and v_new must be [N, Hkv, 128] with dense heads")
     if slots.dtype != torch.int32 or slots.numel() != N or not slots.is_contiguous():
         raise ValueError("slots must be a contiguous [N] int32 tensor")
-    page = k.shape[2]
     if k.dim() != 4 or k.shape[1] != Hkv or k.shape[3] != 128 or k.shape != v.shape or k.stride() != v.stride() \
-            or k.stride()[1:] != (page * 128, 128, 1):
+            or k.stride()[1:] != (k.shape[2] * 128, 128, 1):
         raise ValueError("k and v must be [P, Hkv, page, 128], dense inside a page, with one set of strides")
-    _check(load_library().fp4idx_store_kv(k_new.data_ptr(), k_new.stride(0), v_new.data_ptr(), v_new.stride(0),
-                                          slots.data_ptr(), N, Hkv, page, k.shape[0], k.stride(0), k.data_ptr(),
-                                          v.data_ptr(), _stream(stream)), "fp4idx_store_kv")
+    status = load_library().fp4idx_store_kv(k_new.data_ptr(), k_new.stride(0), v_new.data_ptr(), v_new.stride(0),
+                                            slots.data_ptr(), N, Hkv, k.shape[2], k.shape[0], k.stride(0), k.data_ptr(),
+                                            v.data_ptr(), _stream(stream))
+    if status:
+        _check(status, "fp4idx_store_kv")
 
 
 def fp4idx_build_tables(cached_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.Tensor,
@@ -647,29 +670,36 @@ def fp4idx_build_tables(cached_len: torch.Tensor, new_len: torch.Tensor, block_t
     """Metadata of one step from its request lengths: (cu_seqlens_q [B+1], cu_seqlens_k [B+1], visible_len [T],
     slots [T], pages_taken [1]), int32 on the device; block_table [B, stride] gets its new pages in place from
     free_pages [F].  ``num_pages`` bounds the page ids (default: any); ``out`` may give the five tensors."""
+    i32 = torch.int32
+    if cached_len.dtype != i32 or new_len.dtype != i32 or free_pages.dtype != i32 or block_table.dtype != i32:
+        raise ValueError("cached_len, new_len, block_table and free_pages must be int32")
     B = cached_len.shape[0]
-    for name, x in (("cached_len", cached_len), ("new_len", new_len), ("free_pages", free_pages)):
-        if x.dtype != torch.int32 or x.dim() != 1 or not x.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous 1-D int32 tensor")
-    if new_len.shape[0] != B or block_table.dim() != 2 or block_table.shape[0] != B \
-            or block_table.dtype != torch.int32 or block_table.stride(1) != 1:
-        raise ValueError("new_len must be [B] and block_table [B, stride] int32 with dense rows")
+    if cached_len.stride() != (1,) or new_len.stride() != (1,) or free_pages.stride() != (1,):
+        raise ValueError("cached_len, new_len and free_pages must be contiguous 1-D tensors")
+    if new_len.shape[0] != B or block_table.dim() != 2 or block_table.shape[0] != B or block_table.stride(1) != 1:
+        raise ValueError("new_len must be [B] and block_table [B, stride] with dense rows")
     if out is None:
-        # one allocation; each array starts at a multiple of four entries
-        size = [(n + 3) // 4 * 4 for n in (B + 1, B + 1, num_rows, num_rows, 1)]
-        flat = torch.empty((sum(size),), dtype=torch.int32, device=cached_len.device).split(size)
-        out = (flat[0][:B + 1], flat[1][:B + 1], flat[2][:num_rows], flat[3][:num_rows], flat[4][:1])
-    cu_q, cu_k, visible, slots, taken = out
-    for x, n in ((cu_q, B + 1), (cu_k, B + 1), (visible, num_rows), (slots, num_rows), (taken, 1)):
-        if x.dtype != torch.int32 or x.numel() != n or not x.is_contiguous():
-            raise ValueError("out: cu_seqlens_q [B+1], cu_seqlens_k [B+1], visible_len [T], slots [T], pages_taken [1]")
-    pages = (2 ** 31 - 1) // page_size if num_pages is None and page_size > 0 else num_pages
-    _check(load_library().fp4idx_build_tables(cached_len.data_ptr(), new_len.data_ptr(), B, num_rows, page_size, pages,
-                                              free_pages.data_ptr(), free_pages.shape[0], block_table.data_ptr(),
-                                              block_table.stride(0), cu_q.data_ptr(), cu_k.data_ptr(),
-                                              visible.data_ptr(), slots.data_ptr(), taken.data_ptr(),
-                                              _stream(stream)), "fp4idx_build_tables")
-    return out
+        dev = cached_len.device
+        cu_q = torch.empty((B + 1,), dtype=i32, device=dev)
+        cu_k = torch.empty((B + 1,), dtype=i32, device=dev)
+        visible = torch.empty((num_rows,), dtype=i32, device=dev)
+        slots = torch.empty((num_rows,), dtype=i32, device=dev)
+        taken = torch.empty((1,), dtype=i32, device=dev)
+    else:
+        for x, n in zip(out, (B + 1, B + 1, num_rows, num_rows, 1)):
+            if x.dtype != i32 or x.numel() != n or not x.is_contiguous():
+                raise ValueError("out: cu_seqlens_q [B+1], cu_seqlens_k [B+1], visible_len [T], slots [T], "
+                                 "pages_taken [1]")
+        cu_q, cu_k, visible, slots, taken = out
+    if num_pages is None:
+        num_pages = (2 ** 31 - 1) // page_size if page_size > 0 else 1
+    status = load_library().fp4idx_build_tables(
+        cached_len.data_ptr(), new_len.data_ptr(), B, num_rows, page_size, num_pages, free_pages.data_ptr(),
+        free_pages.shape[0], block_table.data_ptr(), block_table.stride(0), cu_q.data_ptr(), cu_k.data_ptr(),
+        visible.data_ptr(), slots.data_ptr(), taken.data_ptr(), _stream(stream))
+    if status:
+        _check(status, "fp4idx_build_tables")
+    return cu_q, cu_k, visible, slots, taken
 
 
 def fp4idx_get_error(clear: bool = True, stream=None) -> int:

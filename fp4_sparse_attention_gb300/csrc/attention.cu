@@ -45,6 +45,7 @@
 // for different row chunks, close enough in time for the L2 to serve the
 // second reader.  An item cut by a boundary leaves partial sums that
 // join_kernel adds in a fixed order.
+#include <atomic>
 #include <cstring>
 
 #include "attention.h"
@@ -57,6 +58,10 @@ constexpr int kSoftmaxWarps = 4, kMmaWarp = 4;
 constexpr int kTeamWarps = 4, kTeamThreads = 32 * kTeamWarps;  // loader teams take tiles in turn
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxMembers = 8;
+// Pair number / group as (x * ceil(2^40 / group)) >> 40: exact, and inside 64
+// bits, for group <= 1024 and up to 2^20 rows of a request.
+constexpr int kGroupShift = 40;
+constexpr int kMaxRowsOfRequest = 1 << 20;
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 // A row's reference maximum is raised only when the true one is 2^8 above it.
 constexpr float kRaise = 8.0f;
@@ -86,12 +91,35 @@ struct Cfg {
   static constexpr uint32_t kOCols = kDv / 128 * kChunkRows;    // O^T: 64 columns per 128 values
 };
 
+struct Item {
+  int b, hk;
+  int q0;        // first row of the request (or the row of a selection)
+  int rows;      // (row, head) pairs: rows of the request x group
+  int c0;        // first pair of the chunk group
+};
+
+// The part of an item that one CTA computes.
+struct Segment {
+  Item it;
+  int c, rows;       // its pairs [c, c + rows) of the request; none: rows <= 0
+  int max_vis;       // largest visible length among them
+  int lo, hi, tiles; // key tiles [lo, hi) of the item's `tiles`
+};
+
+// A CTA's run of tiles [lo, hi), its first item (which starts at tile
+// `start`) and its first segment, worked out once for all roles.
+struct Run {
+  int64_t lo, hi, start;
+  int item;
+  Segment first;
+};
+
 template <bool LATENT>
 struct Control {
   uint64_t kfull[Cfg<LATENT>::kStages][Cfg<LATENT>::kParts], kempty[Cfg<LATENT>::kStages][Cfg<LATENT>::kParts];
   uint64_t sfull[2], sempty[2], pfull, pvdone, qfull, qempty, oempty, drain;
   int64_t row_off[kChunkRows];                                 // output element of each row
-  int64_t plan[4];                                             // first item, its first tile, lo, hi
+  Run run;
   int32_t key_pos[Cfg<LATENT>::kStages][Cfg<LATENT>::kTk];     // logical position, -1: no key
   alignas(4) uint8_t holes[Cfg<LATENT>::kStages][kTeamWarps];  // a loader warp found a key that does not exist
   float factor[kChunkRows], row_inv[kChunkRows];
@@ -106,18 +134,26 @@ constexpr uint32_t smem_bytes() {
 static_assert(smem_bytes<true>() <= 232448 && smem_bytes<false>() <= 232448, "227 KB per CTA");
 
 // ---------------------------------------------------------------- items
-struct Item {
-  int b, hk;
-  int q0;        // first row of the request (or the row of a selection)
-  int rows;      // (row, head) pairs: rows of the request x group
-  int c0;        // first pair of the chunk group
-};
+// x / group and x % group of a pair number (plan_attention bounds it).
+__device__ __forceinline__ int group_div(const AttnParams& p, int x) {
+  return static_cast<int>((static_cast<uint64_t>(x) * p.group_mul) >> kGroupShift);
+}
+__device__ __forceinline__ int group_mod(const AttnParams& p, int x) { return x - group_div(p, x) * p.group; }
 
 __device__ __forceinline__ Item item_of(const AttnParams& p, int item) {
   Item it;
-  const int cg = item % p.chunk_groups, x = item / p.chunk_groups;
-  it.hk = x % p.num_kv_heads;
-  const int u = x / p.num_kv_heads;
+  int u = item;
+  it.c0 = 0;
+  if (p.chunk_groups > 1) {
+    u = item / p.chunk_groups;
+    it.c0 = (item - u * p.chunk_groups) * p.members * kChunkRows;
+  }
+  it.hk = 0;
+  if (p.num_kv_heads > 1) {
+    const int x = u;
+    u = x / p.num_kv_heads;
+    it.hk = x - u * p.num_kv_heads;
+  }
   if (p.indices) {
     it.q0 = u;
     it.b = attn_request(p, u);
@@ -125,16 +161,16 @@ __device__ __forceinline__ Item item_of(const AttnParams& p, int item) {
   } else {
     it.b = u;
     it.q0 = __ldg(p.cu_seqlens_q + u);
-    it.rows = max(0, min(__ldg(p.cu_seqlens_q + u + 1), p.num_rows) - it.q0) * p.group;
+    const int n = min(__ldg(p.cu_seqlens_q + u + 1), p.num_rows) - it.q0;
+    it.rows = max(0, min(n, p.max_seqlen_q)) * p.group;
   }
-  it.c0 = cg * p.members * kChunkRows;
   return it;
 }
 
 // Largest visible length of the rows that pairs [c, c + n) belong to; called
 // by `step` threads with lane = 0..step-1, each giving its share.
 __device__ __forceinline__ int pairs_max_visible(const AttnParams& p, const Item& it, int c, int n, int lane, int step) {
-  const int first = it.q0 + c / p.group, last = it.q0 + (c + n - 1) / p.group;
+  const int first = it.q0 + group_div(p, c), last = it.q0 + group_div(p, c + n - 1);
   if (!p.visible_len) return attn_visible(p, it.b, last);  // grows with the row
   int v = 0;
   for (int t = first + lane; t <= last; t += step) v = max(v, attn_visible(p, it.b, t));
@@ -153,46 +189,74 @@ __device__ __forceinline__ int item_tiles(const AttnParams& p, const Item& it, i
   return max(1, (v + TK - 1) / TK);
 }
 
+// First tile of a group's run; a 64-bit division takes 200 cycles more.
 __device__ __forceinline__ int64_t run_start(int64_t total, int group, int groups) {
+  if (total < (1 << 22)) return static_cast<uint32_t>(total) * static_cast<uint32_t>(group) / static_cast<uint32_t>(groups);
   return static_cast<int64_t>(static_cast<uint64_t>(total) * group / groups);
 }
 __device__ __forceinline__ int used_groups(const AttnParams& p, int64_t total) {
   return total < p.groups ? static_cast<int>(total) : p.groups;
 }
 
-// The part of an item that one CTA computes.
-struct Segment {
-  Item it;
-  int c, rows;       // its pairs [c, c + rows) of the request
-  int max_vis;       // largest visible length among them
-  int lo, hi, tiles; // key tiles [lo, hi) of the item's `tiles`
+// Segment of the tiles [pos, hi) of the concatenation, of an item of `tiles`
+// tiles that starts at `start`.
+__device__ __forceinline__ Segment segment_of(const AttnParams& p, const Item& it, int tiles, int64_t start, int64_t pos,
+                                              int64_t hi, int member, int lane, int step) {
+  Segment s;
+  s.it = it;
+  s.tiles = tiles;
+  s.c = it.c0 + member * kChunkRows;
+  s.rows = min(kChunkRows, it.rows - s.c);
+  s.lo = static_cast<int>(pos - start);
+  s.hi = static_cast<int>(min(hi, start + tiles) - start);
+  s.max_vis = s.rows > 0 ? pairs_max_visible(p, it, s.c, s.rows, lane, step) : 0;
+  if (step > 1) s.max_vis = __reduce_max_sync(0xffffffffu, s.max_vis);
+  return s;
+}
+
+// What the join needs to know of a group's first item.
+struct GroupInfo {
+  int64_t item, start, tiles, total;  // total: tiles of all items (every group writes it)
+  int64_t q0, rows, c0, hk;
 };
+
+__device__ __forceinline__ void set_run(const AttnParams& p, Run* run, int group, int member, int64_t total, int64_t lo,
+                                        int64_t hi, int item, const Item& it, int64_t start, int tiles) {
+  run->item = item;
+  run->start = start;
+  run->first = segment_of(p, it, tiles, start, lo, hi, member, 0, 1);
+  if (member == 0) {
+    GroupInfo& info = reinterpret_cast<GroupInfo*>(p.info)[group];
+    info.item = item;
+    info.start = start;
+    info.tiles = tiles;
+    info.q0 = it.q0;
+    info.rows = it.rows;
+    info.c0 = it.c0;
+    info.hk = it.hk;
+  }
+}
 
 // Calls f(segment) for every segment of this CTA, in order; whole warps.
 template <int TK, class F>
-__device__ __forceinline__ void for_segments(const AttnParams& p, const int64_t* plan, int member, F&& f) {
+__device__ __forceinline__ void for_segments(const AttnParams& p, const Run& run, int member, F&& f) {
   const int lane = threadIdx.x & 31;
-  int item = static_cast<int>(plan[0]);
-  int64_t start = plan[1], pos = plan[2];
-  const int64_t hi = plan[3];
-  while (pos < hi) {
-    Segment s;
-    s.it = item_of(p, item);
-    s.tiles = item_tiles<TK>(p, s.it, lane, 32);
-    const int64_t end = min(hi, start + s.tiles);
-    if (end > pos) {
-      s.c = s.it.c0 + member * kChunkRows;
-      s.rows = min(kChunkRows, s.it.rows - s.c);
-      s.lo = static_cast<int>(pos - start);
-      s.hi = static_cast<int>(end - start);
-      if (s.rows > 0) {
-        s.max_vis = __reduce_max_sync(0xffffffffu, pairs_max_visible(p, s.it, s.c, s.rows, lane, 32));
-        f(s);
-      }
-      pos = end;
-    }
+  const int64_t hi = run.hi;
+  if (run.lo >= hi) return;
+  Segment s = run.first;
+  int item = run.item;
+  int64_t start = run.start;
+  for (;;) {
+    if (s.rows > 0) f(s);
     start += s.tiles;
-    ++item;
+    if (start >= hi) return;
+    Item it;
+    int tiles;
+    do {  // an item without rows has no tiles
+      it = item_of(p, ++item);
+      tiles = item_tiles<TK>(p, it, lane, 32);
+    } while (tiles == 0);
+    s = segment_of(p, it, tiles, start, start, hi, member, lane, 32);
   }
 }
 
@@ -224,7 +288,7 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
 
   if (base & 1023u) {  // the swizzled layouts need it; the runtime places the window there
     if (tid == 0) {
-      p.info[3] = 0;
+      reinterpret_cast<GroupInfo*>(p.info)->total = 0;
       atomicOr(p.err, kErrTimeout);
     }
     return;
@@ -258,18 +322,16 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
     if (tid == 0) {
       const int64_t total = static_cast<int64_t>(p.items) * p.list_tiles;
       const int used = used_groups(p, total);
-      const int64_t lo = group < used ? run_start(total, group, used) : total;
-      const int64_t item = group < used ? lo / p.list_tiles : 0;
-      ctl.plan[0] = item;
-      ctl.plan[1] = item * p.list_tiles;
-      ctl.plan[2] = lo;
-      ctl.plan[3] = group < used ? run_start(total, group + 1, used) : total;
-      if (member == 0) {
-        int64_t* info = p.info + 4 * group;
-        info[0] = item;
-        info[1] = item * p.list_tiles;
-        info[2] = p.list_tiles;
-        info[3] = total;
+      const bool work = group < used;
+      const int64_t lo = work ? run_start(total, group, used) : 0, hi = work ? run_start(total, group + 1, used) : 0;
+      ctl.run.lo = lo;
+      ctl.run.hi = hi;
+      if (member == 0) reinterpret_cast<GroupInfo*>(p.info)[group].total = total;
+      if (work) {
+        const int item = static_cast<int>(static_cast<uint32_t>(lo >> 32) == 0 ? static_cast<uint32_t>(lo) / static_cast<uint32_t>(p.list_tiles)
+                                                                             : lo / p.list_tiles);
+        set_run(p, &ctl.run, group, member, total, lo, hi, item, item_of(p, item), static_cast<int64_t>(item) * p.list_tiles,
+                p.list_tiles);
       }
     }
   } else {
@@ -279,7 +341,13 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
     const int per = (p.items + C::kThreads - 1) / C::kThreads;
     const int first = min(p.items, tid * per), last = min(p.items, first + per);
     int64_t mine = 0;
-    for (int i = first; i < last; ++i) mine += item_tiles<TK>(p, item_of(p, i), 0, 1);
+    Item it = {};
+    int tiles = 0;
+    for (int i = first; i < last; ++i) {
+      it = item_of(p, i);
+      tiles = item_tiles<TK>(p, it, 0, 1);
+      mine += tiles;
+    }
     int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -289,39 +357,41 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
     if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
     int64_t before = incl - mine, total = 0;
+#pragma unroll
     for (int w = 0; w < C::kThreads / 32; ++w) {
-      before += w < warp ? warp_sum[w] : 0;
-      total += warp_sum[w];
+      const int64_t v = warp_sum[w];
+      before += w < warp ? v : 0;
+      total += v;
     }
     const int used = used_groups(p, total);
-    const int64_t lo = group < used ? run_start(total, group, used) : total;
+    const bool work = group < used;
+    const int64_t lo = work ? run_start(total, group, used) : 0, hi = work ? run_start(total, group + 1, used) : 0;
     if (tid == 0) {
-      ctl.plan[2] = lo;
-      ctl.plan[3] = group < used ? run_start(total, group + 1, used) : total;
-      if (member == 0) p.info[4 * group + 3] = total;
+      ctl.run.lo = lo;
+      ctl.run.hi = hi;
+      if (member == 0) reinterpret_cast<GroupInfo*>(p.info)[group].total = total;
     }
-    if (group < used && before <= lo && lo < before + mine) {
-      int i = first;
-      int n = item_tiles<TK>(p, item_of(p, i), 0, 1);
-      while (before + n <= lo) {
-        before += n;
-        ++i;
-        n = item_tiles<TK>(p, item_of(p, i), 0, 1);
+    if (work && before <= lo && lo < before + mine) {
+      int i = last - 1;
+      if (per > 1) {  // walk this thread's items again
+        i = first - 1;
+        int64_t at = before;
+        tiles = 0;
+        do {
+          before = at;
+          it = item_of(p, ++i);
+          tiles = item_tiles<TK>(p, it, 0, 1);
+          at += tiles;
+        } while (at <= lo);
       }
-      ctl.plan[0] = i;
-      ctl.plan[1] = before;
-      if (member == 0) {
-        int64_t* info = p.info + 4 * group;
-        info[0] = i;
-        info[1] = before;
-        info[2] = n;
-      }
+      set_run(p, &ctl.run, group, member, total, lo, hi, i, it, before, tiles);
     }
   }
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl.tmem;
   const uint32_t s_col = C::kOCols;  // two score buffers behind O^T
+  pdl_launch_dependents();           // the join may take its place; it waits for this grid's end
 
   if (warp >= kMmaWarp + 1) {
     // ================================================================ loaders
@@ -335,7 +405,7 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
     uint32_t g = 0, seg = 0;                                // tiles and segments before this one
     uint32_t issued = 0;                                    // this team's last tile, counted from 1
     bool ok = true;
-    for_segments<TK>(p, ctl.plan, member, [&](const Segment& s) {
+    for_segments<TK>(p, ctl.run, member, [&](const Segment& s) {
       if (!ok) return;
       const int64_t table = attn_table_base(p, s.it.b);
       const int32_t* list = nullptr;
@@ -378,7 +448,7 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
 #pragma unroll 1
       for (int r = team * kPass + key0; r < kChunkRows; r += C::kTeams * kPass) {
         const bool have = r < s.rows;
-        const int x = s.c + (have ? r : 0), t = s.it.q0 + x / p.group, h = s.it.hk * p.group + x % p.group;
+        const int x = s.c + (have ? r : 0), t = s.it.q0 + group_div(p, x), h = s.it.hk * p.group + group_mod(p, x);
         const uint16_t* src = p.q + t * p.q_row_stride + h * p.q_head_stride + u * 8;
         const uint32_t dst = base + C::kOff_Q + r * 128 + ((u ^ (r & 7)) << 4);
 #pragma unroll
@@ -532,7 +602,7 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
     const auto done = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_test_wait(smem_u32(bar), parity));
     };
-    for_segments<TK>(p, ctl.plan, member, [&](const Segment& s) {
+    for_segments<TK>(p, ctl.run, member, [&](const Segment& s) {
       if (!ok) return;
       const uint32_t pv_idesc = uniform(idesc_f16(128, (s.rows + 15) & ~15, DTYPE == FP4IDX_BF16, true, false));
       const uint32_t n = uniform(s.hi - s.lo);
@@ -628,13 +698,13 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
     bool ok = true;
     const int r0 = 16 * warp + (lane >> 2);                 // this thread's rows: r0 and r0 + 8
     const uint32_t quarter = static_cast<uint32_t>(warp) << 21;  // TMEM lanes 32 * warp
-    for_segments<TK>(p, ctl.plan, member, [&](const Segment& s) {
+    for_segments<TK>(p, ctl.run, member, [&](const Segment& s) {
       // rows past the chunk's end have zero queries: their scores are harmless
       int vis[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = r0 + 8 * i;
-        vis[i] = r < s.rows ? attn_visible(p, s.it.b, s.it.q0 + (s.c + r) / p.group) : INT32_MAX;
+        vis[i] = r < s.rows ? attn_visible(p, s.it.b, s.it.q0 + group_div(p, s.c + r)) : INT32_MAX;
       }
       // tiles that all of the warp's rows see whole (a selection's keys are all visible or holes)
       const int full_tiles = p.indices ? INT32_MAX : __reduce_min_sync(0xffffffffu, min(vis[0], vis[1])) / TK;
@@ -766,7 +836,7 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int r = r0 + 8 * e;
-          const int t = s.it.q0 + (s.c + r) / p.group, h = s.it.hk * p.group + (s.c + r) % p.group;
+          const int t = s.it.q0 + group_div(p, s.c + r), h = s.it.hk * p.group + group_mod(p, s.c + r);
           ctl.row_inv[r] = sum[e] == 0.0f ? 0.0f : 1.0f / sum[e];
           ctl.row_off[r] = t * p.out_row_stride + static_cast<int64_t>(h) * C::kDv;
           if (r < s.rows && ok) {
@@ -814,7 +884,6 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
     tc_fence_before();
   }
   __syncthreads();
-  pdl_launch_dependents();
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc<kTmemCols>(tmem);
@@ -834,90 +903,107 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   using C = Cfg<LATENT>;
   constexpr int kVec = C::kDv / 128;  // float4s per lane
   __shared__ float4 sum[BY_ITEM ? kJoinWarps : 1][C::kDv / 4];
-  __shared__ float part_l[kJoinWarps];
+  __shared__ float2 part[kJoinWarps];
+  __shared__ int64_t total_tiles;
   __shared__ int first_group;
+  __shared__ GroupInfo shared_info;
   pdl_wait();
   pdl_launch_dependents();
   const int tid = threadIdx.x, member = blockIdx.y, warp = tid >> 5, lane = tid & 31;
-  const int64_t total = p.info[3];
-  const int used = used_groups(p, total);
-  // the groups whose run begins inside the item: consecutive ones
-  const int item = BY_ITEM ? blockIdx.x : static_cast<int>(blockIdx.x) + 1 < used ? static_cast<int>(p.info[4 * (blockIdx.x + 1)]) : -1;
-  const bool inside = tid > 0 && tid < used && p.info[4 * tid] == item && p.info[4 * tid + 1] < run_start(total, tid, used);
-  if (tid == 0) first_group = INT32_MAX;
-  const int parts = 1 + __syncthreads_count(inside);
-  if (inside) atomicMin(&first_group, tid);
+  // one group per thread (plan_attention); groups without work hold nothing but the total
+  const GroupInfo* infos = reinterpret_cast<const GroupInfo*>(p.info);
+  GroupInfo info = {};
+  if (tid < p.groups) info = infos[tid];
+  const int64_t candidate = BY_ITEM ? blockIdx.x : infos[blockIdx.x + 1].item;
+  if (tid == 0) {
+    total_tiles = info.total;
+    first_group = INT32_MAX;
+  }
   __syncthreads();
+  const int used = used_groups(p, total_tiles);
+  // the groups whose run begins inside the item: consecutive ones
+  const bool inside = tid > 0 && tid < used && info.item == candidate && info.start < run_start(total_tiles, tid, used);
+  if (inside) atomicMin(&first_group, tid);
+  const int parts = 1 + __syncthreads_count(inside);
   const int group = first_group;  // the first boundary; the part before it is the previous group's
   if (parts == 1 || (!BY_ITEM && group != static_cast<int>(blockIdx.x) + 1)) return;
-  const Item it = item_of(p, item);
-  const int c = it.c0 + member * kChunkRows;
+  if (tid == group) shared_info = info;
+  __syncthreads();
+  const int c = static_cast<int>(shared_info.c0) + member * kChunkRows;
   const int r = BY_ITEM ? blockIdx.z : blockIdx.z * kJoinWarps + warp;
-  const bool have = r < min(kChunkRows, it.rows - c);
-  if (BY_ITEM && !have) return;
-  if (have) {
-    // part i: group - 1 + i; the first one is its group's last segment, the others their groups' first
-    const auto row_of = [&](int i) {
-      return ((static_cast<int64_t>(group - 1 + i) * 2 + (i == 0)) * p.members + member) * kChunkRows + r;
-    };
-    float M = -INFINITY;
-    for (int i = lane; i < parts; i += 32) M = fmaxf(M, p.stats[row_of(i)].x);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float ref = M == -INFINITY ? 0.0f : M;
-    float4 acc[kVec] = {};
-    float l = 0.0f;
+  if (r >= min(kChunkRows, static_cast<int>(shared_info.rows) - c)) return;  // (BY_ITEM: the whole CTA)
+  // this warp's partials, each added relative to the largest maximum so far
+  float4 acc[kVec] = {};
+  float m = -INFINITY, l = 0.0f;
 #pragma unroll 4
-    for (int i = BY_ITEM ? warp : 0; i < parts; i += BY_ITEM ? kJoinWarps : 1) {
-      const int64_t row = row_of(i);
-      const float2 s = p.stats[row];
-      const float w = ex2(s.x - ref);
-      l = fmaf(w, s.y, l);
+  for (int i = BY_ITEM ? warp : 0; i < parts; i += BY_ITEM ? kJoinWarps : 1) {
+    // part i is group - 1 + i; the first one is its group's last segment, the others their groups' first
+    const int64_t row = ((static_cast<int64_t>(group - 1 + i) * 2 + (i == 0)) * p.members + member) * kChunkRows + r;
+    const float2 s = p.stats[row];
+    float4 o[kVec];
 #pragma unroll
-      for (int v = 0; v < kVec; ++v) {
-        const float4 o = reinterpret_cast<const float4*>(p.partial + row * C::kDv)[v * 32 + lane];
-        acc[v].x = fmaf(w, o.x, acc[v].x);
-        acc[v].y = fmaf(w, o.y, acc[v].y);
-        acc[v].z = fmaf(w, o.z, acc[v].z);
-        acc[v].w = fmaf(w, o.w, acc[v].w);
-      }
+    for (int v = 0; v < kVec; ++v) o[v] = reinterpret_cast<const float4*>(p.partial + row * C::kDv)[v * 32 + lane];
+    const float top = fmaxf(m, s.x), ref = top == -INFINITY ? 0.0f : top;
+    const float keep = ex2(m - ref), w = ex2(s.x - ref);
+    m = top;
+    l = l * keep + w * s.y;
+#pragma unroll
+    for (int v = 0; v < kVec; ++v) {
+      acc[v].x = acc[v].x * keep + w * o[v].x;
+      acc[v].y = acc[v].y * keep + w * o[v].y;
+      acc[v].z = acc[v].z * keep + w * o[v].z;
+      acc[v].w = acc[v].w * keep + w * o[v].w;
     }
-    if constexpr (BY_ITEM) {
-#pragma unroll
-      for (int v = 0; v < kVec; ++v) sum[warp][v * 32 + lane] = acc[v];
-      if (lane == 0) part_l[warp] = l;
-      __syncthreads();
-      if (warp >= kVec) return;
-      // warp v adds the warps' shares of its 128 values
-      l = part_l[0];
-      acc[0] = sum[0][warp * 32 + lane];
-#pragma unroll
-      for (int w = 1; w < kJoinWarps; ++w) {
-        const float4 o = sum[w][warp * 32 + lane];
-        l += part_l[w];
-        acc[0].x += o.x;
-        acc[0].y += o.y;
-        acc[0].z += o.z;
-        acc[0].w += o.w;
-      }
-    }
-    const int t = it.q0 + (c + r) / p.group, h = it.hk * p.group + (c + r) % p.group;
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    uint2* out = reinterpret_cast<uint2*>(p.out + t * p.out_row_stride + static_cast<int64_t>(h) * C::kDv);
-#pragma unroll
-    for (int v = 0; v < (BY_ITEM ? 1 : kVec); ++v)
-      out[(BY_ITEM ? warp : v) * 32 + lane] =
-          make_uint2(pack2<DTYPE>(acc[v].x * inv, acc[v].y * inv), pack2<DTYPE>(acc[v].z * inv, acc[v].w * inv));
-    if (p.lse && lane == 0 && (!BY_ITEM || warp == 0))
-      p.lse[static_cast<int64_t>(t) * p.num_heads + h] = row_lse(M, l);
   }
+  if constexpr (BY_ITEM) {
+#pragma unroll
+    for (int v = 0; v < kVec; ++v) sum[warp][v * 32 + lane] = acc[v];
+    if (lane == 0) part[warp] = make_float2(m, l);
+    __syncthreads();
+    if (warp >= kVec) return;
+    // warp v adds the warps' shares of its 128 values
+    m = part[0].x;
+#pragma unroll
+    for (int w = 1; w < kJoinWarps; ++w) m = fmaxf(m, part[w].x);
+    const float ref = m == -INFINITY ? 0.0f : m;
+    l = 0.0f;
+    acc[0] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      const float4 o = sum[w][warp * 32 + lane];
+      const float f = ex2(part[w].x - ref);
+      l = fmaf(f, part[w].y, l);
+      acc[0].x = fmaf(f, o.x, acc[0].x);
+      acc[0].y = fmaf(f, o.y, acc[0].y);
+      acc[0].z = fmaf(f, o.z, acc[0].z);
+      acc[0].w = fmaf(f, o.w, acc[0].w);
+    }
+  }
+  const int t = static_cast<int>(shared_info.q0) + group_div(p, c + r);
+  const int h = static_cast<int>(shared_info.hk) * p.group + group_mod(p, c + r);
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  uint2* out = reinterpret_cast<uint2*>(p.out + t * p.out_row_stride + static_cast<int64_t>(h) * C::kDv);
+#pragma unroll
+  for (int v = 0; v < (BY_ITEM ? 1 : kVec); ++v)
+    out[(BY_ITEM ? warp : v) * 32 + lane] =
+        make_uint2(pack2<DTYPE>(acc[v].x * inv, acc[v].y * inv), pack2<DTYPE>(acc[v].z * inv, acc[v].w * inv));
+  if (p.lse && lane == 0 && (!BY_ITEM || warp == 0))
+    p.lse[static_cast<int64_t>(t) * p.num_heads + h] = row_lse(m, l);
 }
 
 template <int DTYPE, bool LATENT>
 cudaError_t launch(const AttnParams& p, const AttnMaps& maps, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(attention_kernel<DTYPE, LATENT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       smem_bytes<LATENT>());
+  static std::atomic<uint64_t> ready{0};  // devices whose kernel has its shared memory limit (a call costs 1 us)
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t{1} << (dev & 63);
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(attention_kernel<DTYPE, LATENT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             smem_bytes<LATENT>());
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3(static_cast<unsigned>(p.groups * p.members));
@@ -955,7 +1041,8 @@ bool plan_attention(AttnParams* p, int sms) {
   p->members = static_cast<int32_t>(chunks < kMaxMembers ? chunks : kMaxMembers);
   const int64_t cg = (chunks + p->members - 1) / p->members;
   const int64_t items = static_cast<int64_t>(p->indices ? p->num_rows : p->num_seqs) * p->num_kv_heads * cg;
-  if (items > INT32_MAX) return false;
+  if (items > INT32_MAX || p->max_seqlen_q > kMaxRowsOfRequest) return false;
+  p->group_mul = ((uint64_t{1} << kGroupShift) + p->group - 1) / p->group;
   p->chunk_groups = static_cast<int32_t>(cg);
   p->items = static_cast<int32_t>(items);
   const int tk = latent ? Cfg<true>::kTk : Cfg<false>::kTk;
@@ -972,14 +1059,14 @@ bool plan_attention(AttnParams* p, int sms) {
 size_t attention_workspace(const AttnParams& p) {
   const int64_t rows = static_cast<int64_t>(p.groups) * 2 * p.members * kChunkRows;
   const int64_t dv = p.v == nullptr ? kLatentDim : kPagedDim;
-  return static_cast<size_t>(round16(p.groups * 4 * 8) + round16(rows * 8) + rows * dv * 4);
+  return static_cast<size_t>(round16(p.groups * static_cast<int64_t>(sizeof(GroupInfo))) + round16(rows * 8) + rows * dv * 4);
 }
 
 cudaError_t launch_attention(AttnParams p, const AttnMaps& maps, int dtype, void* workspace, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(p.groups) * 2 * p.members * kChunkRows;
   char* w = static_cast<char*>(workspace);
   p.info = reinterpret_cast<int64_t*>(w);
-  w += round16(p.groups * 4 * 8);
+  w += round16(p.groups * static_cast<int64_t>(sizeof(GroupInfo)));
   p.stats = reinterpret_cast<float2*>(w);
   w += round16(rows * 8);
   p.partial = reinterpret_cast<float*>(w);

@@ -35,6 +35,7 @@ struct AttnParams {
   int32_t page_size, page_shift;
   int32_t num_seqs, num_rows, num_heads, num_kv_heads;
   int32_t group;                        // num_heads / num_kv_heads
+  uint64_t group_mul;                   // division by it (plan_attention)
   int32_t max_seqlen_q, max_seqlen_k;
   const int32_t* indices;               // nullptr: whole prefix
   int32_t num_indices;
@@ -51,7 +52,7 @@ struct AttnParams {
   int32_t items;        // (request or row) x K/V head x chunk group
   int32_t list_tiles;   // key tiles of an item with a selection (0: whole prefix)
   // workspace
-  int64_t* info;        // [groups][4]: first item, its first tile, its tiles, all tiles
+  void* info;           // [groups] GroupInfo: the first item of each group's run
   float2* stats;        // [groups][2][members][64]: reference maximum and sum of a partial row
   float* partial;       // [groups][2][members][64][dv]: its unnormalised output
 };

@@ -480,7 +480,8 @@ typedef enum fp4idx_dtype {
  * returns the matching status).  The result does not depend on its contents
  * and is the same from call to call.  No allocation, no synchronisation;
  * graph-capturable; replays see updated device metadata.
- * Supported: page_size 64 or 128; num_indices <= 2^20; num_heads <= 1024.
+ * Supported: page_size 64 or 128; num_indices <= 2^20; num_heads <= 1024;
+ * max_seqlen_q <= 2^20.
  */
 typedef struct fp4idx_attention {
   int32_t dtype;            /* fp4idx_dtype_t */
