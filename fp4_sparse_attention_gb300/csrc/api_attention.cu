@@ -174,7 +174,7 @@ fp4idx_status_t store_rows(StoreRowsParams* p, const int32_t* slots, int32_t num
                            int32_t page_size, int64_t num_pages, int64_t page_stride, void* stream) {
   if (num_tokens == 0) return FP4IDX_OK;
   const int64_t pieces = static_cast<int64_t>(num_tokens) * heads * (p->part[0].units + p->part[1].units);
-  if (pieces > static_cast<int64_t>(INT32_MAX) * 256) FAIL(FP4IDX_EUNSUPPORTED, "too many tokens");
+  if (pieces > UINT32_MAX - 256) FAIL(FP4IDX_EUNSUPPORTED, "more than 2^32 16-byte pieces in a call");
   int sms = 0;
   fp4idx_status_t s = call_device(&sms, &p->err);
   if (s != FP4IDX_OK) return s;
@@ -185,7 +185,7 @@ fp4idx_status_t store_rows(StoreRowsParams* p, const int32_t* slots, int32_t num
   p->page_shift = page_size == 128 ? 7 : 6;
   p->num_pages = num_pages;
   p->page_stride = page_stride;
-  return cuda_status(launch_store_rows(*p, static_cast<cudaStream_t>(stream)), "store launch");
+  return cuda_status(launch_store_rows(*p, sms, static_cast<cudaStream_t>(stream)), "store launch");
 }
 
 }  // namespace

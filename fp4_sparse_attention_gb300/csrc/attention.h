@@ -82,6 +82,8 @@ struct StoreRowsParams {
   int32_t num_tokens, heads;
   int32_t page_size, page_shift;
   int64_t num_pages, page_stride;
+  uint32_t per_token;  // 16-byte pieces of a token (launch_store_rows)
+  int32_t slice;       // tokens between a thread's tokens
   uint32_t* err;
 };
 
@@ -115,7 +117,7 @@ fp4idx_status_t call_tensor_map16(CUtensorMap* m, const void* base, int rank, co
 bool plan_attention(AttnParams* p, int sms);
 size_t attention_workspace(const AttnParams& p);
 cudaError_t launch_attention(AttnParams p, const AttnMaps& maps, int dtype, void* workspace, cudaStream_t stream);
-cudaError_t launch_store_rows(const StoreRowsParams& p, cudaStream_t stream);
+cudaError_t launch_store_rows(StoreRowsParams p, int sms, cudaStream_t stream);
 cudaError_t launch_tables(TablesParams p, int sms, cudaStream_t stream);
 
 #ifdef __CUDACC__

@@ -2,7 +2,8 @@
 // (fp4idx_store_latent: a token's latent and rotary values into one cache
 // row; fp4idx_store_kv: K and V rows of every KV head).
 //
-// One thread per 16-byte piece of one (token, head) row, pieces of a row in
+// A thread owns one 16-byte piece of the (token, head) rows and takes it of
+// kTokens tokens, all loads before the first store; the pieces of a row are in
 // consecutive threads, so both sides are coalesced.  Nothing is computed:
 // bound by memory for many tokens, by the launch for few.
 #include <cstring>
@@ -15,40 +16,49 @@ namespace {
 
 constexpr int kStoreThreads = 256;
 
+template <int kTokens>
 __global__ void __launch_bounds__(kStoreThreads) store_rows_kernel(const StoreRowsParams p) {
   pdl_wait();  // tokens and slots may come from the kernel before this one
   pdl_launch_dependents();
   const uint32_t u0 = p.part[0].units, units = u0 + p.part[1].units;
-  const uint32_t per_token = units * p.heads;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kStoreThreads + threadIdx.x;
-  const int64_t tok = i / per_token;
-  if (tok >= p.num_tokens) return;
-  const uint32_t rest = static_cast<uint32_t>(i - tok * per_token);
+  const uint32_t i = blockIdx.x * kStoreThreads + threadIdx.x;  // piece of one token of the first slice
+  const uint32_t tok0 = i / p.per_token;
+  if (tok0 >= static_cast<uint32_t>(p.slice)) return;
+  const uint32_t rest = i - tok0 * p.per_token;
   const uint32_t head = rest / units;
   uint32_t unit = rest - head * units;
-  const int32_t slot = __ldg(p.slots + tok);
-  if (slot < 0) return;
-  const int64_t page = slot >> p.page_shift;
-  if (page >= p.num_pages) {
-    if (rest == 0) atomicOr(p.err, kErrPageRange);
-    return;
-  }
   const StoreRowsPart& w = unit < u0 ? p.part[0] : p.part[1];
   if (unit >= u0) unit -= u0;
-  const uint4 v = __ldg(reinterpret_cast<const uint4*>(w.src + tok * w.token_stride + head * w.head_stride) + unit);
-  uint16_t* row = w.dst + page * p.page_stride + head * w.dst_head_stride +
-                  static_cast<int64_t>(slot & (p.page_size - 1)) * w.dst_row;
-  reinterpret_cast<uint4*>(row)[unit] = v;
+  const uint16_t* src = w.src + head * w.head_stride + unit * 8;
+  uint16_t* dst = w.dst + head * w.dst_head_stride + unit * 8;
+  // tokens tok0, tok0 + slice, ...
+  int32_t slot[kTokens];
+  uint4 v[kTokens];
+#pragma unroll
+  for (int n = 0; n < kTokens; ++n) {
+    const int64_t tok = tok0 + static_cast<int64_t>(n) * p.slice;
+    slot[n] = tok < p.num_tokens ? __ldg(p.slots + tok) : -1;
+    if (tok < p.num_tokens) v[n] = __ldg(reinterpret_cast<const uint4*>(src + tok * w.token_stride));
+  }
+#pragma unroll
+  for (int n = 0; n < kTokens; ++n) {
+    if (slot[n] < 0) continue;
+    const int64_t page = slot[n] >> p.page_shift;
+    if (page >= p.num_pages) {
+      if (rest == 0) atomicOr(p.err, kErrPageRange);
+      continue;
+    }
+    *reinterpret_cast<uint4*>(dst + page * p.page_stride + static_cast<int64_t>(slot[n] & (p.page_size - 1)) * w.dst_row) = v[n];
+  }
 }
 
-}  // namespace
-
-cudaError_t launch_store_rows(const StoreRowsParams& p, cudaStream_t stream) {
-  const int64_t pieces = static_cast<int64_t>(p.num_tokens) * p.heads * (p.part[0].units + p.part[1].units);
-  if (pieces == 0) return cudaSuccess;
+template <int kTokens>
+cudaError_t launch(StoreRowsParams p, cudaStream_t stream) {
+  p.slice = (p.num_tokens + kTokens - 1) / kTokens;
+  const int64_t threads = static_cast<int64_t>(p.slice) * p.per_token;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3(static_cast<unsigned>((pieces + kStoreThreads - 1) / kStoreThreads));
+  cfg.gridDim = dim3(static_cast<unsigned>((threads + kStoreThreads - 1) / kStoreThreads));
   cfg.blockDim = dim3(kStoreThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -56,7 +66,17 @@ cudaError_t launch_store_rows(const StoreRowsParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, store_rows_kernel, p);
+  return cudaLaunchKernelEx(&cfg, store_rows_kernel<kTokens>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_store_rows(StoreRowsParams p, int sms, cudaStream_t stream) {
+  p.per_token = static_cast<uint32_t>(p.heads) * (p.part[0].units + p.part[1].units);
+  if (p.num_tokens == 0) return cudaSuccess;
+  // four pieces a thread once they fill the GPU several times over
+  const int64_t pieces = static_cast<int64_t>(p.num_tokens) * p.per_token;
+  return pieces >= static_cast<int64_t>(sms) * 2048 * 8 ? launch<4>(p, stream) : launch<1>(p, stream);
 }
 
 }  // namespace fp4idx
