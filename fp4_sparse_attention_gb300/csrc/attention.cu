@@ -173,6 +173,7 @@ __device__ __forceinline__ int pairs_max_visible(const AttnParams& p, const Item
   const int first = it.q0 + group_div(p, c), last = it.q0 + group_div(p, c + n - 1);
   if (!p.visible_len) return attn_visible(p, it.b, last);  // grows with the row
   int v = 0;
+#pragma unroll 1
   for (int t = first + lane; t <= last; t += step) v = max(v, attn_visible(p, it.b, t));
   return v;
 }
@@ -343,6 +344,7 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
     int64_t mine = 0;
     Item it = {};
     int tiles = 0;
+#pragma unroll 1
     for (int i = first; i < last; ++i) {
       it = item_of(p, i);
       tiles = item_tiles<TK>(p, it, 0, 1);
@@ -593,7 +595,8 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ================================================================ MMA issuer
-    // The whole warp runs this loop; one elected lane issues.
+    // The whole warp runs this loop; one elected lane issues (always the same
+    // one: a commit covers its own thread's products).
     uint32_t g = 0, seg = 0;
     bool ok = true;
     const uint32_t tm = uniform(tmem);
@@ -626,6 +629,7 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
           tc_fence_after();
           const uint32_t d = tm + s_col + buf * TK;
           const uint64_t k_desc = desc_sw128(base + st * C::kStage, 16);
+          ++qk;
 #pragma unroll
           for (int j = 0; j < (LATENT ? C::kParts : 1); ++j) {
             if (j > 0) {  // the other parts follow at once
@@ -633,19 +637,24 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
               if (!ok) break;
               tc_fence_after();
             }
+            if (elect_one()) {
 #pragma unroll
-            for (int r = 0; r < C::kRuns; ++r)
+              for (int r = 0; r < C::kRuns; ++r)
 #pragma unroll
-              for (int c = 0; c < C::kPartPieces; ++c)
+                for (int c = 0; c < C::kPartPieces; ++c)
 #pragma unroll
-                for (int k = 0; k < 4; ++k)  // descriptor addresses count 16 bytes
-                  tc_mma_f16(d + r * 64, q_desc + (j * C::kPartPieces + c) * (kChunkRows * 8) + k * 2,
-                             k_desc + (j * C::kPart >> 4) + (r * C::kPartPieces + c) * (C::kPiece >> 4) + k * 2, qk_idesc,
-                             j + c + k > 0);
+                  for (int k = 0; k < 4; ++k)  // descriptor addresses count 16 bytes
+                    tc_mma_f16(d + r * 64, q_desc + (j * C::kPartPieces + c) * (kChunkRows * 8) + k * 2,
+                               k_desc + (j * C::kPart >> 4) + (r * C::kPartPieces + c) * (C::kPiece >> 4) + k * 2, qk_idesc,
+                               j + c + k > 0);
+              if (!LATENT || j == C::kParts - 1) {
+                if constexpr (!LATENT) tc_commit(smem_u32(&ctl.kempty[st][0]));  // the keys' last reader
+                tc_commit(smem_u32(&ctl.sfull[buf]));
+                if (qk == n) tc_commit(smem_u32(&ctl.qempty));
+              }
+            }
+            __syncwarp();
           }
-          if constexpr (!LATENT) tc_commit_elected(smem_u32(&ctl.kempty[st][0]));  // the keys' last reader
-          tc_commit_elected(smem_u32(&ctl.sfull[buf]));
-          if (++qk == n) tc_commit_elected(smem_u32(&ctl.qempty));
         }
         if (act == 2) {
           const uint32_t x = g + pv, st = uniform(x % C::kStages);
@@ -653,17 +662,20 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
             tc_fence_after();
             const uint64_t v_desc = desc_sw128(base + st * C::kStage + C::kV, C::kPiece);
             const uint32_t more = pv > 0;
+            if (elect_one()) {
 #pragma unroll
-            for (int d = 0; d < C::kDv / 128; ++d) {
+              for (int d = 0; d < C::kDv / 128; ++d) {
 #pragma unroll
-              for (int k = 0; k < TK / 16; ++k)
-                tc_mma_f16(tm + d * kChunkRows, v_desc + (d * 2 + (k >> 2) * C::kPartPieces) * (C::kPiece >> 4) + (k & 3) * 128,
-                           p_desc + (k >> 2) * (kChunkRows * 8) + (k & 3) * 2, pv_idesc, k > 0 ? 1u : more);
-              // 128 values are pieces 2d and 2d+1; part j of a latent tile is pieces 3j .. 3j+2
-              if (LATENT && d > 0) tc_commit_elected(smem_u32(&ctl.kempty[st][d - 1]));
+                for (int k = 0; k < TK / 16; ++k)
+                  tc_mma_f16(tm + d * kChunkRows, v_desc + (d * 2 + (k >> 2) * C::kPartPieces) * (C::kPiece >> 4) + (k & 3) * 128,
+                             p_desc + (k >> 2) * (kChunkRows * 8) + (k & 3) * 2, pv_idesc, k > 0 ? 1u : more);
+                // 128 values are pieces 2d and 2d+1; part j of a latent tile is pieces 3j .. 3j+2
+                if (LATENT && d > 0) tc_commit(smem_u32(&ctl.kempty[st][d - 1]));
+              }
+              if constexpr (!LATENT) tc_commit(smem_u32(&ctl.kempty[st][1]));
+              tc_commit(smem_u32(&ctl.pvdone));
             }
-            if constexpr (!LATENT) tc_commit_elected(smem_u32(&ctl.kempty[st][1]));
-            tc_commit_elected(smem_u32(&ctl.pvdone));
+            __syncwarp();
             ++pv;
           }
         }
@@ -684,7 +696,8 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
       ++seg;
     });
     // no product is in flight when TMEM is freed
-    tc_commit_elected(smem_u32(&ctl.drain));
+    if (elect_one()) tc_commit(smem_u32(&ctl.drain));
+    __syncwarp();
     if (lane == 0) {
       int never = 0;
       mbar_wait(smem_u32(&ctl.drain), 0, &never, p.err);

@@ -7,24 +7,22 @@
 
 namespace fp4idx {
 
-// D[tmem] (+)= A[smem] * B[smem]^T, 16-bit operands, fp32 accumulator, issued
-// by one elected lane of a converged warp.  The whole warp executes the call
-// so that the operands stay in uniform registers: issued from a single
-// thread's branch each MMA cost 56 cycles of register moves, which is more
-// than a 64x64x16 or 128x64x16 MMA takes (31 and 45 cycles, measured).
+// One lane of a converged warp.  MMAs are issued inside `if (elect_one())`
+// by a warp that runs its role converged: their operands then stay in uniform
+// registers.  Measured issue cost of a 64x64x16 MMA (which takes 31 cycles): 30
+// cycles so, 39 with an election per MMA, 56 from a branch of one thread.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
+  return p != 0;
+}
+// D[tmem] (+)= A[smem] * B[smem]^T, 16-bit operands, fp32 accumulator.
 __device__ __forceinline__ void tc_mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                            uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// tc_commit by the same elected lane (a commit covers its own thread's MMAs).
-__device__ __forceinline__ void tc_commit_elected(uint32_t bar) {
-  asm volatile(
-      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
-      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
       : "memory");
 }
 // Whole-warp wait for the phase of `parity`: every lane executes the same
@@ -40,21 +38,23 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
+__device__ __noinline__ bool warp_try_again(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* err) {
+  const uint64_t t0 = globaltimer();
+  bool ok = false;
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try(bar, parity);
+    if (ok || *abort) return ok;
+    if (globaltimer() - t0 > kWaitLimitNs) {
+      if ((threadIdx.x & 31) == 0) atomicOr(err, kErrTimeout);
+      *abort = 1;
+      return false;
+    }
+  }
+}
 __device__ __forceinline__ bool warp_try(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* err) {
   bool ok = mbar_try(bar, parity);
-  if (!ok) {
-    const uint64_t t0 = globaltimer();
-    do {
-#pragma unroll 1
-      for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try(bar, parity);
-      if (!ok && *abort) break;
-      if (!ok && globaltimer() - t0 > kWaitLimitNs) {
-        if ((threadIdx.x & 31) == 0) atomicOr(err, kErrTimeout);
-        *abort = 1;
-        break;
-      }
-    } while (!ok);
-  }
+  if (!ok) ok = warp_try_again(bar, parity, abort, err);
   return __all_sync(0xffffffffu, ok);
 }
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
