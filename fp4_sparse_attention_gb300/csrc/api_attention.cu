@@ -141,7 +141,7 @@ fp4idx_status_t attention_any(const fp4idx_attention_t* a, bool latent, void* wo
   AttnParams p = attention_params(a);
   int sms = 0;
   if ((s = call_device(&sms, &p.err)) != FP4IDX_OK) return s;
-  if (!plan_attention(&p, sms)) FAIL(FP4IDX_EUNSUPPORTED, "more than 2^31 work items or 2^20 rows per request");
+  if (!plan_attention(&p, sms)) FAIL(FP4IDX_EUNSUPPORTED, "more than 2^31 key tiles or 2^20 rows per request");
   const size_t need = attention_workspace(p);
   if (!workspace || workspace_bytes < need)
     FAIL(FP4IDX_EWORKSPACE, "workspace of %zu bytes is smaller than %zu", workspace ? workspace_bytes : size_t{0}, need);

@@ -101,24 +101,30 @@ struct Item {
 // The part of an item that one CTA computes.
 struct Segment {
   Item it;
-  int c, rows;       // its pairs [c, c + rows) of the request; none: rows <= 0
+  int c, rows;       // its pairs [c, c + rows) of the request; rows <= 0: nothing to do
   int max_vis;       // largest visible length among them
-  int lo, hi, tiles; // key tiles [lo, hi) of the item's `tiles`
+  int lo, hi;        // key tiles [lo, hi) of the item's `tiles`
+  int tiles;
 };
 
-// A CTA's run of tiles [lo, hi), its first item (which starts at tile
-// `start`) and its first segment, worked out once for all roles.
+// A CTA's run of tiles [lo, hi) of the concatenation; its first item starts
+// at tile `start`.
 struct Run {
-  int64_t lo, hi, start;
-  int item;
-  Segment first;
+  int lo, hi, item, start;
 };
+
+// Segments are worked out by one loader warp and read by all roles.  Four
+// slots: the loader is at most kStages tiles, so at most as many segments,
+// ahead of the slowest role.
+constexpr int kSegSlots = 4;
 
 template <bool LATENT>
 struct Control {
   uint64_t kfull[Cfg<LATENT>::kStages][Cfg<LATENT>::kParts], kempty[Cfg<LATENT>::kStages][Cfg<LATENT>::kParts];
   uint64_t sfull[2], sempty[2], pfull, pvdone, qfull, qempty, oempty, drain;
   int64_t row_off[kChunkRows];                                 // output element of each row
+  uint64_t seg_ready[kSegSlots];
+  Segment seg[kSegSlots];
   Run run;
   int32_t key_pos[Cfg<LATENT>::kStages][Cfg<LATENT>::kTk];     // logical position, -1: no key
   alignas(4) uint8_t holes[Cfg<LATENT>::kStages][kTeamWarps];  // a loader warp found a key that does not exist
@@ -190,26 +196,25 @@ __device__ __forceinline__ int item_tiles(const AttnParams& p, const Item& it, i
   return max(1, (v + TK - 1) / TK);
 }
 
-// First tile of a group's run; a 64-bit division takes 200 cycles more.
-__device__ __forceinline__ int64_t run_start(int64_t total, int group, int groups) {
-  if (total < (1 << 22)) return static_cast<uint32_t>(total) * static_cast<uint32_t>(group) / static_cast<uint32_t>(groups);
-  return static_cast<int64_t>(static_cast<uint64_t>(total) * group / groups);
+// First tile of a group's run: the runs of all groups differ by one tile at
+// most.  (32 bits: plan_attention bounds the tiles.)
+__device__ __forceinline__ int run_start(int total, int group, int groups) {
+  const int each = static_cast<int>(static_cast<uint32_t>(total) / static_cast<uint32_t>(groups));
+  return group * each + min(group, total - each * groups);
 }
-__device__ __forceinline__ int used_groups(const AttnParams& p, int64_t total) {
-  return total < p.groups ? static_cast<int>(total) : p.groups;
-}
+__device__ __forceinline__ int used_groups(const AttnParams& p, int total) { return min(total, p.groups); }
 
 // Segment of the tiles [pos, hi) of the concatenation, of an item of `tiles`
 // tiles that starts at `start`.
-__device__ __forceinline__ Segment segment_of(const AttnParams& p, const Item& it, int tiles, int64_t start, int64_t pos,
-                                              int64_t hi, int member, int lane, int step) {
+__device__ __forceinline__ Segment segment_of(const AttnParams& p, const Item& it, int tiles, int start, int pos, int hi,
+                                              int member, int lane, int step) {
   Segment s;
   s.it = it;
   s.tiles = tiles;
   s.c = it.c0 + member * kChunkRows;
   s.rows = min(kChunkRows, it.rows - s.c);
-  s.lo = static_cast<int>(pos - start);
-  s.hi = static_cast<int>(min(hi, start + tiles) - start);
+  s.lo = pos - start;
+  s.hi = min(hi, start + tiles) - start;
   s.max_vis = s.rows > 0 ? pairs_max_visible(p, it, s.c, s.rows, lane, step) : 0;
   if (step > 1) s.max_vis = __reduce_max_sync(0xffffffffu, s.max_vis);
   return s;
@@ -217,47 +222,22 @@ __device__ __forceinline__ Segment segment_of(const AttnParams& p, const Item& i
 
 // What the join needs to know of a group's first item.
 struct GroupInfo {
-  int64_t item, start, tiles, total;  // total: tiles of all items (every group writes it)
-  int64_t q0, rows, c0, hk;
+  int item, start, total;  // total: tiles of all items (every group writes it)
+  int q0, rows, c0, hk, pad;
 };
 
-__device__ __forceinline__ void set_run(const AttnParams& p, Run* run, int group, int member, int64_t total, int64_t lo,
-                                        int64_t hi, int item, const Item& it, int64_t start, int tiles) {
-  run->item = item;
-  run->start = start;
-  run->first = segment_of(p, it, tiles, start, lo, hi, member, 0, 1);
-  if (member == 0) {
-    GroupInfo& info = reinterpret_cast<GroupInfo*>(p.info)[group];
-    info.item = item;
-    info.start = start;
-    info.tiles = tiles;
-    info.q0 = it.q0;
-    info.rows = it.rows;
-    info.c0 = it.c0;
-    info.hk = it.hk;
-  }
-}
-
 // Calls f(segment) for every segment of this CTA, in order; whole warps.
-template <int TK, class F>
-__device__ __forceinline__ void for_segments(const AttnParams& p, const Run& run, int member, F&& f) {
-  const int lane = threadIdx.x & 31;
-  const int64_t hi = run.hi;
-  if (run.lo >= hi) return;
-  Segment s = run.first;
-  int item = run.item;
-  int64_t start = run.start;
-  for (;;) {
-    if (s.rows > 0) f(s);
-    start += s.tiles;
-    if (start >= hi) return;
-    Item it;
-    int tiles;
-    do {  // an item without rows has no tiles
-      it = item_of(p, ++item);
-      tiles = item_tiles<TK>(p, it, lane, 32);
-    } while (tiles == 0);
-    s = segment_of(p, it, tiles, start, start, hi, member, lane, 32);
+// SOFTMAX: the role's warps leave together, since they meet at named barriers.
+template <bool LATENT, bool SOFTMAX, class F>
+__device__ __forceinline__ void for_segments(Control<LATENT>& ctl, uint32_t* err, F&& f) {
+  if (ctl.run.lo >= ctl.run.hi) return;
+  for (uint32_t k = 0;; ++k) {
+    bool ok = warp_try(smem_u32(&ctl.seg_ready[k % kSegSlots]), (k / kSegSlots) & 1, &ctl.abort, err);
+    if (SOFTMAX) ok = !bar_red_or(1, 32 * kSoftmaxWarps, !ok);
+    if (!ok) return;
+    const Segment s = ctl.seg[k % kSegSlots];
+    if (s.rows <= 0) return;
+    f(s, k);
   }
 }
 
@@ -305,6 +285,7 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
       mbar_init(smem_u32(&ctl.sfull[s]), 1);
       mbar_init(smem_u32(&ctl.sempty[s]), kSoftmaxWarps);
     }
+    for (int k = 0; k < kSegSlots; ++k) mbar_init(smem_u32(&ctl.seg_ready[k]), 1);
     mbar_init(smem_u32(&ctl.pfull), kSoftmaxWarps);
     mbar_init(smem_u32(&ctl.pvdone), 1);
     mbar_init(smem_u32(&ctl.qfull), C::kTeams * kTeamWarps);
@@ -315,78 +296,85 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
     fence_barrier_init();
   }
   if (warp == kMmaWarp) tmem_alloc<kTmemCols>(smem_u32(&ctl.tmem));
+  __syncthreads();
   pdl_wait();  // everything below reads what earlier kernels wrote
 
-  // ---- the run of tiles of this CTA's group
+  // ---- the run of tiles of this CTA's group and its first segment
   const int group = blockIdx.x / p.members, member = blockIdx.x - group * p.members;
-  if (p.indices) {
-    if (tid == 0) {
-      const int64_t total = static_cast<int64_t>(p.items) * p.list_tiles;
-      const int used = used_groups(p, total);
-      const bool work = group < used;
-      const int64_t lo = work ? run_start(total, group, used) : 0, hi = work ? run_start(total, group + 1, used) : 0;
-      ctl.run.lo = lo;
-      ctl.run.hi = hi;
-      if (member == 0) reinterpret_cast<GroupInfo*>(p.info)[group].total = total;
-      if (work) {
-        const int item = static_cast<int>(static_cast<uint32_t>(lo >> 32) == 0 ? static_cast<uint32_t>(lo) / static_cast<uint32_t>(p.list_tiles)
-                                                                             : lo / p.list_tiles);
-        set_run(p, &ctl.run, group, member, total, lo, hi, item, item_of(p, item), static_cast<int64_t>(item) * p.list_tiles,
-                p.list_tiles);
-      }
-    }
-  } else {
-    // every thread sums a run of items; then the thread whose run holds this
-    // group's first tile finds the item (the key ring is not in use yet)
-    int64_t* warp_sum = reinterpret_cast<int64_t*>(smem);
-    const int per = (p.items + C::kThreads - 1) / C::kThreads;
-    const int first = min(p.items, tid * per), last = min(p.items, first + per);
-    int64_t mine = 0;
-    Item it = {};
-    int tiles = 0;
+  {
+    int total, before = 0, mine = 0, first = 0;  // all tiles; those before this thread's items, of them
+    int per = 1, tiles = 0;
+    Item it;
+    if (p.indices) {
+      total = p.items * p.list_tiles;
+      mine = tid == 0 ? total : 0;
+    } else {
+      // every thread sums a run of items (the key ring is not in use yet)
+      int* warp_sum = reinterpret_cast<int*>(smem);
+      per = (p.items + C::kThreads - 1) / C::kThreads;
+      first = min(p.items, tid * per);
+      const int last = min(p.items, first + per);
 #pragma unroll 1
-    for (int i = first; i < last; ++i) {
-      it = item_of(p, i);
-      tiles = item_tiles<TK>(p, it, 0, 1);
-      mine += tiles;
-    }
-    int64_t incl = mine;
+      for (int i = first; i < last; ++i) {
+        it = item_of(p, i);
+        tiles = item_tiles<TK>(p, it, 0, 1);
+        mine += tiles;
+      }
+      int incl = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    int64_t before = incl - mine, total = 0;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (lane == 31) warp_sum[warp] = incl;
+      __syncthreads();
+      before = incl - mine;
+      total = 0;
 #pragma unroll
-    for (int w = 0; w < C::kThreads / 32; ++w) {
-      const int64_t v = warp_sum[w];
-      before += w < warp ? v : 0;
-      total += v;
+      for (int w = 0; w < C::kThreads / 32; ++w) {
+        const int v = warp_sum[w];
+        before += w < warp ? v : 0;
+        total += v;
+      }
     }
     const int used = used_groups(p, total);
     const bool work = group < used;
-    const int64_t lo = work ? run_start(total, group, used) : 0, hi = work ? run_start(total, group + 1, used) : 0;
+    const int lo = work ? run_start(total, group, used) : 0, hi = work ? run_start(total, group + 1, used) : 0;
+    GroupInfo& info = reinterpret_cast<GroupInfo*>(p.info)[group];
     if (tid == 0) {
       ctl.run.lo = lo;
       ctl.run.hi = hi;
-      if (member == 0) reinterpret_cast<GroupInfo*>(p.info)[group].total = total;
+      if (member == 0) info.total = total;
     }
-    if (work && before <= lo && lo < before + mine) {
-      int i = last - 1;
-      if (per > 1) {  // walk this thread's items again
-        i = first - 1;
-        int64_t at = before;
-        tiles = 0;
+    if (work && before <= lo && lo < before + mine) {  // the thread whose items hold the first tile
+      int item = first;
+      if (p.indices) {
+        item = static_cast<uint32_t>(lo) / static_cast<uint32_t>(p.list_tiles);
+        it = item_of(p, item);
+        tiles = p.list_tiles;
+        before = item * tiles;
+      } else if (per > 1) {  // walk its items again
+        --item;
+        int at = before;
         do {
           before = at;
-          it = item_of(p, ++i);
+          it = item_of(p, ++item);
           tiles = item_tiles<TK>(p, it, 0, 1);
           at += tiles;
         } while (at <= lo);
       }
-      set_run(p, &ctl.run, group, member, total, lo, hi, i, it, before, tiles);
+      ctl.run.item = item;
+      ctl.run.start = before;
+      ctl.seg[0] = segment_of(p, it, tiles, before, lo, hi, member, 0, 1);
+      if (ctl.seg[0].rows > 0) mbar_arrive(smem_u32(&ctl.seg_ready[0]));
+      if (member == 0) {
+        info.item = item;
+        info.start = before;
+        info.q0 = it.q0;
+        info.rows = it.rows;
+        info.c0 = it.c0;
+        info.hk = it.hk;
+      }
     }
   }
   __syncthreads();
@@ -404,10 +392,30 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
     const int u = lt & 7, key0 = lt >> 3;                   // 16-byte unit of a 128-byte piece; first key
     constexpr int kPass = kTeamThreads / 8;                 // keys the team copies at a time
     constexpr int kFind = LATENT ? 64 / kPass : C::kRuns;   // positions a thread looks up: runs, or its listed keys
-    uint32_t g = 0, seg = 0;                                // tiles and segments before this one
+    uint32_t g = 0;                                         // tiles before this segment
     uint32_t issued = 0;                                    // this team's last tile, counted from 1
     bool ok = true;
-    for_segments<TK>(p, ctl.run, member, [&](const Segment& s) {
+    // the next segment with rows behind an item of `tiles` tiles, or the end (rows 0), as segment k
+    int item = ctl.run.item, start = ctl.run.start;
+    const auto publish = [&](int tiles, uint32_t k) {
+      Segment n;
+      const int hi = ctl.run.hi;
+      do {
+        start += tiles;
+        n.rows = 0;
+        if (start >= hi) break;
+        const Item it = item_of(p, ++item);
+        tiles = item_tiles<TK>(p, it, lane, 32);
+        if (tiles > 0) n = segment_of(p, it, tiles, start, start, hi, member, lane, 32);
+      } while (n.rows <= 0);
+      if (lane == 0) {
+        ctl.seg[k % kSegSlots] = n;
+        mbar_arrive(smem_u32(&ctl.seg_ready[k % kSegSlots]));
+      }
+      __syncwarp();
+    };
+    if (lw == 0 && ctl.run.lo < ctl.run.hi && ctl.seg[0].rows <= 0) publish(ctl.seg[0].tiles, 0);
+    for_segments<LATENT, false>(ctl, p.err, [&](const Segment& s, uint32_t seg) {
       if (!ok) return;
       const int64_t table = attn_table_base(p, s.it.b);
       const int32_t* list = nullptr;
@@ -448,7 +456,7 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
       ok = warp_try(smem_u32(&ctl.qempty), (seg & 1) ^ 1, abort_flag, p.err);
       if (!ok) return;
 #pragma unroll 1
-      for (int r = team * kPass + key0; r < kChunkRows; r += C::kTeams * kPass) {
+      for (int r = team * kPass + key0; r < ((s.rows + 15) & ~15); r += C::kTeams * kPass) {
         const bool have = r < s.rows;
         const int x = s.c + (have ? r : 0), t = s.it.q0 + group_div(p, x), h = s.it.hk * p.group + group_mod(p, x);
         const uint16_t* src = p.q + t * p.q_row_stride + h * p.q_head_stride + u * 8;
@@ -583,7 +591,7 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
         queries_landed();
       }
       g += s.hi - s.lo;
-      ++seg;
+      if (lw == 0) publish(s.tiles, seg + 1);
     });
     // after a time-out: this warp's copies land before the CTA can exit
     cp_async_wait_all();
@@ -597,7 +605,7 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
     // ================================================================ MMA issuer
     // The whole warp runs this loop; one elected lane issues (always the same
     // one: a commit covers its own thread's products).
-    uint32_t g = 0, seg = 0;
+    uint32_t g = 0;
     bool ok = true;
     const uint32_t tm = uniform(tmem);
     const uint32_t qk_idesc = uniform(idesc_f16(64, 64, DTYPE == FP4IDX_BF16, false, p.negate != 0));
@@ -605,7 +613,7 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
     const auto done = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_test_wait(smem_u32(bar), parity));
     };
-    for_segments<TK>(p, ctl.run, member, [&](const Segment& s) {
+    for_segments<LATENT, false>(ctl, p.err, [&](const Segment& s, uint32_t seg) {
       if (!ok) return;
       const uint32_t pv_idesc = uniform(idesc_f16(128, (s.rows + 15) & ~15, DTYPE == FP4IDX_BF16, true, false));
       const uint32_t n = uniform(s.hi - s.lo);
@@ -693,7 +701,6 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
         }
       }
       g += n;
-      ++seg;
     });
     // no product is in flight when TMEM is freed
     if (elect_one()) tc_commit(smem_u32(&ctl.drain));
@@ -711,7 +718,7 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
     bool ok = true;
     const int r0 = 16 * warp + (lane >> 2);                 // this thread's rows: r0 and r0 + 8
     const uint32_t quarter = static_cast<uint32_t>(warp) << 21;  // TMEM lanes 32 * warp
-    for_segments<TK>(p, ctl.run, member, [&](const Segment& s) {
+    for_segments<LATENT, true>(ctl, p.err, [&](const Segment& s, uint32_t) {
       // rows past the chunk's end have zero queries: their scores are harmless
       int vis[2];
 #pragma unroll
@@ -917,7 +924,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   constexpr int kVec = C::kDv / 128;  // float4s per lane
   __shared__ float4 sum[BY_ITEM ? kJoinWarps : 1][C::kDv / 4];
   __shared__ float2 part[kJoinWarps];
-  __shared__ int64_t total_tiles;
+  __shared__ int total_tiles;
   __shared__ int first_group;
   __shared__ GroupInfo shared_info;
   pdl_wait();
@@ -927,7 +934,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   const GroupInfo* infos = reinterpret_cast<const GroupInfo*>(p.info);
   GroupInfo info = {};
   if (tid < p.groups) info = infos[tid];
-  const int64_t candidate = BY_ITEM ? blockIdx.x : infos[blockIdx.x + 1].item;
+  const int candidate = BY_ITEM ? blockIdx.x : infos[blockIdx.x + 1].item;
   if (tid == 0) {
     total_tiles = info.total;
     first_group = INT32_MAX;
@@ -942,9 +949,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   if (parts == 1 || (!BY_ITEM && group != static_cast<int>(blockIdx.x) + 1)) return;
   if (tid == group) shared_info = info;
   __syncthreads();
-  const int c = static_cast<int>(shared_info.c0) + member * kChunkRows;
+  const int c = shared_info.c0 + member * kChunkRows;
   const int r = BY_ITEM ? blockIdx.z : blockIdx.z * kJoinWarps + warp;
-  if (r >= min(kChunkRows, static_cast<int>(shared_info.rows) - c)) return;  // (BY_ITEM: the whole CTA)
+  if (r >= min(kChunkRows, shared_info.rows - c)) return;  // (BY_ITEM: the whole CTA)
   // this warp's partials, each added relative to the largest maximum so far
   float4 acc[kVec] = {};
   float m = -INFINITY, l = 0.0f;
@@ -992,8 +999,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
       acc[0].w = fmaf(f, o.w, acc[0].w);
     }
   }
-  const int t = static_cast<int>(shared_info.q0) + group_div(p, c + r);
-  const int h = static_cast<int>(shared_info.hk) * p.group + group_mod(p, c + r);
+  const int t = shared_info.q0 + group_div(p, c + r);
+  const int h = shared_info.hk * p.group + group_mod(p, c + r);
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   uint2* out = reinterpret_cast<uint2*>(p.out + t * p.out_row_stride + static_cast<int64_t>(h) * C::kDv);
 #pragma unroll
@@ -1063,6 +1070,7 @@ bool plan_attention(AttnParams* p, int sms) {
   // no more groups than tiles can exist
   const int64_t per_item = p->indices ? p->list_tiles : (static_cast<int64_t>(p->max_seqlen_k) + tk - 1) / tk;
   const int64_t most = items * (per_item < 1 ? 1 : per_item);
+  if (most > INT32_MAX) return false;
   int64_t groups = sms / p->members;
   if (groups > kJoinThreads) groups = kJoinThreads;  // the join looks at one group per thread
   p->groups = static_cast<int32_t>(most < groups ? most : groups);
