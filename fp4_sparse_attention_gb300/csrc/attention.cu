@@ -452,24 +452,30 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
       }
 #pragma unroll
       for (int n = 0; n < kFind; ++n) page[n] = entry(now[n]);
-      // queries of the segment, once the previous segment's products are done
-      ok = warp_try(smem_u32(&ctl.qempty), (seg & 1) ^ 1, abort_flag, p.err);
-      if (!ok) return;
+      // this team's share of the segment's queries, once the previous segment's
+      // products are done; the team that loads the first tile does that first
+      bool q_issued = false, q_landed = false;
+      const auto load_queries = [&] {
+        q_issued = true;
+        ok = warp_try(smem_u32(&ctl.qempty), (seg & 1) ^ 1, abort_flag, p.err);
+        if (!ok) return;
 #pragma unroll 1
-      for (int r = team * kPass + key0; r < ((s.rows + 15) & ~15); r += C::kTeams * kPass) {
-        const bool have = r < s.rows;
-        const int x = s.c + (have ? r : 0), t = s.it.q0 + group_div(p, x), h = s.it.hk * p.group + group_mod(p, x);
-        const uint16_t* src = p.q + t * p.q_row_stride + h * p.q_head_stride + u * 8;
-        const uint32_t dst = base + C::kOff_Q + r * 128 + ((u ^ (r & 7)) << 4);
+        for (int r = team * kPass + key0; r < ((s.rows + 15) & ~15); r += C::kTeams * kPass) {
+          const bool have = r < s.rows;
+          const int x = s.c + (have ? r : 0), t = s.it.q0 + group_div(p, x), h = s.it.hk * p.group + group_mod(p, x);
+          const uint16_t* src = p.q + t * p.q_row_stride + h * p.q_head_stride + u * 8;
+          const uint32_t dst = base + C::kOff_Q + r * 128 + ((u ^ (r & 7)) << 4);
 #pragma unroll
-        for (int c = 0; c < C::kKc; ++c) cp_async_16_or_zero(dst + c * (kChunkRows * 128), src + c * 64, have);
-      }
-      cp_async_commit();
-      bool q_landed = false;
-      const auto queries_landed = [&] {  // called once this warp's copies so far have landed
-        if (lane == 0 && !q_landed) mbar_arrive(smem_u32(&ctl.qfull));
-        q_landed = true;
+          for (int c = 0; c < C::kKc; ++c) cp_async_16_or_zero(dst + c * (kChunkRows * 128), src + c * 64, have);
+        }
+        cp_async_commit();
       };
+      const auto queries_landed = [&] {  // called once this warp's copies so far have landed
+        if (lane == 0 && q_issued && !q_landed) mbar_arrive(smem_u32(&ctl.qfull));
+        q_landed = q_issued;
+      };
+      if (i != s.lo) load_queries();
+      if (!ok) return;
       for (; i < s.hi; i += C::kTeams) {
         const uint32_t x = g + (i - s.lo), st = x % C::kStages, ph = ((x / C::kStages) & 1) ^ 1;
         const uint32_t stage = base + st * C::kStage;
@@ -559,6 +565,10 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
             cp_async_commit();
           }
         }
+        if (!q_issued) {
+          load_queries();
+          if (!ok) return;
+        }
         // look ahead while the loads are under way
 #pragma unroll
         for (int n = 0; n < kFind; ++n) {
@@ -567,14 +577,15 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
           next[n] = find(i + 2 * C::kTeams, n);
         }
         if (!boxes) {
+          const bool all = !q_landed;  // queries behind the parts: one wait for both
 #pragma unroll
           for (int j = 0; j < C::kParts; ++j) {
-            if (C::kParts - 1 - j == 2) cp_async_wait_group<2>();
-            else if (C::kParts - 1 - j == 1) cp_async_wait_group<1>();
-            else cp_async_wait_group<0>();
+            if (all || j == C::kParts - 1) cp_async_wait_group<0>();
+            else if (j == C::kParts - 2) cp_async_wait_group<1>();
+            else cp_async_wait_group<2>();
             fence_proxy_async_smem();  // the products read the copies through the async proxy
             __syncwarp();
-            queries_landed();
+            if (j == 0) queries_landed();
             if (lane == 0) mbar_arrive(smem_u32(&ctl.kfull[st][j]));
           }
         } else if (!q_landed) {
