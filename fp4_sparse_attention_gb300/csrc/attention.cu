@@ -25,8 +25,7 @@
 //               a row's maximum grew by more than 2^8 (until then the older
 //               maximum serves as the reference: weights stay below 2^8 and
 //               the result is the same up to rounding); the output.
-//   warp 4      MMA issuer: whichever of the next tile's Q K^T and this
-//               tile's V^T P^T is ready.
+//   warp 4      MMA issuer.
 //   warps 5-    loaders: a 64-key run of one page by TMA; listed keys, and a
 //               run that a request ends in, by 16-byte asynchronous copies
 //               (zeros for keys that do not exist); key positions.  A gather
@@ -621,95 +620,75 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
     const uint32_t tm = uniform(tmem);
     const uint32_t qk_idesc = uniform(idesc_f16(64, 64, DTYPE == FP4IDX_BF16, false, p.negate != 0));
     const uint64_t q_desc = desc_sw128(base + C::kOff_Q, 16), p_desc = desc_sw128(base + C::kOff_P, 16);
-    const auto done = [&](uint64_t* bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_test_wait(smem_u32(bar), parity));
-    };
+    // Order of the products: two score products, then their two value products
+    // (latent: the stages hold two tiles), or a score product two tiles ahead of
+    // each value product (paged).  A fixed order with blocking waits: choosing
+    // what is ready by polling cost 400 cycles at every hand-over.
     for_segments<LATENT, false>(ctl, p.err, [&](const Segment& s, uint32_t seg) {
       if (!ok) return;
       const uint32_t pv_idesc = uniform(idesc_f16(128, (s.rows + 15) & ~15, DTYPE == FP4IDX_BF16, true, false));
       const uint32_t n = uniform(s.hi - s.lo);
-      uint32_t qk = 0, pv = 0, spins = 0;
-      uint64_t t0 = 0;
-      ok = warp_try(smem_u32(&ctl.qfull), seg & 1, abort_flag, p.err);
-      while (ok && pv < n) {
-        // what can be issued: 1 the next score product (its first part is there), 2 the oldest value product
-        int act = 0;
-        {
-          const uint32_t x = g + qk, y = g + pv;
-          if (pv < qk && done(&ctl.pfull, y & 1) && (pv > 0 || done(&ctl.oempty, (seg & 1) ^ 1)) &&
-              (LATENT || done(&ctl.kfull[y % C::kStages][1], (y / C::kStages) & 1)))
-            act = 2;
-          else if (qk < n && qk - pv < 2 && done(&ctl.kfull[x % C::kStages][0], (x / C::kStages) & 1) &&
-                   done(&ctl.sempty[x & 1], ((x >> 1) & 1) ^ 1))
-            act = 1;
-        }
-        if (act == 1) {
-          const uint32_t x = g + qk, st = uniform(x % C::kStages), buf = x & 1;
+      const auto score = [&](uint32_t i) {
+        const uint32_t x = g + i, st = uniform(x % C::kStages), use = (x / C::kStages) & 1, buf = x & 1;
+        const uint32_t d = tm + s_col + buf * TK;
+        const uint64_t k_desc = desc_sw128(base + st * C::kStage, 16);
+        ok = warp_try(smem_u32(&ctl.sempty[buf]), ((x >> 1) & 1) ^ 1, abort_flag, p.err);
+#pragma unroll
+        for (int j = 0; j < (LATENT ? C::kParts : 1); ++j) {
+          ok = ok && warp_try(smem_u32(&ctl.kfull[st][j]), use, abort_flag, p.err);
+          if (!ok) return;
           tc_fence_after();
-          const uint32_t d = tm + s_col + buf * TK;
-          const uint64_t k_desc = desc_sw128(base + st * C::kStage, 16);
-          ++qk;
+          if (elect_one()) {
 #pragma unroll
-          for (int j = 0; j < (LATENT ? C::kParts : 1); ++j) {
-            if (j > 0) {  // the other parts follow at once
-              ok = warp_try(smem_u32(&ctl.kfull[st][j]), (x / C::kStages) & 1, abort_flag, p.err);
-              if (!ok) break;
-              tc_fence_after();
+            for (int r = 0; r < C::kRuns; ++r)
+#pragma unroll
+              for (int c = 0; c < C::kPartPieces; ++c)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)  // descriptor addresses count 16 bytes
+                  tc_mma_f16(d + r * 64, q_desc + (j * C::kPartPieces + c) * (kChunkRows * 8) + k * 2,
+                             k_desc + (j * C::kPart >> 4) + (r * C::kPartPieces + c) * (C::kPiece >> 4) + k * 2, qk_idesc,
+                             j + c + k > 0);
+            if (!LATENT || j == C::kParts - 1) {
+              if constexpr (!LATENT) tc_commit(smem_u32(&ctl.kempty[st][0]));  // the keys' last reader
+              tc_commit(smem_u32(&ctl.sfull[buf]));
+              if (i + 1 == n) tc_commit(smem_u32(&ctl.qempty));
             }
-            if (elect_one()) {
-#pragma unroll
-              for (int r = 0; r < C::kRuns; ++r)
-#pragma unroll
-                for (int c = 0; c < C::kPartPieces; ++c)
-#pragma unroll
-                  for (int k = 0; k < 4; ++k)  // descriptor addresses count 16 bytes
-                    tc_mma_f16(d + r * 64, q_desc + (j * C::kPartPieces + c) * (kChunkRows * 8) + k * 2,
-                               k_desc + (j * C::kPart >> 4) + (r * C::kPartPieces + c) * (C::kPiece >> 4) + k * 2, qk_idesc,
-                               j + c + k > 0);
-              if (!LATENT || j == C::kParts - 1) {
-                if constexpr (!LATENT) tc_commit(smem_u32(&ctl.kempty[st][0]));  // the keys' last reader
-                tc_commit(smem_u32(&ctl.sfull[buf]));
-                if (qk == n) tc_commit(smem_u32(&ctl.qempty));
-              }
-            }
-            __syncwarp();
           }
+          __syncwarp();
         }
-        if (act == 2) {
-          const uint32_t x = g + pv, st = uniform(x % C::kStages);
-          {
-            tc_fence_after();
-            const uint64_t v_desc = desc_sw128(base + st * C::kStage + C::kV, C::kPiece);
-            const uint32_t more = pv > 0;
-            if (elect_one()) {
+      };
+      const auto value = [&](uint32_t i) {
+        const uint32_t x = g + i, st = uniform(x % C::kStages), more = i > 0;
+        const uint64_t v_desc = desc_sw128(base + st * C::kStage + C::kV, C::kPiece);
+        if (i == 0) ok = warp_try(smem_u32(&ctl.oempty), (seg & 1) ^ 1, abort_flag, p.err);
+        if constexpr (!LATENT)
+          ok = ok && warp_try(smem_u32(&ctl.kfull[st][1]), (x / C::kStages) & 1, abort_flag, p.err);
+        ok = ok && warp_try(smem_u32(&ctl.pfull), x & 1, abort_flag, p.err);
+        if (!ok) return;
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-              for (int d = 0; d < C::kDv / 128; ++d) {
+          for (int d = 0; d < C::kDv / 128; ++d) {
 #pragma unroll
-                for (int k = 0; k < TK / 16; ++k)
-                  tc_mma_f16(tm + d * kChunkRows, v_desc + (d * 2 + (k >> 2) * C::kPartPieces) * (C::kPiece >> 4) + (k & 3) * 128,
-                             p_desc + (k >> 2) * (kChunkRows * 8) + (k & 3) * 2, pv_idesc, k > 0 ? 1u : more);
-                // 128 values are pieces 2d and 2d+1; part j of a latent tile is pieces 3j .. 3j+2
-                if (LATENT && d > 0) tc_commit(smem_u32(&ctl.kempty[st][d - 1]));
-              }
-              if constexpr (!LATENT) tc_commit(smem_u32(&ctl.kempty[st][1]));
-              tc_commit(smem_u32(&ctl.pvdone));
-            }
-            __syncwarp();
-            ++pv;
+            for (int k = 0; k < TK / 16; ++k)
+              tc_mma_f16(tm + d * kChunkRows, v_desc + (d * 2 + (k >> 2) * C::kPartPieces) * (C::kPiece >> 4) + (k & 3) * 128,
+                         p_desc + (k >> 2) * (kChunkRows * 8) + (k & 3) * 2, pv_idesc, k > 0 ? 1u : more);
+            // 128 values are pieces 2d and 2d+1; part j of a latent tile is pieces 3j .. 3j+2
+            if (LATENT && d > 0) tc_commit(smem_u32(&ctl.kempty[st][d - 1]));
           }
+          if constexpr (!LATENT) tc_commit(smem_u32(&ctl.kempty[st][1]));
+          tc_commit(smem_u32(&ctl.pvdone));
         }
-        if (act != 0) {
-          spins = 0;
-        } else if ((++spins & 1023u) == 0) {  // every wait ends
-          if (spins == 1024u) t0 = globaltimer();
-          bool stop = *abort_flag != 0;
-          if (globaltimer() - t0 > kWaitLimitNs) {
-            if (lane == 0) atomicOr(p.err, kErrTimeout);
-            *abort_flag = 1;
-            stop = true;
-          }
-          ok = !__any_sync(0xffffffffu, stop);
-        }
+        __syncwarp();
+      };
+      ok = warp_try(smem_u32(&ctl.qfull), seg & 1, abort_flag, p.err);
+      uint32_t scored = 0;
+#pragma unroll 1
+      for (uint32_t i = 0; ok && i < n; ++i) {
+        const uint32_t ahead = min(n, (LATENT ? i & ~1u : i) + 2);
+#pragma unroll 1
+        for (; ok && scored < ahead; ++scored) score(scored);
+        if (ok) value(i);
       }
       g += n;
     });
