@@ -679,14 +679,12 @@ def fp4idx_build_tables(cached_len: torch.Tensor, new_len: torch.Tensor, block_t
     if new_len.shape[0] != B or block_table.dim() != 2 or block_table.shape[0] != B or block_table.stride(1) != 1:
         raise ValueError("new_len must be [B] and block_table [B, stride] with dense rows")
     if out is None:
-        # one allocation, five arrays in it
-        at = 2 * (B + 1)
-        flat = torch.empty((at + 2 * num_rows + 1,), dtype=i32, device=cached_len.device)
-        cu_q = flat.as_strided((B + 1,), (1,), 0)
-        cu_k = flat.as_strided((B + 1,), (1,), B + 1)
-        visible = flat.as_strided((num_rows,), (1,), at)
-        slots = flat.as_strided((num_rows,), (1,), at + num_rows)
-        taken = flat.as_strided((1,), (1,), at + 2 * num_rows)
+        dev = cached_len.device
+        cu_q = torch.empty((B + 1,), dtype=i32, device=dev)
+        cu_k = torch.empty((B + 1,), dtype=i32, device=dev)
+        visible = torch.empty((num_rows,), dtype=i32, device=dev)
+        slots = torch.empty((num_rows,), dtype=i32, device=dev)
+        taken = torch.empty((1,), dtype=i32, device=dev)
     else:
         for x, n in zip(out, (B + 1, B + 1, num_rows, num_rows, 1)):
             if x.dtype != i32 or x.numel() != n or not x.is_contiguous():

@@ -45,6 +45,7 @@
 // second reader.  An item cut by a boundary leaves partial sums that
 // join_kernel adds in a fixed order.
 #include <atomic>
+#include <cstddef>
 #include <cstring>
 
 #include "attention.h"
@@ -106,10 +107,11 @@ struct Segment {
   int tiles;
 };
 
-// A CTA's run of tiles [lo, hi) of the concatenation; its first item starts
-// at tile `start`.
+// A CTA's run of tiles [lo, hi) of the concatenation, which ends before item
+// `end`; its first item starts at tile `start`.  With whole items a run is
+// the items [item, end), counted from tile 0.
 struct Run {
-  int lo, hi, item, start;
+  int lo, hi, item, start, end;
 };
 
 // Segments are worked out by one loader warp and read by all roles.  Four
@@ -125,12 +127,15 @@ struct Control {
   uint64_t seg_ready[kSegSlots];
   Segment seg[kSegSlots];
   Run run;
-  int32_t key_pos[Cfg<LATENT>::kStages][Cfg<LATENT>::kTk];     // logical position, -1: no key
+  alignas(8) int32_t key_pos[Cfg<LATENT>::kStages][Cfg<LATENT>::kTk];  // logical position, -1: no key (read in pairs)
   alignas(4) uint8_t holes[Cfg<LATENT>::kStages][kTeamWarps];  // a loader warp found a key that does not exist
   float factor[kChunkRows], row_inv[kChunkRows];
   uint32_t tmem;
   int abort;
 };
+
+static_assert(offsetof(Control<true>, key_pos) % 8 == 0 && offsetof(Control<false>, key_pos) % 8 == 0, "int2 reads");
+static_assert(offsetof(Control<true>, holes) % 4 == 0 && offsetof(Control<false>, holes) % 4 == 0, "one-word reads");
 
 template <bool LATENT>
 constexpr uint32_t smem_bytes() {
@@ -195,11 +200,15 @@ __device__ __forceinline__ int item_tiles(const AttnParams& p, const Item& it, i
   return max(1, (v + TK - 1) / TK);
 }
 
-// First tile of a group's run: the runs of all groups differ by one tile at
-// most.  (32 bits: plan_attention bounds the tiles.)
+// First tile of a group's run: runs differ by one tile at most, and cut items
+// of one length alike when there is a whole number of groups per item.  (32
+// bits: plan_attention bounds the tiles; long concatenations put the longer
+// runs first.)
 __device__ __forceinline__ int run_start(int total, int group, int groups) {
-  const int each = static_cast<int>(static_cast<uint32_t>(total) / static_cast<uint32_t>(groups));
-  return group * each + min(group, total - each * groups);
+  const uint32_t n = total, g = group, all = groups;
+  if (n < (1u << 23)) return n * g / all;
+  const uint32_t each = n / all;
+  return g * each + min(g, n - each * all);
 }
 __device__ __forceinline__ int used_groups(const AttnParams& p, int total) { return min(total, p.groups); }
 
@@ -304,7 +313,10 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
     int total, before = 0, mine = 0, first = 0;  // all tiles; those before this thread's items, of them
     int per = 1, tiles = 0;
     Item it;
-    if (p.indices) {
+    if (p.whole_items) {
+      total = p.items;
+      mine = tid == 0 ? total : 0;
+    } else if (p.indices) {
       total = p.items * p.list_tiles;
       mine = tid == 0 ? total : 0;
     } else {
@@ -341,13 +353,20 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
     const int lo = work ? run_start(total, group, used) : 0, hi = work ? run_start(total, group + 1, used) : 0;
     GroupInfo& info = reinterpret_cast<GroupInfo*>(p.info)[group];
     if (tid == 0) {
-      ctl.run.lo = lo;
-      ctl.run.hi = hi;
+      ctl.run.lo = p.whole_items ? 0 : lo;
+      ctl.run.hi = p.whole_items ? (work ? INT32_MAX : 0) : hi;
+      ctl.run.end = p.whole_items ? hi : p.items;
       if (member == 0) info.total = total;
     }
     if (work && before <= lo && lo < before + mine) {  // the thread whose items hold the first tile
-      int item = first;
-      if (p.indices) {
+      int item = first, from = lo, to = hi;
+      if (p.whole_items) {
+        item = lo;
+        it = item_of(p, item);
+        tiles = item_tiles<TK>(p, it, 0, 1);
+        before = from = 0;
+        to = INT32_MAX;
+      } else if (p.indices) {
         item = static_cast<uint32_t>(lo) / static_cast<uint32_t>(p.list_tiles);
         it = item_of(p, item);
         tiles = p.list_tiles;
@@ -364,7 +383,7 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
       }
       ctl.run.item = item;
       ctl.run.start = before;
-      ctl.seg[0] = segment_of(p, it, tiles, before, lo, hi, member, 0, 1);
+      ctl.seg[0] = segment_of(p, it, tiles, before, from, to, member, 0, 1);
       if (ctl.seg[0].rows > 0) mbar_arrive(smem_u32(&ctl.seg_ready[0]));
       if (member == 0) {
         info.item = item;
@@ -398,12 +417,12 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
     int item = ctl.run.item, start = ctl.run.start;
     const auto publish = [&](int tiles, uint32_t k) {
       Segment n;
-      const int hi = ctl.run.hi;
+      const int hi = ctl.run.hi, end = ctl.run.end;
       do {
         start += tiles;
         n.rows = 0;
-        if (start >= hi) break;
-        const Item it = item_of(p, ++item);
+        if (start >= hi || ++item >= end) break;
+        const Item it = item_of(p, item);
         tiles = item_tiles<TK>(p, it, lane, 32);
         if (tiles > 0) n = segment_of(p, it, tiles, start, start, hi, member, lane, 32);
       } while (n.rows <= 0);
@@ -458,8 +477,10 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
         q_issued = true;
         ok = warp_try(smem_u32(&ctl.qempty), (seg & 1) ^ 1, abort_flag, p.err);
         if (!ok) return;
+        // the team without the first tile takes the first rows
+        const int turn = (team + 2 * C::kTeams - 1 - static_cast<int>(g % C::kTeams)) % C::kTeams;
 #pragma unroll 1
-        for (int r = team * kPass + key0; r < ((s.rows + 15) & ~15); r += C::kTeams * kPass) {
+        for (int r = turn * kPass + key0; r < ((s.rows + 15) & ~15); r += C::kTeams * kPass) {
           const bool have = r < s.rows;
           const int x = s.c + (have ? r : 0), t = s.it.q0 + group_div(p, x), h = s.it.hk * p.group + group_mod(p, x);
           const uint16_t* src = p.q + t * p.q_row_stride + h * p.q_head_stride + u * 8;
@@ -493,13 +514,13 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
         }
         const bool boxes = !rows_listed && !ends, issuer = boxes && tw == 0;
         hole = __any_sync(0xffffffffu, hole || ends);
-        if (issuer) {
+        const bool fresh = x < C::kStages;                  // a stage's first use: nothing to wait for
+        if (issuer && !fresh) {
           // the bytes can be announced before the part is free, once its last load is complete
 #pragma unroll
           for (int j = 0; j < C::kParts; ++j) {
             const uint32_t bar = smem_u32(&ctl.kfull[st][j]);
-            const bool over = x < C::kStages || warp_try(bar, ph, abort_flag, p.err);
-            if (over && lane == 0) mbar_arrive_expect_tx(bar, C::kPart);
+            if (warp_try(bar, ph, abort_flag, p.err) && lane == 0) mbar_arrive_expect_tx(bar, C::kPart);
           }
         }
         __syncwarp();
@@ -520,7 +541,7 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
         }
 #pragma unroll
         for (int j = 0; j < C::kParts; ++j) {
-          ok = warp_try(smem_u32(&ctl.kempty[st][j]), ph, abort_flag, p.err);
+          ok = fresh || warp_try(smem_u32(&ctl.kempty[st][j]), ph, abort_flag, p.err);
           if (!ok) return;
           if (j == C::kPosPart && !issuer) {                // positions for the masks
             if (rows_listed) {
@@ -563,6 +584,10 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
             }
             cp_async_commit();
           }
+        }
+        if (issuer && fresh && lane == 0) {  // the loads are on their way before their bytes are announced
+#pragma unroll
+          for (int j = 0; j < C::kParts; ++j) mbar_arrive_expect_tx(smem_u32(&ctl.kfull[st][j]), C::kPart);
         }
         if (!q_issued) {
           load_queries();
@@ -905,8 +930,8 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
 // an item that crosses run boundaries, in the order of its keys.  The eight
 // warps of a CTA take a row each when an item has few partials (BY_ITEM
 // false: blockIdx.x counts run boundaries, the first boundary inside an item
-// does its work), and share one row's partials when there are fewer items
-// than groups, so that many partials meet (BY_ITEM: blockIdx.x is the item).
+// does its work), and share one row's partials when many meet (BY_ITEM:
+// blockIdx.x is the item).
 
 template <int DTYPE, bool LATENT, bool BY_ITEM>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnParams p) {
@@ -1026,13 +1051,13 @@ cudaError_t launch(const AttnParams& p, const AttnMaps& maps, cudaStream_t strea
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, attention_kernel<DTYPE, LATENT>, p, maps)) != cudaSuccess) return e;
-  if (p.groups < 2) return cudaSuccess;
+  if (p.groups < 2 || p.whole_items) return cudaSuccess;
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   // rows that a CTA of the first kernel can hold
   const int64_t pairs = (p.indices ? 1 : static_cast<int64_t>(p.max_seqlen_q)) * p.group;
   const unsigned rows = static_cast<unsigned>(pairs < kChunkRows ? pairs : kChunkRows);
-  if (p.items < p.groups) {
+  if (p.groups > 4 * static_cast<int64_t>(p.items)) {  // more than four partials per row
     cfg.gridDim = dim3(static_cast<unsigned>(p.items), static_cast<unsigned>(p.members), rows);
     return cudaLaunchKernelEx(&cfg, join_kernel<DTYPE, LATENT, true>, p);
   }
@@ -1063,7 +1088,26 @@ bool plan_attention(AttnParams* p, int sms) {
   if (most > INT32_MAX) return false;
   int64_t groups = sms / p->members;
   if (groups > kJoinThreads) groups = kJoinThreads;  // the join looks at one group per thread
-  p->groups = static_cast<int32_t>(most < groups ? most : groups);
+  // How are the items cut?  In tiles' time of the longest run:
+  //   whole items: no partial sums and no join;
+  //   each item into an equal number of runs: partial sums and a join, which
+  //     cost as much as two (latent) or three (paged) tiles;
+  //   equal runs over all items: every group busy, but most CTAs also cross from
+  //     one item to the next, five tiles in all.
+  // Measured, whole against cut into single tiles: one request of 2 / 3 latent
+  // tiles 9.8 / 11.7 against 10.8 / 10.8 us, of 3 / 5 paged tiles 8.1 / 10.0
+  // against 9.0 / 9.0 us; whole against equal runs: 64 requests of 4 latent tiles
+  // 13.1 against 16.0 us, 160 items of 4 / 6 paged tiles 17.6 / 23.0 against
+  // 19.6 / 23.3 us.
+  const int64_t longest = per_item < 1 ? 1 : per_item;
+  const int64_t whole = (items + groups - 1) / groups * longest;
+  int64_t cuts = groups / items < longest ? groups / items : longest;
+  const int64_t cut = cuts > 1 ? (longest + cuts - 1) / cuts + (latent ? 2 : 3) : INT64_MAX;
+  const int64_t equal = longest * items / groups + 5;
+  p->whole_items = whole < cut && whole <= equal;
+  if (!p->whole_items && cut <= equal) groups = cuts * items;
+  const int64_t units = p->whole_items ? items : most;
+  p->groups = static_cast<int32_t>(units < groups ? units : groups);
   return true;
 }
 
