@@ -122,7 +122,7 @@ constexpr int kSegSlots = 4;
 template <bool LATENT>
 struct Control {
   uint64_t kfull[Cfg<LATENT>::kStages][Cfg<LATENT>::kParts], kempty[Cfg<LATENT>::kStages][Cfg<LATENT>::kParts];
-  uint64_t sfull[2], sempty[2], pfull, pvdone, qfull, qempty, oempty, drain;
+  uint64_t sfull[2], sempty[2], pfull, pvdone, qfull[2], qempty[2], oempty, drain;
   int64_t row_off[kChunkRows];                                 // output element of each row
   uint64_t seg_ready[kSegSlots];
   Segment seg[kSegSlots];
@@ -228,6 +228,18 @@ __device__ __forceinline__ Segment segment_of(const AttnParams& p, const Item& i
   return s;
 }
 
+// Where a segment's queries go: with at most 32 rows a CTA the buffer holds two
+// segments' queries (32 rows each), so the next ones load early.  (The product
+// of the second half reads 64 rows from row 32 on: what lies behind its 32
+// rows only reaches score rows that nobody reads.)
+struct QuerySlot {
+  uint32_t slot, use;  // half, and how often it was used before
+};
+__device__ __forceinline__ QuerySlot query_slot(const AttnParams& p, uint32_t seg) {
+  return p.two_queries ? QuerySlot{seg & 1, seg >> 1} : QuerySlot{0, seg};
+}
+constexpr uint32_t kQueryHalf = 32 * 128;
+
 // What the join needs to know of a group's first item.
 struct GroupInfo {
   int item, start, total;  // total: tiles of all items (every group writes it)
@@ -292,12 +304,12 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_u32(&ctl.sfull[s]), 1);
       mbar_init(smem_u32(&ctl.sempty[s]), kSoftmaxWarps);
+      mbar_init(smem_u32(&ctl.qfull[s]), C::kTeams * kTeamWarps);
+      mbar_init(smem_u32(&ctl.qempty[s]), 1);
     }
     for (int k = 0; k < kSegSlots; ++k) mbar_init(smem_u32(&ctl.seg_ready[k]), 1);
     mbar_init(smem_u32(&ctl.pfull), kSoftmaxWarps);
     mbar_init(smem_u32(&ctl.pvdone), 1);
-    mbar_init(smem_u32(&ctl.qfull), C::kTeams * kTeamWarps);
-    mbar_init(smem_u32(&ctl.qempty), 1);
     mbar_init(smem_u32(&ctl.oempty), kSoftmaxWarps);
     mbar_init(smem_u32(&ctl.drain), 1);
     ctl.abort = 0;
@@ -472,10 +484,11 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
       for (int n = 0; n < kFind; ++n) page[n] = entry(now[n]);
       // this team's share of the segment's queries, once the previous segment's
       // products are done; the team that loads the first tile does that first
-      bool q_issued = false, q_landed = false;
+      bool q_issued = false, q_landed = false, published = false;
+      const QuerySlot qs = query_slot(p, seg);
       const auto load_queries = [&] {
         q_issued = true;
-        ok = warp_try(smem_u32(&ctl.qempty), (seg & 1) ^ 1, abort_flag, p.err);
+        ok = warp_try(smem_u32(&ctl.qempty[qs.slot]), (qs.use & 1) ^ 1, abort_flag, p.err);
         if (!ok) return;
         // the team without the first tile takes the first rows
         const int turn = (team + 2 * C::kTeams - 1 - static_cast<int>(g % C::kTeams)) % C::kTeams;
@@ -484,14 +497,14 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
           const bool have = r < s.rows;
           const int x = s.c + (have ? r : 0), t = s.it.q0 + group_div(p, x), h = s.it.hk * p.group + group_mod(p, x);
           const uint16_t* src = p.q + t * p.q_row_stride + h * p.q_head_stride + u * 8;
-          const uint32_t dst = base + C::kOff_Q + r * 128 + ((u ^ (r & 7)) << 4);
+          const uint32_t dst = base + C::kOff_Q + qs.slot * kQueryHalf + r * 128 + ((u ^ (r & 7)) << 4);
 #pragma unroll
           for (int c = 0; c < C::kKc; ++c) cp_async_16_or_zero(dst + c * (kChunkRows * 128), src + c * 64, have);
         }
         cp_async_commit();
       };
       const auto queries_landed = [&] {  // called once this warp's copies so far have landed
-        if (lane == 0 && q_issued && !q_landed) mbar_arrive(smem_u32(&ctl.qfull));
+        if (lane == 0 && q_issued && !q_landed) mbar_arrive(smem_u32(&ctl.qfull[qs.slot]));
         q_landed = q_issued;
       };
       if (i != s.lo) load_queries();
@@ -593,6 +606,10 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
           load_queries();
           if (!ok) return;
         }
+        if (lw == 0 && !published) {
+          publish(s.tiles, seg + 1);
+          published = true;
+        }
         // look ahead while the loads are under way
 #pragma unroll
         for (int n = 0; n < kFind; ++n) {
@@ -626,7 +643,7 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
         queries_landed();
       }
       g += s.hi - s.lo;
-      if (lw == 0) publish(s.tiles, seg + 1);
+      if (lw == 0 && !published) publish(s.tiles, seg + 1);
     });
     // after a time-out: this warp's copies land before the CTA can exit
     cp_async_wait_all();
@@ -653,6 +670,8 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
       if (!ok) return;
       const uint32_t pv_idesc = uniform(idesc_f16(128, (s.rows + 15) & ~15, DTYPE == FP4IDX_BF16, true, false));
       const uint32_t n = uniform(s.hi - s.lo);
+      const QuerySlot qs = query_slot(p, seg);
+      const uint64_t qh_desc = q_desc + uniform(qs.slot * (kQueryHalf >> 4));
       const auto score = [&](uint32_t i) {
         const uint32_t x = g + i, st = uniform(x % C::kStages), use = (x / C::kStages) & 1, buf = x & 1;
         const uint32_t d = tm + s_col + buf * TK;
@@ -670,13 +689,13 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
               for (int c = 0; c < C::kPartPieces; ++c)
 #pragma unroll
                 for (int k = 0; k < 4; ++k)  // descriptor addresses count 16 bytes
-                  tc_mma_f16(d + r * 64, q_desc + (j * C::kPartPieces + c) * (kChunkRows * 8) + k * 2,
+                  tc_mma_f16(d + r * 64, qh_desc + (j * C::kPartPieces + c) * (kChunkRows * 8) + k * 2,
                              k_desc + (j * C::kPart >> 4) + (r * C::kPartPieces + c) * (C::kPiece >> 4) + k * 2, qk_idesc,
                              j + c + k > 0);
             if (!LATENT || j == C::kParts - 1) {
               if constexpr (!LATENT) tc_commit(smem_u32(&ctl.kempty[st][0]));  // the keys' last reader
               tc_commit(smem_u32(&ctl.sfull[buf]));
-              if (i + 1 == n) tc_commit(smem_u32(&ctl.qempty));
+              if (i + 1 == n) tc_commit(smem_u32(&ctl.qempty[qs.slot]));
             }
           }
           __syncwarp();
@@ -706,7 +725,7 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
         }
         __syncwarp();
       };
-      ok = warp_try(smem_u32(&ctl.qfull), seg & 1, abort_flag, p.err);
+      ok = warp_try(smem_u32(&ctl.qfull[qs.slot]), qs.use & 1, abort_flag, p.err);
       uint32_t scored = 0;
 #pragma unroll 1
       for (uint32_t i = 0; ok && i < n; ++i) {
@@ -1078,6 +1097,7 @@ bool plan_attention(AttnParams* p, int sms) {
   const int64_t items = static_cast<int64_t>(p->indices ? p->num_rows : p->num_seqs) * p->num_kv_heads * cg;
   if (items > INT32_MAX || p->max_seqlen_q > kMaxRowsOfRequest) return false;
   p->group_mul = ((uint64_t{1} << kGroupShift) + p->group - 1) / p->group;
+  p->two_queries = pairs <= 32;
   p->chunk_groups = static_cast<int32_t>(cg);
   p->items = static_cast<int32_t>(items);
   const int tk = latent ? Cfg<true>::kTk : Cfg<false>::kTk;
