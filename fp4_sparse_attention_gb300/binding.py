@@ -635,6 +635,8 @@ def fp4idx_store_latent(latent: torch.Tensor, rope: torch.Tensor, slots: torch.T
         raise ValueError("slots must be a contiguous [N] int32 tensor")
     if cache.dim() != 3 or cache.shape[2] != 576 or cache.stride()[1:] != (576, 1):
         raise ValueError("cache must be [P, page, 576], dense inside a page")
+    if N == 0:
+        return
     status = load_library().fp4idx_store_latent(latent.data_ptr(), ls, rope.data_ptr(), rs, slots.data_ptr(), N,
                                                 cache.shape[1], cache.shape[0], cache.stride(0), cache.data_ptr(),
                                                 _stream(stream))
@@ -657,6 +659,8 @@ def fp4idx_store_kv(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tenso
     if k.dim() != 4 or k.shape[1] != Hkv or k.shape[3] != 128 or k.shape != v.shape or k.stride() != v.stride() \
             or k.stride()[1:] != (k.shape[2] * 128, 128, 1):
         raise ValueError("k and v must be [P, Hkv, page, 128], dense inside a page, with one set of strides")
+    if N == 0:
+        return
     status = load_library().fp4idx_store_kv(k_new.data_ptr(), k_new.stride(0), v_new.data_ptr(), v_new.stride(0),
                                             slots.data_ptr(), N, Hkv, k.shape[2], k.shape[0], k.stride(0), k.data_ptr(),
                                             v.data_ptr(), _stream(stream))

@@ -48,7 +48,10 @@ fp4idx_status_t check_attention(const fp4idx_attention_t* a, bool latent) {
     FAIL(FP4IDX_EUNSUPPORTED, "num_pages below 2^31 - 1 and page_stride below 2^39 are supported");
   if (a->max_seqlen_q < 1 || a->max_seqlen_k < 0)
     FAIL(FP4IDX_EINVAL, "max_seqlen_q >= 1 and max_seqlen_k >= 0 required");
-  if (!a->q || !a->k || (!latent && !a->v) || !a->cu_seqlens_q || !a->cu_seqlens_k || !a->block_table || !a->out)
+  if (a->max_seqlen_k > 1 << 30) FAIL(FP4IDX_EUNSUPPORTED, "max_seqlen_k %d: up to 2^30", a->max_seqlen_k);
+  // (a call without rows may come with the null pointers of empty tensors)
+  if ((a->num_rows > 0 && (!a->q || !a->out)) || !a->k || (!latent && !a->v) || !a->cu_seqlens_q || !a->cu_seqlens_k ||
+      !a->block_table)
     FAIL(FP4IDX_EINVAL, "q, k, v (paged), cu_seqlens_q, cu_seqlens_k, block_table and out are required");
   const int dk = latent ? kLatentDim + kRopeDim : kPagedDim, dv = latent ? kLatentDim : kPagedDim;
   if (!aligned(a->q, 16) || !aligned(a->k, 16) || !aligned(a->v, 16) || !aligned(a->out, 16))

@@ -481,7 +481,7 @@ typedef enum fp4idx_dtype {
  * and is the same from call to call.  No allocation, no synchronisation;
  * graph-capturable; replays see updated device metadata.
  * Supported: page_size 64 or 128; num_indices <= 2^20; num_heads <= 1024;
- * max_seqlen_q <= 2^20.
+ * max_seqlen_q <= 2^20; max_seqlen_k <= 2^30.
  */
 typedef struct fp4idx_attention {
   int32_t dtype;            /* fp4idx_dtype_t */

@@ -84,6 +84,7 @@ BAD = [
     (dict(dtype=2), 1), (dict(num_seqs=0), 1), (dict(num_rows=-1), 1), (dict(num_heads=0), 1),
     (dict(num_heads=2048, q_row_stride=2048 * 576, out_row_stride=2048 * 512), 2), (dict(page_size=32), 2),
     (dict(page_size=96), 2), (dict(num_pages=0), 1), (dict(max_seqlen_q=0), 1), (dict(max_seqlen_k=-1), 1),
+    (dict(max_seqlen_k=2 ** 31 - 1, table_stride=1 << 30), 2),
     (dict(q=None), 1), (dict(k=None), 1), (dict(out=None), 1), (dict(cu_seqlens_q=None), 1),
     (dict(cu_seqlens_k=None), 1), (dict(block_table=None), 1), (dict(q=FAKE + 8), 1), (dict(k=FAKE + 2), 1),
     (dict(out=FAKE + 4), 1), (dict(lse=FAKE + 2), 1), (dict(q_head_stride=64), 1), (dict(q_head_stride=577), 1),
@@ -114,6 +115,7 @@ def test_attention_null_and_empty(lib):
     assert lib.fp4idx_attention_workspace_bytes(None) == 0
     for latent, f in ((True, lib.fp4idx_latent_attention), (False, lib.fp4idx_paged_attention)):
         assert f(ctypes.byref(_attention(latent, num_rows=0)), None, 0, None) == 0
+        assert f(ctypes.byref(_attention(latent, num_rows=0, q=None, out=None)), None, 0, None) == 0
 
 
 @pytest.mark.parametrize("over,status", [

@@ -311,3 +311,19 @@ def test_lse_is_optional():
     call(a)
     torch.cuda.synchronize()
     assert torch.equal(a.out, want) and bool((a.lse == 3).all())
+
+
+@pytest.mark.parametrize("kv", [None, 2])
+def test_no_rows(kv):
+    c = R.make_case(26, [0, 0], [70, 3], heads=16, kv_heads=kv, visibility="full", device="cuda")
+    out, lse = call(build(c))
+    torch.cuda.synchronize()
+    assert out.shape[0] == 0 and lse.shape[0] == 0 and B.fp4idx_get_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("kv,heads", [(None, 16), (None, 128), (2, 8)])
+@pytest.mark.parametrize("requests,length", [(1, 128), (1, 200), (30, 256), (60, 700), (200, 300)])
+def test_every_way_of_cutting_items(requests, length, kv, heads):
+    # whole items, items cut alike, equal runs over all items: chosen by sizes alone
+    lens = [max(1, length - 37 * (i % 5)) for i in range(requests)]
+    run_case(requests + length, [1] * requests, lens, heads=heads, kv_heads=kv, visibility="full")

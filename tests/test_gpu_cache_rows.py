@@ -54,6 +54,17 @@ def test_store_kv(n, heads, page):
     assert torch.equal(dv.cpu().view(torch.int16), wv.view(torch.int16))
 
 
+def test_no_tokens():
+    cache = torch.zeros((2, 64, 576), dtype=torch.bfloat16, device="cuda")
+    x = torch.ones((0, 576), dtype=torch.bfloat16, device="cuda")
+    n = torch.zeros((0,), dtype=torch.int32, device="cuda")
+    B.fp4idx_store_latent(x[:, :512], x[:, 512:], n, cache)
+    kv = torch.zeros((2, 2, 3, 64, 128), dtype=torch.bfloat16, device="cuda")
+    e = torch.zeros((0, 3, 128), dtype=torch.bfloat16, device="cuda")
+    B.fp4idx_store_kv(e, e, n, kv[0], kv[1])
+    assert B.fp4idx_get_error(clear=True) == 0 and not cache.any()
+
+
 def test_slots_past_the_cache_are_skipped_and_reported():
     cache = torch.zeros((2, 64, 576), dtype=torch.bfloat16, device="cuda")
     x = torch.ones((4, 576), dtype=torch.bfloat16, device="cuda")
