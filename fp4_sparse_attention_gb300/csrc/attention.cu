@@ -11,13 +11,21 @@
 //   P   = 2^(S - m)                      registers, rounded to 16 bits once
 //   O^T [dv x 64 rows]      += V^T P^T   tcgen05, M = 128 of dv, N = rows
 //
-// The second product is transposed so that M is the value dimension: 64 rows
-// on M would use half of the tensor pipe, and O^T of 512 values x 64 rows
+// The second product is transposed so that M is the value dimension: M = 64
+// runs at half of the tensor pipe's rate, and O^T of 512 values x 64 rows
 // takes 256 TMEM columns where O would take all 512.  Both operands of both
 // products come from one copy of the keys in shared memory: a key's row lies
 // in 128-byte swizzled pieces of 64 values, which is the K-major layout Q K^T
 // wants and, read along the other axis, the MN-major layout V^T wants; for
 // the latent cache K and V are even the same bytes.
+//
+// A latent tile takes 74 KB, so a ring of three leaves no room for 74 KB of
+// queries: 512 of their 576 values lie in TMEM, half of them in each half of
+// the lanes that M = 64 leaves free (two accumulators, added by the softmax),
+// the rotary ones in shared memory, and the weights take the place of the
+// tile's rotary piece, which only the score product reads.  With two stages
+// (queries in shared memory) neither loads nor softmax could be hidden: a tile
+// took 3,200 cycles, now 2,200, of which the products fill 1,900.
 //
 // Roles (one CTA per SM):
 //   warps 0-3   softmax: TMEM S as row fragments (four lanes per row), mask,
@@ -25,18 +33,18 @@
 //               a row's maximum grew by more than 2^8 (until then the older
 //               maximum serves as the reference: weights stay below 2^8 and
 //               the result is the same up to rounding); the output.
-//   warp 4      MMA issuer.
-//   warps 5-    loaders: a 64-key run of one page by TMA; listed keys, and a
+//   warp 4, 5   MMA issuers of the score and the value products.
+//   warps 6-    loaders: a 64-key run of one page by TMA; listed keys, and a
 //               run that a request ends in, by 16-byte asynchronous copies
-//               (zeros for keys that do not exist); key positions.  A gather
-//               of four rows by TMA (tile::gather4) moves 512 bytes an
+//               (zeros for keys that do not exist); key positions; queries.  A
+//               gather of four rows by TMA (tile::gather4) moves 512 bytes an
 //               instruction and reached 6.7-8.7 TB/s from L2 where the copies
 //               reach 20.
 // A tile arrives and leaves in parts (latent: three times 192 of the 576
 // values; paged: keys, values): the score product starts with the first part
-// and a part is loaded again as soon as its last product is done, which is
-// what two 74 KB stages of latent keys beside 74 KB of queries need to
-// overlap loads with products.
+// and a part is loaded again as soon as its last product is done.  A latent
+// segment's queries pass through a place of the ring like a tile and are
+// copied to TMEM from there, so they load while the segment before computes.
 //
 // Work split: the tiles of all items (request or row, K/V head, row chunk)
 // are concatenated and cut into equal runs, one per CTA group, so long and
@@ -54,7 +62,7 @@
 namespace fp4idx {
 namespace {
 
-constexpr int kSoftmaxWarps = 4, kMmaWarp = 4;
+constexpr int kSoftmaxWarps = 4, kScoreWarp = 4, kLoadWarp = kScoreWarp + 2;
 constexpr int kTeamWarps = 4, kTeamThreads = 32 * kTeamWarps;  // loader teams take tiles in turn
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxMembers = 8;
@@ -72,24 +80,35 @@ struct Cfg {
   static constexpr int kDv = LATENT ? kLatentDim : kPagedDim;
   static constexpr int kTk = LATENT ? 64 : 128;                 // keys per tile
   static constexpr int kRuns = kTk / 64;                        // 64-key runs of a tile: each inside one page
-  static constexpr int kStages = LATENT ? 2 : 3;
+  static constexpr int kStages = 3;
   static constexpr int kParts = LATENT ? 3 : 2;                 // parts of a stage that arrive and leave alone
   static constexpr int kPosPart = LATENT ? 0 : 1;               // the part whose barriers guard the positions: it leaves after the softmax
   static constexpr int kTeams = LATENT ? 2 : 1;
-  static constexpr int kThreads = 32 * (kSoftmaxWarps + 1 + kTeams * kTeamWarps);
+  // Slots of planned segments: a team plans the next one behind its first load
+  // in a segment, which waited for the products kStages places before: no role
+  // still reads the segment whose slot is taken.
+  static constexpr int kSegSlots = kStages + 1;
+  static constexpr int kThreads = 32 * (kLoadWarp + kTeams * kTeamWarps);
   static constexpr int kKc = kDk / 64;                          // 128-byte pieces of a key
   static constexpr int kPartPieces = LATENT ? kLatentBoxPieces : kPagedBoxPieces;  // pieces of a part, per run
   static constexpr uint32_t kPiece = 64 * 128;                  // one piece of a run's keys
   static constexpr uint32_t kPart = kRuns * kPartPieces * kPiece;
   static constexpr uint32_t kStage = kParts * kPart;
   static constexpr uint32_t kV = LATENT ? 0 : kPart;            // values inside a stage
-  static constexpr uint32_t kQ = kKc * kChunkRows * 128;
-  static constexpr uint32_t kP = kTk / 64 * kChunkRows * 128;
+  static constexpr int kQPieces = LATENT ? 8 : 0;               // 64-value pieces of the queries in TMEM; the others in shared memory
+  static constexpr uint32_t kQ = (kKc - kQPieces) * kChunkRows * 128;
+  // Latent weights take the place of the tile's rotary piece, which only the
+  // score product reads.
+  static constexpr uint32_t kP = LATENT ? 0 : kTk / 64 * kChunkRows * 128;
   static constexpr uint32_t kOff_Q = kStages * kStage;
-  static constexpr uint32_t kOff_P = kOff_Q + kQ;
-  static constexpr uint32_t kOff_Ctl = kOff_P + kP;
-  static constexpr uint32_t kOCols = kDv / 128 * kChunkRows;    // O^T: 64 columns per 128 values
+  static constexpr uint32_t kOff_P = LATENT ? kQPieces * kPiece : kOff_Q + kQ;
+  static constexpr uint32_t kOff_Ctl = kOff_Q + kQ + kP;
+  // TMEM: O^T, 64 columns per 128 values; score buffers; latent queries
+  static constexpr uint32_t kOCols = kDv / 128 * kChunkRows;
+  static constexpr uint32_t kQCol = kOCols + 2 * kTk;
 };
+constexpr uint32_t kUpper = 16u << 16;  // the other 16 lanes of each TMEM quarter that M = 64 leaves free
+static_assert(Cfg<true>::kQCol + Cfg<true>::kQPieces * 16 == kTmemCols && Cfg<false>::kQCol <= kTmemCols, "TMEM");
 
 struct Item {
   int b, hk;
@@ -114,22 +133,19 @@ struct Run {
   int lo, hi, item, start, end;
 };
 
-// Segments are worked out by one loader warp and read by all roles.  Four
-// slots: the loader is at most kStages tiles, so at most as many segments,
-// ahead of the slowest role.
-constexpr int kSegSlots = 4;
-
+// Segments are worked out by one loader warp and read by all roles.
 template <bool LATENT>
 struct Control {
   uint64_t kfull[Cfg<LATENT>::kStages][Cfg<LATENT>::kParts], kempty[Cfg<LATENT>::kStages][Cfg<LATENT>::kParts];
   uint64_t sfull[2], sempty[2], pfull, pvdone, qfull[2], qempty[2], oempty, drain;
   int64_t row_off[kChunkRows];                                 // output element of each row
-  uint64_t seg_ready[kSegSlots];
-  Segment seg[kSegSlots];
+  uint64_t seg_ready[Cfg<LATENT>::kSegSlots];
+  Segment seg[Cfg<LATENT>::kSegSlots];
   Run run;
   alignas(8) int32_t key_pos[Cfg<LATENT>::kStages][Cfg<LATENT>::kTk];  // logical position, -1: no key (read in pairs)
   alignas(4) uint8_t holes[Cfg<LATENT>::kStages][kTeamWarps];  // a loader warp found a key that does not exist
-  float factor[kChunkRows], row_inv[kChunkRows];
+  alignas(16) float factor[kChunkRows], row_inv[kChunkRows];
+  uint8_t grown[kSoftmaxWarps];                                // a warp's rows have factors below 1
   uint32_t tmem;
   int abort;
 };
@@ -252,10 +268,10 @@ template <bool LATENT, bool SOFTMAX, class F>
 __device__ __forceinline__ void for_segments(Control<LATENT>& ctl, uint32_t* err, F&& f) {
   if (ctl.run.lo >= ctl.run.hi) return;
   for (uint32_t k = 0;; ++k) {
-    bool ok = warp_try(smem_u32(&ctl.seg_ready[k % kSegSlots]), (k / kSegSlots) & 1, &ctl.abort, err);
+    bool ok = warp_try(smem_u32(&ctl.seg_ready[k % Cfg<LATENT>::kSegSlots]), (k / Cfg<LATENT>::kSegSlots) & 1, &ctl.abort, err);
     if (SOFTMAX) ok = !bar_red_or(1, 32 * kSoftmaxWarps, !ok);
     if (!ok) return;
-    const Segment s = ctl.seg[k % kSegSlots];
+    const Segment s = ctl.seg[k % Cfg<LATENT>::kSegSlots];
     if (s.rows <= 0) return;
     f(s, k);
   }
@@ -304,18 +320,18 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_u32(&ctl.sfull[s]), 1);
       mbar_init(smem_u32(&ctl.sempty[s]), kSoftmaxWarps);
-      mbar_init(smem_u32(&ctl.qfull[s]), C::kTeams * kTeamWarps);
+      mbar_init(smem_u32(&ctl.qfull[s]), LATENT ? 1 : kTeamWarps);
       mbar_init(smem_u32(&ctl.qempty[s]), 1);
     }
-    for (int k = 0; k < kSegSlots; ++k) mbar_init(smem_u32(&ctl.seg_ready[k]), 1);
+    for (int k = 0; k < Cfg<LATENT>::kSegSlots; ++k) mbar_init(smem_u32(&ctl.seg_ready[k]), 1);
     mbar_init(smem_u32(&ctl.pfull), kSoftmaxWarps);
     mbar_init(smem_u32(&ctl.pvdone), 1);
     mbar_init(smem_u32(&ctl.oempty), kSoftmaxWarps);
-    mbar_init(smem_u32(&ctl.drain), 1);
+    mbar_init(smem_u32(&ctl.drain), 2);
     ctl.abort = 0;
     fence_barrier_init();
   }
-  if (warp == kMmaWarp) tmem_alloc<kTmemCols>(smem_u32(&ctl.tmem));
+  if (warp == kScoreWarp) tmem_alloc<kTmemCols>(smem_u32(&ctl.tmem));
   __syncthreads();
   pdl_wait();  // everything below reads what earlier kernels wrote
 
@@ -410,20 +426,20 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl.tmem;
-  const uint32_t s_col = C::kOCols;  // two score buffers behind O^T
+  const uint32_t s_col = C::kOCols;  // score buffers behind O^T
   pdl_launch_dependents();           // the join may take its place; it waits for this grid's end
 
-  if (warp >= kMmaWarp + 1) {
+  if (warp >= kLoadWarp) {
     // ================================================================ loaders
     // Every warp of a team arrives once per part, after its share is issued
     // (TMA, whose bytes the barrier counts) or has landed (copies).
-    const int lw = warp - (kMmaWarp + 1), team = lw / kTeamWarps, tw = lw % kTeamWarps;
-    const int lt = tid - 32 * (kMmaWarp + 1) - team * kTeamThreads;
+    const int lw = warp - kLoadWarp, team = lw / kTeamWarps, tw = lw % kTeamWarps;
+    const int lt = tid - 32 * kLoadWarp - team * kTeamThreads;
     const int u = lt & 7, key0 = lt >> 3;                   // 16-byte unit of a 128-byte piece; first key
     constexpr int kPass = kTeamThreads / 8;                 // keys the team copies at a time
     constexpr int kFind = LATENT ? 64 / kPass : C::kRuns;   // positions a thread looks up: runs, or its listed keys
-    uint32_t g = 0;                                         // tiles before this segment
-    uint32_t issued = 0;                                    // this team's last tile, counted from 1
+    uint32_t g = 0;                                         // places of the ring before this segment
+    uint32_t issued = 0;                                    // this team's last place, counted from 1
     bool ok = true;
     // the next segment with rows behind an item of `tiles` tiles, or the end (rows 0), as segment k
     int item = ctl.run.item, start = ctl.run.start;
@@ -439,8 +455,8 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
         if (tiles > 0) n = segment_of(p, it, tiles, start, start, hi, member, lane, 32);
       } while (n.rows <= 0);
       if (lane == 0) {
-        ctl.seg[k % kSegSlots] = n;
-        mbar_arrive(smem_u32(&ctl.seg_ready[k % kSegSlots]));
+        ctl.seg[k % Cfg<LATENT>::kSegSlots] = n;
+        mbar_arrive(smem_u32(&ctl.seg_ready[k % Cfg<LATENT>::kSegSlots]));
       }
       __syncwarp();
     };
@@ -474,6 +490,8 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
         return q >= 0 && q < s.max_vis ? __ldg(p.block_table + table + (q >> p.page_shift)) : -1;
       };
       int i = s.lo + static_cast<int>((team + C::kTeams - g % C::kTeams) % C::kTeams);  // the team's first tile
+      const bool queries = LATENT && i == s.lo;                  // latent: place g of the ring takes the queries
+      if (LATENT) i += queries ? C::kTeams - 1 : -1;
       int32_t now[kFind], page[kFind], next[kFind];
 #pragma unroll
       for (int n = 0; n < kFind; ++n) {
@@ -482,18 +500,15 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
       }
 #pragma unroll
       for (int n = 0; n < kFind; ++n) page[n] = entry(now[n]);
-      // this team's share of the segment's queries, once the previous segment's
-      // products are done; the team that loads the first tile does that first
-      bool q_issued = false, q_landed = false, published = false;
+      // paged: the segment's queries, once the previous segment's products are done
+      bool q_issued = LATENT, q_landed = LATENT, published = false;
       const QuerySlot qs = query_slot(p, seg);
       const auto load_queries = [&] {
         q_issued = true;
         ok = warp_try(smem_u32(&ctl.qempty[qs.slot]), (qs.use & 1) ^ 1, abort_flag, p.err);
         if (!ok) return;
-        // the team without the first tile takes the first rows
-        const int turn = (team + 2 * C::kTeams - 1 - static_cast<int>(g % C::kTeams)) % C::kTeams;
 #pragma unroll 1
-        for (int r = turn * kPass + key0; r < ((s.rows + 15) & ~15); r += C::kTeams * kPass) {
+        for (int r = key0; r < ((s.rows + 15) & ~15); r += kPass) {
           const bool have = r < s.rows;
           const int x = s.c + (have ? r : 0), t = s.it.q0 + group_div(p, x), h = s.it.hk * p.group + group_mod(p, x);
           const uint16_t* src = p.q + t * p.q_row_stride + h * p.q_head_stride + u * 8;
@@ -507,10 +522,50 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
         if (lane == 0 && q_issued && !q_landed) mbar_arrive(smem_u32(&ctl.qfull[qs.slot]));
         q_landed = q_issued;
       };
-      if (i != s.lo) load_queries();
-      if (!ok) return;
+      if constexpr (LATENT) {
+        if (queries) {
+          // Eight pieces the way the copy to TMEM wants them, 128 rows a piece:
+          // 16 query rows of piece c, then the same rows of piece c + 4, for
+          // each quarter of the lanes.  The rotary piece has a place of its own,
+          // free when the previous segment's score products are done.
+          const uint32_t st = g % C::kStages, ph = ((g / C::kStages) & 1) ^ 1;
+          uint4 rot[kChunkRows / kPass];
+#pragma unroll
+          for (int n = 0; n < kChunkRows / kPass; ++n) {
+            const int r = n * kPass + key0;
+            const bool have = r < s.rows;
+            const int x = s.c + (have ? r : 0), t = s.it.q0 + group_div(p, x), h = s.it.hk * p.group + group_mod(p, x);
+            const uint16_t* src = p.q + t * p.q_row_stride + h * p.q_head_stride + u * 8;
+            if (n == 0) {
+#pragma unroll
+              for (int j = 0; j < C::kParts; ++j)
+                ok = ok && (g < C::kStages || warp_try(smem_u32(&ctl.kempty[st][j]), ph, abort_flag, p.err));
+              if (!ok) return;
+            }
+            const uint32_t dst = base + st * C::kStage + ((r >> 4) * 4 + ((r >> 3) & 1)) * 1024 + (r & 7) * 128 + ((u ^ (r & 7)) << 4);
+#pragma unroll
+            for (int c = 0; c < C::kQPieces; ++c)
+              cp_async_16_or_zero(dst + (c & 3) * (2 * C::kPiece) + (c >> 2) * 2048, src + c * 64, have);
+            rot[n] = have ? __ldg(reinterpret_cast<const uint4*>(src + C::kQPieces * 64)) : make_uint4(0, 0, 0, 0);
+          }
+          cp_async_commit();
+          if (lw == 0) publish(s.tiles, seg + 1);
+          published = true;
+          ok = warp_try(smem_u32(&ctl.qempty[0]), (seg & 1) ^ 1, abort_flag, p.err);
+          if (!ok) return;
+#pragma unroll
+          for (int n = 0; n < kChunkRows / kPass; ++n) {
+            const int r = n * kPass + key0;
+            *reinterpret_cast<uint4*>(smem + C::kOff_Q + r * 128 + ((u ^ (r & 7)) << 4)) = rot[n];
+          }
+          cp_async_wait_group<0>();
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane < C::kParts) mbar_arrive(smem_u32(&ctl.kfull[st][lane]));
+        }
+      }
       for (; i < s.hi; i += C::kTeams) {
-        const uint32_t x = g + (i - s.lo), st = x % C::kStages, ph = ((x / C::kStages) & 1) ^ 1;
+        const uint32_t x = g + LATENT + (i - s.lo), st = x % C::kStages, ph = ((x / C::kStages) & 1) ^ 1;
         const uint32_t stage = base + st * C::kStage;
         // what the table says: pages outside the cache hold no keys
         int32_t pos[kFind];
@@ -636,106 +691,145 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
           queries_landed();
         }
       }
-      if (!q_landed) {  // no tile of this segment was the team's
-        cp_async_wait_group<0>();
-        fence_proxy_async_smem();
-        __syncwarp();
-        queries_landed();
-      }
-      g += s.hi - s.lo;
-      if (lw == 0 && !published) publish(s.tiles, seg + 1);
+      g += LATENT + (s.hi - s.lo);
     });
     // after a time-out: this warp's copies land before the CTA can exit
     cp_async_wait_all();
-    if (!ok && lane == 0 && issued > 0) {
+    if (!ok && lane == 0) {
       int never = 0;
-      for (int j = 0; j < C::kParts; ++j)
-        mbar_wait(smem_u32(&ctl.kfull[(issued - 1) % C::kStages][j]), ((issued - 1) / C::kStages) & 1, &never, p.err);
+      for (uint32_t x = issued; x > 0 && x + C::kStages > issued; x -= min(x, static_cast<uint32_t>(C::kTeams)))
+        for (int j = 0; j < C::kParts; ++j)
+          mbar_wait(smem_u32(&ctl.kfull[(x - 1) % C::kStages][j]), ((x - 1) / C::kStages) & 1, &never, p.err);
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
-    // ================================================================ MMA issuer
-    // The whole warp runs this loop; one elected lane issues (always the same
-    // one: a commit covers its own thread's products).
+  } else if (warp >= kScoreWarp) {
+    // ================================================================ MMA issuers
+    // One warp issues the score products, one the value products: the tensor
+    // pipe's queue is short, and a warp spends about 100 cycles on each barrier
+    // and 50 on each commit, which the other's products cover.  The whole warp
+    // runs its loop; one elected lane issues (always the same one: a commit
+    // covers its own thread's products).
     uint32_t g = 0;
     bool ok = true;
     const uint32_t tm = uniform(tmem);
-    const uint32_t qk_idesc = uniform(idesc_f16(64, 64, DTYPE == FP4IDX_BF16, false, p.negate != 0));
-    const uint64_t q_desc = desc_sw128(base + C::kOff_Q, 16), p_desc = desc_sw128(base + C::kOff_P, 16);
-    // Order of the products: two score products, then their two value products
-    // (latent: the stages hold two tiles), or a score product two tiles ahead of
-    // each value product (paged).  A fixed order with blocking waits: choosing
-    // what is ready by polling cost 400 cycles at every hand-over.
-    for_segments<LATENT, false>(ctl, p.err, [&](const Segment& s, uint32_t seg) {
-      if (!ok) return;
-      const uint32_t pv_idesc = uniform(idesc_f16(128, (s.rows + 15) & ~15, DTYPE == FP4IDX_BF16, true, false));
-      const uint32_t n = uniform(s.hi - s.lo);
-      const QuerySlot qs = query_slot(p, seg);
-      const uint64_t qh_desc = q_desc + uniform(qs.slot * (kQueryHalf >> 4));
-      const auto score = [&](uint32_t i) {
-        const uint32_t x = g + i, st = uniform(x % C::kStages), use = (x / C::kStages) & 1, buf = x & 1;
-        const uint32_t d = tm + s_col + buf * TK;
-        const uint64_t k_desc = desc_sw128(base + st * C::kStage, 16);
-        ok = warp_try(smem_u32(&ctl.sempty[buf]), ((x >> 1) & 1) ^ 1, abort_flag, p.err);
+    if (warp == kScoreWarp) {
+      const uint32_t idesc = uniform(idesc_f16(64, 64, DTYPE == FP4IDX_BF16, false, p.negate != 0));
+      const uint64_t q_desc = desc_sw128(base + C::kOff_Q, 16);
+      for_segments<LATENT, false>(ctl, p.err, [&](const Segment& s, uint32_t seg) {
+        if (!ok) return;
+        const uint32_t n = uniform(s.hi - s.lo);
+        const QuerySlot qs = query_slot(p, seg);
+        const uint64_t qh_desc = q_desc + uniform(qs.slot * (kQueryHalf >> 4));
+        const uint32_t first = g + (LATENT ? seg + 1 : 0);  // place of the first tile in the ring
+        if constexpr (LATENT) {                             // the queries' place is the one before
+          const uint32_t st = uniform((first - 1) % C::kStages), use = ((first - 1) / C::kStages) & 1;
 #pragma unroll
-        for (int j = 0; j < (LATENT ? C::kParts : 1); ++j) {
-          ok = ok && warp_try(smem_u32(&ctl.kfull[st][j]), use, abort_flag, p.err);
+          for (int j = 0; j < C::kParts; ++j) ok = ok && warp_try(smem_u32(&ctl.kfull[st][j]), use, abort_flag, p.err);
+          if (!ok) return;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t from = desc_sw128(base + st * C::kStage, 16);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                tc_cp_128x256b(tm + C::kQCol + c * 32 + k * 8, from + c * (2 * C::kPiece >> 4) + k * 2);
+            tc_commit(smem_u32(&ctl.qfull[0]));
+          }
+          __syncwarp();
+        } else {
+          ok = warp_try(smem_u32(&ctl.qfull[qs.slot]), qs.use & 1, abort_flag, p.err);
+        }
+#pragma unroll 1
+        for (uint32_t i = 0; ok && i < n; ++i) {
+          const uint32_t x = g + i, buf = x & 1;
+          const uint32_t st = uniform((first + i) % C::kStages), use = ((first + i) / C::kStages) & 1;
+          const uint32_t d = tm + s_col + buf * TK;
+          const uint64_t k_desc = desc_sw128(base + st * C::kStage, 16);
+          ok = warp_try(smem_u32(&ctl.sempty[buf]), ((x >> 1) & 1) ^ 1, abort_flag, p.err);
+#pragma unroll
+          for (int j = 0; j < (LATENT ? C::kParts : 1); ++j) {
+            ok = ok && warp_try(smem_u32(&ctl.kfull[st][j]), use, abort_flag, p.err);
+            if (!ok) return;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int r = 0; r < C::kRuns; ++r)
+#pragma unroll
+                for (int c = 0; c < C::kPartPieces; ++c)
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {  // descriptor addresses count 16 bytes
+                    const uint64_t b = k_desc + (j * C::kPart >> 4) + (r * C::kPartPieces + c) * (C::kPiece >> 4) + k * 2;
+                    if constexpr (LATENT) {  // both halves of the queries, each into its own lanes
+                      const int step = (j * C::kPartPieces + c) * 4 + k, half = step / (C::kQPieces * 2), at = step % (C::kQPieces * 2);
+                      if (step < C::kQPieces * 4)
+                        tc_mma_f16_tmem(d + half * kUpper, tm + C::kQCol + half * kUpper + at * 8, b, idesc, at > 0);
+                      else
+                        tc_mma_f16(d, q_desc + k * 2, b, idesc, 1);
+                    } else {
+                      tc_mma_f16(d + r * 64, qh_desc + c * (kChunkRows * 8) + k * 2, b, idesc, c + k > 0);
+                    }
+                  }
+              if (!LATENT || j == C::kParts - 1) {
+                if constexpr (!LATENT) tc_commit(smem_u32(&ctl.kempty[st][0]));  // the keys' last reader
+                tc_commit(smem_u32(&ctl.sfull[buf]));
+                if (i + 1 == n) tc_commit(smem_u32(&ctl.qempty[qs.slot]));
+              }
+            }
+            __syncwarp();
+          }
+        }
+        g += n;
+      });
+    } else {
+      const uint64_t p_base = desc_sw128(base + C::kOff_P, 16);
+      for_segments<LATENT, false>(ctl, p.err, [&](const Segment& s, uint32_t seg) {
+        if (!ok) return;
+        const uint32_t idesc = uniform(idesc_f16(128, (s.rows + 15) & ~15, DTYPE == FP4IDX_BF16, true, false));
+        const uint32_t n = uniform(s.hi - s.lo);
+        if constexpr (LATENT) {
+          // The queries are in TMEM: their place of the ring is free, but only
+          // released behind the value products of the places before it.  The
+          // loader teams take places in turn, and the parity that a team waits
+          // for tells two uses of a stage apart only if places come free in order.
+          const uint32_t place = g + seg, st = uniform(place % C::kStages);
+          ok = warp_try(smem_u32(&ctl.qfull[0]), seg & 1, abort_flag, p.err);
+          if (!ok) return;
+          if (elect_one()) {
+#pragma unroll
+            for (int j = 0; j < C::kParts; ++j) tc_commit(smem_u32(&ctl.kempty[st][j]));
+          }
+          __syncwarp();
+        }
+        ok = warp_try(smem_u32(&ctl.oempty), (seg & 1) ^ 1, abort_flag, p.err);
+#pragma unroll 1
+        for (uint32_t i = 0; ok && i < n; ++i) {
+          const uint32_t x = g + i, place = x + (LATENT ? seg + 1 : 0), st = uniform(place % C::kStages), more = i > 0;
+          const uint64_t v_desc = desc_sw128(base + st * C::kStage + C::kV, C::kPiece);
+          const uint64_t p_desc = p_base + (LATENT ? st * (C::kStage >> 4) : 0);
+          if constexpr (!LATENT)
+            ok = warp_try(smem_u32(&ctl.kfull[st][1]), (place / C::kStages) & 1, abort_flag, p.err);
+          ok = ok && warp_try(smem_u32(&ctl.pfull), x & 1, abort_flag, p.err);
           if (!ok) return;
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll
-            for (int r = 0; r < C::kRuns; ++r)
+            for (int d = 0; d < C::kDv / 128; ++d) {
 #pragma unroll
-              for (int c = 0; c < C::kPartPieces; ++c)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)  // descriptor addresses count 16 bytes
-                  tc_mma_f16(d + r * 64, qh_desc + (j * C::kPartPieces + c) * (kChunkRows * 8) + k * 2,
-                             k_desc + (j * C::kPart >> 4) + (r * C::kPartPieces + c) * (C::kPiece >> 4) + k * 2, qk_idesc,
-                             j + c + k > 0);
-            if (!LATENT || j == C::kParts - 1) {
-              if constexpr (!LATENT) tc_commit(smem_u32(&ctl.kempty[st][0]));  // the keys' last reader
-              tc_commit(smem_u32(&ctl.sfull[buf]));
-              if (i + 1 == n) tc_commit(smem_u32(&ctl.qempty[qs.slot]));
+              for (int k = 0; k < TK / 16; ++k)
+                tc_mma_f16(tm + d * kChunkRows, v_desc + (d * 2 + (k >> 2) * C::kPartPieces) * (C::kPiece >> 4) + (k & 3) * 128,
+                           p_desc + (k >> 2) * (kChunkRows * 8) + (k & 3) * 2, idesc, k > 0 ? 1u : more);
+              // 128 values are pieces 2d and 2d+1; part j of a latent tile is pieces 3j .. 3j+2
+              if (LATENT && d > 0) tc_commit(smem_u32(&ctl.kempty[st][d - 1]));
             }
+            if constexpr (!LATENT) tc_commit(smem_u32(&ctl.kempty[st][1]));
+            tc_commit(smem_u32(&ctl.pvdone));
           }
           __syncwarp();
         }
-      };
-      const auto value = [&](uint32_t i) {
-        const uint32_t x = g + i, st = uniform(x % C::kStages), more = i > 0;
-        const uint64_t v_desc = desc_sw128(base + st * C::kStage + C::kV, C::kPiece);
-        if (i == 0) ok = warp_try(smem_u32(&ctl.oempty), (seg & 1) ^ 1, abort_flag, p.err);
-        if constexpr (!LATENT)
-          ok = ok && warp_try(smem_u32(&ctl.kfull[st][1]), (x / C::kStages) & 1, abort_flag, p.err);
-        ok = ok && warp_try(smem_u32(&ctl.pfull), x & 1, abort_flag, p.err);
-        if (!ok) return;
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int d = 0; d < C::kDv / 128; ++d) {
-#pragma unroll
-            for (int k = 0; k < TK / 16; ++k)
-              tc_mma_f16(tm + d * kChunkRows, v_desc + (d * 2 + (k >> 2) * C::kPartPieces) * (C::kPiece >> 4) + (k & 3) * 128,
-                         p_desc + (k >> 2) * (kChunkRows * 8) + (k & 3) * 2, pv_idesc, k > 0 ? 1u : more);
-            // 128 values are pieces 2d and 2d+1; part j of a latent tile is pieces 3j .. 3j+2
-            if (LATENT && d > 0) tc_commit(smem_u32(&ctl.kempty[st][d - 1]));
-          }
-          if constexpr (!LATENT) tc_commit(smem_u32(&ctl.kempty[st][1]));
-          tc_commit(smem_u32(&ctl.pvdone));
-        }
-        __syncwarp();
-      };
-      ok = warp_try(smem_u32(&ctl.qfull[qs.slot]), qs.use & 1, abort_flag, p.err);
-      uint32_t scored = 0;
-#pragma unroll 1
-      for (uint32_t i = 0; ok && i < n; ++i) {
-        const uint32_t ahead = min(n, (LATENT ? i & ~1u : i) + 2);
-#pragma unroll 1
-        for (; ok && scored < ahead; ++scored) score(scored);
-        if (ok) value(i);
-      }
-      g += n;
-    });
+        g += n;
+      });
+    }
     // no product is in flight when TMEM is freed
     if (elect_one()) tc_commit(smem_u32(&ctl.drain));
     __syncwarp();
@@ -752,7 +846,7 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
     bool ok = true;
     const int r0 = 16 * warp + (lane >> 2);                 // this thread's rows: r0 and r0 + 8
     const uint32_t quarter = static_cast<uint32_t>(warp) << 21;  // TMEM lanes 32 * warp
-    for_segments<LATENT, true>(ctl, p.err, [&](const Segment& s, uint32_t) {
+    for_segments<LATENT, true>(ctl, p.err, [&](const Segment& s, uint32_t seg) {
       // rows past the chunk's end have zero queries: their scores are harmless
       int vis[2];
 #pragma unroll
@@ -767,13 +861,13 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
       float m[2] = {-INFINITY, -INFINITY};                   // reference maximum, in powers of two
       float2 l[2] = {};                                      // this thread's share of the sums
       for (int i = s.lo; i < s.hi; ++i, ++g) {
-        const uint32_t buf = g & 1, st = g % C::kStages;
+        const uint32_t buf = g & 1, place = g + (LATENT ? seg + 1 : 0), st = place % C::kStages;
         float x[TK / 2];
         bool raise = false;
         float f[2] = {1.0f, 1.0f};
         if (active) {
           if (ok) ok = warp_try(smem_u32(&ctl.sfull[buf]), (g >> 1) & 1, abort_flag, p.err);
-          if (ok) ok = warp_try(smem_u32(&ctl.kfull[st][C::kPosPart]), (g / C::kStages) & 1, abort_flag, p.err);
+          if (ok) ok = warp_try(smem_u32(&ctl.kfull[st][C::kPosPart]), (place / C::kStages) & 1, abort_flag, p.err);
           tc_fence_after();
           static_assert(kTeamWarps == 4, "holes of a stage are read as one word");
           const bool mask = i >= full_tiles || *reinterpret_cast<const uint32_t*>(ctl.holes[st]) != 0;
@@ -781,12 +875,24 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
           for (int c = 0; c < TK / 64; ++c) {
             uint32_t r[32];
             tmem_ld_16x256b_x8(tmem + quarter + s_col + buf * TK + c * 64, r);
-            tmem_wait_ld();
-            reg_fence(r);
+            if constexpr (LATENT) {  // the sums over the two halves of the query
+              uint32_t upper[32];
+              tmem_ld_16x256b_x8(tmem + quarter + kUpper + s_col + buf * TK, upper);
+              tmem_wait_ld();
+              reg_fence(r);
+              reg_fence(upper);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[c * 32 + e] = __uint_as_float(r[e]);
+              for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(r[e]) + __uint_as_float(upper[e]);
+            } else {
+              tmem_wait_ld();
+              reg_fence(r);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x[c * 32 + e] = __uint_as_float(r[e]);
+            }
           }
           tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ctl.sempty[buf]));
           if (mask) {
 #pragma unroll
             for (int j = 0; j < TK / 8; ++j) {
@@ -813,8 +919,7 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
             }
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctl.sempty[buf]));
+        if (!active && lane == 0) mbar_arrive(smem_u32(&ctl.sempty[buf]));
         const bool any = bar_red_or(1, 32 * kSoftmaxWarps, raise);
         uint32_t w[TK / 4];
         if (active) {
@@ -839,10 +944,10 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
             w[2 * j + 1] = pack2<DTYPE>(b.x, b.y);
           }
         }
-        // the previous product has read P and updated O^T
+        // the previous product has read P (paged) and updated O^T
         if (ok && g > 0) ok = warp_try(smem_u32(&ctl.pvdone), (g - 1) & 1, abort_flag, p.err);
         if (active) {
-          uint8_t* prow = smem + C::kOff_P + r0 * 128 + (lane & 3) * 4;
+          uint8_t* prow = smem + C::kOff_P + (LATENT ? st * C::kStage : 0) + r0 * 128 + (lane & 3) * 4;
 #pragma unroll
           for (int j = 0; j < TK / 8; ++j) {
             uint8_t* at = prow + (j >> 3) * (kChunkRows * 128) + (((j & 7) ^ (r0 & 7)) << 4);
@@ -852,6 +957,8 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
           fence_proxy_async_smem();
         }
         if (any && i > s.lo) {
+          const bool grown = __any_sync(0xffffffffu, raise);
+          if (lane == 0) ctl.grown[warp] = grown;
           if ((lane & 3) == 0) {
             ctl.factor[r0] = f[0];
             ctl.factor[r0 + 8] = f[1];
@@ -859,16 +966,20 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
           bar_sync(2, 32 * kSoftmaxWarps);
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < C::kDv / 128 * cols; c += 16) {
-            const int d = c / cols, col = c - d * cols;
-            const uint32_t at = tmem + quarter + d * kChunkRows + col;
-            uint32_t r[16];
-            tmem_ld(at, r);
-            tmem_wait_ld();
-            reg_fence(r);
+          for (int c = 0; c < cols; c += 16) {
+            if (!ctl.grown[c >> 4]) continue;
+#pragma unroll 1
+            for (int d = 0; d < C::kDv / 128; ++d) {
+              const uint32_t at = tmem + quarter + d * kChunkRows + c;
+              uint32_t r[16];
+              __syncwarp();
+              tmem_ld(at, r);
+              tmem_wait_ld();
+              reg_fence(r);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * ctl.factor[col + e]);
-            tmem_st_x16(at, r);
+              for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * ctl.factor[c + e]);
+              tmem_st_x16(at, r);
+            }
           }
           tmem_wait_st();
           tc_fence_before();
@@ -938,7 +1049,7 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
     tc_fence_before();
   }
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     tc_fence_after();
     tmem_dealloc<kTmemCols>(tmem);
   }
@@ -1097,7 +1208,7 @@ bool plan_attention(AttnParams* p, int sms) {
   const int64_t items = static_cast<int64_t>(p->indices ? p->num_rows : p->num_seqs) * p->num_kv_heads * cg;
   if (items > INT32_MAX || p->max_seqlen_q > kMaxRowsOfRequest) return false;
   p->group_mul = ((uint64_t{1} << kGroupShift) + p->group - 1) / p->group;
-  p->two_queries = pairs <= 32;
+  p->two_queries = !latent && pairs <= 32;
   p->chunk_groups = static_cast<int32_t>(cg);
   p->items = static_cast<int32_t>(items);
   const int tk = latent ? Cfg<true>::kTk : Cfg<false>::kTk;

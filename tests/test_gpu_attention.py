@@ -327,3 +327,17 @@ def test_every_way_of_cutting_items(requests, length, kv, heads):
     # whole items, items cut alike, equal runs over all items: chosen by sizes alone
     lens = [max(1, length - 37 * (i % 5)) for i in range(requests)]
     run_case(requests + length, [1] * requests, lens, heads=heads, kv_heads=kv, visibility="full")
+
+
+@pytest.mark.parametrize("kv,heads,select", [(None, 128, 0), (None, 16, 0), (None, 64, 300), (4, 32, 0), (4, 32, 3)])
+def test_many_short_items_in_a_row(kv, heads, select):
+    # several items of one to ten tiles per CTA, whole and cut: the ring carries on from item to item
+    n = 700
+    lengths = [1 + (i * 2654435761 >> 7) % 600 for i in range(n)]
+    c = R.make_case(26, [1] * n, lengths, heads=heads, kv_heads=kv, select=select, device="cuda")
+    a = build(c)
+    first = [x.clone() for x in call(a)]
+    check(c, first)
+    for _ in range(20):
+        a.out.zero_()
+        assert all(torch.equal(x, y) for x, y in zip(first, call(a)))
