@@ -40,6 +40,7 @@
 //               gather of four rows by TMA (tile::gather4) moves 512 bytes an
 //               instruction and reached 6.7-8.7 TB/s from L2 where the copies
 //               reach 20.
+//   last warp   planner: the segments (runs of one item's tiles) to come.
 // A tile arrives and leaves in parts (latent: three times 192 of the 576
 // values; paged: keys, values): the score product starts with the first part
 // and a part is loaded again as soon as its last product is done.  A latent
@@ -52,7 +53,9 @@
 // for different row chunks, close enough in time for the L2 to serve the
 // second reader.  An item cut by a boundary leaves partial sums that
 // join_kernel adds in a fixed order.
+#include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstddef>
 #include <cstring>
 
@@ -84,11 +87,9 @@ struct Cfg {
   static constexpr int kParts = LATENT ? 3 : 2;                 // parts of a stage that arrive and leave alone
   static constexpr int kPosPart = LATENT ? 0 : 1;               // the part whose barriers guard the positions: it leaves after the softmax
   static constexpr int kTeams = LATENT ? 2 : 1;
-  // Slots of planned segments: a team plans the next one behind its first load
-  // in a segment, which waited for the products kStages places before: no role
-  // still reads the segment whose slot is taken.
-  static constexpr int kSegSlots = kStages + 1;
-  static constexpr int kThreads = 32 * (kLoadWarp + kTeams * kTeamWarps);
+  static constexpr int kSegSlots = 4;                           // planned segments
+  static constexpr int kPlanWarp = kLoadWarp + kTeams * kTeamWarps;  // the last one
+  static constexpr int kThreads = 32 * (kPlanWarp + 1);
   static constexpr int kKc = kDk / 64;                          // 128-byte pieces of a key
   static constexpr int kPartPieces = LATENT ? kLatentBoxPieces : kPagedBoxPieces;  // pieces of a part, per run
   static constexpr uint32_t kPiece = 64 * 128;                  // one piece of a run's keys
@@ -133,13 +134,13 @@ struct Run {
   int lo, hi, item, start, end;
 };
 
-// Segments are worked out by one loader warp and read by all roles.
+// Segments are worked out by a warp of its own, ahead of the roles that read them.
 template <bool LATENT>
 struct Control {
   uint64_t kfull[Cfg<LATENT>::kStages][Cfg<LATENT>::kParts], kempty[Cfg<LATENT>::kStages][Cfg<LATENT>::kParts];
   uint64_t sfull[2], sempty[2], pfull, pvdone, qfull[2], qempty[2], oempty, drain;
   int64_t row_off[kChunkRows];                                 // output element of each row
-  uint64_t seg_ready[Cfg<LATENT>::kSegSlots];
+  uint64_t seg_ready[Cfg<LATENT>::kSegSlots], seg_free[Cfg<LATENT>::kSegSlots];
   Segment seg[Cfg<LATENT>::kSegSlots];
   Run run;
   alignas(8) int32_t key_pos[Cfg<LATENT>::kStages][Cfg<LATENT>::kTk];  // logical position, -1: no key (read in pairs)
@@ -272,6 +273,8 @@ __device__ __forceinline__ void for_segments(Control<LATENT>& ctl, uint32_t* err
     if (SOFTMAX) ok = !bar_red_or(1, 32 * kSoftmaxWarps, !ok);
     if (!ok) return;
     const Segment s = ctl.seg[k % Cfg<LATENT>::kSegSlots];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&ctl.seg_free[k % Cfg<LATENT>::kSegSlots]));
     if (s.rows <= 0) return;
     f(s, k);
   }
@@ -285,6 +288,33 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   else
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+// One value dimension a lane (dimension q = lane / 4 of eight), 16 rows (v) ->
+// all eight dimensions of rows q and q + 8: three exchanges between lanes whose
+// q differs in one bit, each lane keeping the rows that have its bit.
+template <int DTYPE>
+__device__ __forceinline__ void rows_to_lanes(const float (&v)[16], int q, uint4 (&out)[2]) {
+  const bool b0 = q & 1, b1 = q & 2, b2 = q & 4;
+  uint32_t w[8];  // two dimensions of row 2 i + b0
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const uint32_t even = pack2<DTYPE>(v[2 * i], v[2 * i + 2]), odd = pack2<DTYPE>(v[2 * i + 1], v[2 * i + 3]);
+    const uint32_t mine = b0 ? odd : even, theirs = __shfl_xor_sync(0xffffffffu, b0 ? even : odd, 4);
+    w[i] = __byte_perm(mine, theirs, b0 ? 0x1054 : 0x5410);
+    w[i + 1] = __byte_perm(mine, theirs, b0 ? 0x3276 : 0x7632);
+  }
+  uint2 u[4];  // four dimensions of row 4 i + 2 b1 + b0
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t mine = b1 ? w[2 * i + 1] : w[2 * i], theirs = __shfl_xor_sync(0xffffffffu, b1 ? w[2 * i] : w[2 * i + 1], 8);
+    u[i] = b1 ? make_uint2(theirs, mine) : make_uint2(mine, theirs);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint2 mine = b2 ? u[2 * i + 1] : u[2 * i], send = b2 ? u[2 * i] : u[2 * i + 1];
+    const uint2 theirs = make_uint2(__shfl_xor_sync(0xffffffffu, send.x, 16), __shfl_xor_sync(0xffffffffu, send.y, 16));
+    out[i] = b2 ? make_uint4(theirs.x, theirs.y, mine.x, mine.y) : make_uint4(mine.x, mine.y, theirs.x, theirs.y);
+  }
 }
 // ln(sum) of a row with reference maximum m (in powers of two) and sum l.
 __device__ __forceinline__ float row_lse(float m, float l) {
@@ -323,7 +353,10 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
       mbar_init(smem_u32(&ctl.qfull[s]), LATENT ? 1 : kTeamWarps);
       mbar_init(smem_u32(&ctl.qempty[s]), 1);
     }
-    for (int k = 0; k < Cfg<LATENT>::kSegSlots; ++k) mbar_init(smem_u32(&ctl.seg_ready[k]), 1);
+    for (int k = 0; k < C::kSegSlots; ++k) {
+      mbar_init(smem_u32(&ctl.seg_ready[k]), 1);
+      mbar_init(smem_u32(&ctl.seg_free[k]), C::kPlanWarp);
+    }
     mbar_init(smem_u32(&ctl.pfull), kSoftmaxWarps);
     mbar_init(smem_u32(&ctl.pvdone), 1);
     mbar_init(smem_u32(&ctl.oempty), kSoftmaxWarps);
@@ -429,7 +462,37 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
   const uint32_t s_col = C::kOCols;  // score buffers behind O^T
   pdl_launch_dependents();           // the join may take its place; it waits for this grid's end
 
-  if (warp >= kLoadWarp) {
+  if (warp == C::kPlanWarp) {
+    // ================================================================ planner
+    // The segments behind the first one, up to kSegSlots ahead: an item's lengths
+    // are several dependent loads away.
+    const int lo = ctl.run.lo, hi = ctl.run.hi, end = ctl.run.end;
+    if (lo < hi) {
+      int item = ctl.run.item, start = ctl.run.start, tiles = ctl.seg[0].tiles;
+      Segment n;
+      n.rows = ctl.seg[0].rows;
+      bool done = false;
+#pragma unroll 1
+      for (uint32_t k = n.rows > 0 ? 1 : 0; !done; ++k) {
+        do {
+          start += tiles;
+          n.rows = 0;
+          done = start >= hi || ++item >= end;
+          if (done) break;
+          const Item it = item_of(p, item);
+          tiles = item_tiles<TK>(p, it, lane, 32);
+          if (tiles > 0) n = segment_of(p, it, tiles, start, start, hi, member, lane, 32);
+        } while (n.rows <= 0);
+        const uint32_t slot = k % C::kSegSlots;
+        if (k >= C::kSegSlots && !warp_try(smem_u32(&ctl.seg_free[slot]), (k / C::kSegSlots - 1) & 1, abort_flag, p.err)) break;
+        if (lane == 0) {
+          ctl.seg[slot] = n;
+          mbar_arrive(smem_u32(&ctl.seg_ready[slot]));
+        }
+        __syncwarp();
+      }
+    }
+  } else if (warp >= kLoadWarp) {
     // ================================================================ loaders
     // Every warp of a team arrives once per part, after its share is issued
     // (TMA, whose bytes the barrier counts) or has landed (copies).
@@ -441,26 +504,6 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
     uint32_t g = 0;                                         // places of the ring before this segment
     uint32_t issued = 0;                                    // this team's last place, counted from 1
     bool ok = true;
-    // the next segment with rows behind an item of `tiles` tiles, or the end (rows 0), as segment k
-    int item = ctl.run.item, start = ctl.run.start;
-    const auto publish = [&](int tiles, uint32_t k) {
-      Segment n;
-      const int hi = ctl.run.hi, end = ctl.run.end;
-      do {
-        start += tiles;
-        n.rows = 0;
-        if (start >= hi || ++item >= end) break;
-        const Item it = item_of(p, item);
-        tiles = item_tiles<TK>(p, it, lane, 32);
-        if (tiles > 0) n = segment_of(p, it, tiles, start, start, hi, member, lane, 32);
-      } while (n.rows <= 0);
-      if (lane == 0) {
-        ctl.seg[k % Cfg<LATENT>::kSegSlots] = n;
-        mbar_arrive(smem_u32(&ctl.seg_ready[k % Cfg<LATENT>::kSegSlots]));
-      }
-      __syncwarp();
-    };
-    if (lw == 0 && ctl.run.lo < ctl.run.hi && ctl.seg[0].rows <= 0) publish(ctl.seg[0].tiles, 0);
     for_segments<LATENT, false>(ctl, p.err, [&](const Segment& s, uint32_t seg) {
       if (!ok) return;
       const int64_t table = attn_table_base(p, s.it.b);
@@ -501,7 +544,7 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
 #pragma unroll
       for (int n = 0; n < kFind; ++n) page[n] = entry(now[n]);
       // paged: the segment's queries, once the previous segment's products are done
-      bool q_issued = LATENT, q_landed = LATENT, published = false;
+      bool q_issued = LATENT, q_landed = LATENT;
       const QuerySlot qs = query_slot(p, seg);
       const auto load_queries = [&] {
         q_issued = true;
@@ -549,8 +592,6 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
             rot[n] = have ? __ldg(reinterpret_cast<const uint4*>(src + C::kQPieces * 64)) : make_uint4(0, 0, 0, 0);
           }
           cp_async_commit();
-          if (lw == 0) publish(s.tiles, seg + 1);
-          published = true;
           ok = warp_try(smem_u32(&ctl.qempty[0]), (seg & 1) ^ 1, abort_flag, p.err);
           if (!ok) return;
 #pragma unroll
@@ -660,10 +701,6 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
         if (!q_issued) {
           load_queries();
           if (!ok) return;
-        }
-        if (lw == 0 && !published) {
-          publish(s.tiles, seg + 1);
-          published = true;
         }
         // look ahead while the loads are under way
 #pragma unroll
@@ -1015,31 +1052,76 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
       if (ok) ok = warp_try(smem_u32(&ctl.pvdone), (g - 1) & 1, abort_flag, p.err);
       bar_sync(2, 32 * kSoftmaxWarps);
       tc_fence_after();
+      if (LATENT && whole) {
+        // Row fragments of 16 dimensions: this lane has dimension lane / 4 (and
+        // that + 8) of rows 8 j + 2 (lane % 4) + {0, 1}; after an exchange, 16
+        // dimensions of two rows.
+        const int q = lane >> 2, mine = 2 * (lane & 3);
+        int row[2];
+        int64_t off[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          row[n] = 8 * (4 * n + (q >> 1)) + mine + (q & 1);
+          off[n] = ctl.row_off[row[n]] + 32 * warp;
+        }
+        float2 inv[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) inv[j] = *reinterpret_cast<const float2*>(&ctl.row_inv[8 * j + mine]);
 #pragma unroll 1
-      for (int c = 0; c < C::kDv / 128 * cols; c += 16) {
-        const int d = c / cols, col = c - d * cols;
-        const int dv = d * 128 + tid;  // this thread's value dimension (tid < 128)
-        uint32_t r[16];
-        tmem_ld(tmem + quarter + d * kChunkRows + col, r);
-        tmem_wait_ld();
-        reg_fence(r);
-        if (!ok) continue;
-        if (whole) {
-          // neighbouring lanes swap rows so that each stores two values of one row
+        for (int i = 0; i < C::kDv / 64; ++i) {
+          uint32_t r[32];
+          __syncwarp();
+          tmem_ld_16x256b_x8(tmem + quarter + (i >> 1) * kChunkRows + (i & 1) * kUpper, r);
+          tmem_wait_ld();
+          reg_fence(r);
+          uint4 w[2][2];
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            const int row = col + e + (lane & 1);
-            const float a = __uint_as_float(r[e]) * ctl.row_inv[col + e];
-            const float b = __uint_as_float(r[e + 1]) * ctl.row_inv[col + e + 1];
-            const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : b, 1);
-            const uint32_t v = lane & 1 ? pack2<DTYPE>(other, b) : pack2<DTYPE>(a, other);
-            if (row < s.rows) *reinterpret_cast<uint32_t*>(p.out + ctl.row_off[row] + (dv & ~1)) = v;
+          for (int o = 0; o < 2; ++o) {
+            float v[16];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              v[2 * j] = __uint_as_float(r[4 * j + 2 * o]) * inv[j].x;
+              v[2 * j + 1] = __uint_as_float(r[4 * j + 2 * o + 1]) * inv[j].y;
+            }
+            rows_to_lanes<DTYPE>(v, q, w[o]);
           }
-        } else {
-          float* o = p.partial + (slot * kChunkRows + col) * C::kDv + dv;
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (col + e < s.rows) o[e * C::kDv] = __uint_as_float(r[e]);
+          for (int n = 0; n < 2; ++n) {
+            if (ok && row[n] < s.rows) {
+              uint4* to = reinterpret_cast<uint4*>(p.out + off[n] + (i >> 1) * 128 + (i & 1) * 16);
+              to[0] = w[0][n];
+              to[1] = w[1][n];
+            }
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < C::kDv / 128 * cols; c += 16) {
+          const int d = c / cols, col = c - d * cols;
+          const int dv = d * 128 + tid;  // this thread's value dimension (tid < 128)
+          uint32_t r[16];
+          __syncwarp();
+          tmem_ld(tmem + quarter + d * kChunkRows + col, r);
+          tmem_wait_ld();
+          reg_fence(r);
+          if (!ok) continue;
+          if (!LATENT && whole) {
+            // neighbouring lanes swap rows so that each stores two values of one row
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const int row = col + e + (lane & 1);
+              const float a = __uint_as_float(r[e]) * ctl.row_inv[col + e];
+              const float b = __uint_as_float(r[e + 1]) * ctl.row_inv[col + e + 1];
+              const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : b, 1);
+              const uint32_t v = lane & 1 ? pack2<DTYPE>(other, b) : pack2<DTYPE>(a, other);
+              if (row < s.rows) *reinterpret_cast<uint32_t*>(p.out + ctl.row_off[row] + (dv & ~1)) = v;
+            }
+          } else {
+            float* o = p.partial + (slot * kChunkRows + col) * C::kDv + dv;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (col + e < s.rows) o[e * C::kDv] = __uint_as_float(r[e]);
+          }
         }
       }
       tc_fence_before();
@@ -1219,22 +1301,29 @@ bool plan_attention(AttnParams* p, int sms) {
   if (most > INT32_MAX) return false;
   int64_t groups = sms / p->members;
   if (groups > kJoinThreads) groups = kJoinThreads;  // the join looks at one group per thread
-  // How are the items cut?  In tiles' time of the longest run:
+  // How are the items cut?  In tiles' time:
   //   whole items: no partial sums and no join;
   //   each item into an equal number of runs: partial sums and a join, which
   //     cost as much as two (latent) or three (paged) tiles;
   //   equal runs over all items: every group busy, but most CTAs also cross from
   //     one item to the next, five tiles in all.
-  // Measured, whole against cut into single tiles: one request of 2 / 3 latent
-  // tiles 9.8 / 11.7 against 10.8 / 10.8 us, of 3 / 5 paged tiles 8.1 / 10.0
-  // against 9.0 / 9.0 us; whole against equal runs: 64 requests of 4 latent tiles
-  // 13.1 against 16.0 us, 160 items of 4 / 6 paged tiles 17.6 / 23.0 against
-  // 19.6 / 23.3 us.
-  const int64_t longest = per_item < 1 ? 1 : per_item;
-  const int64_t whole = (items + groups - 1) / groups * longest;
-  int64_t cuts = groups / items < longest ? groups / items : longest;
-  const int64_t cut = cuts > 1 ? (longest + cuts - 1) / cuts + (latent ? 2 : 3) : INT64_MAX;
-  const int64_t equal = longest * items / groups + 5;
+  // Lists have one length, so that HBM, which feeds as many CTAs as `feeds`,
+  // bounds each form from below; a prefix may be far shorter than max_seqlen_k.
+  // Measured, whole against cut: one request of 2 / 3 / 4 latent tiles 10.4 /
+  // 11.5 / 12.6 against 10.4 / 10.5 / 10.6 us, of 3 / 4 / 5 paged tiles 8.4 / 9.1
+  // / 9.9 against 9.7 / 9.4 / 9.2 us, 64 requests of 3 / 12 latent tiles 11.7 /
+  // 23.1 against 13.9 / 22.8 us, 96 items of 8-32 paged tiles 36.2 against 32.2;
+  // whole against equal runs: 160 items of 4 / 6 / 8 paged tiles 18.1 / 22.7 /
+  // 27.2 against 19.6 / 23.2 / 25.8 us, 256 listed items of 16 49.3 against 53.5 us.
+  const double feeds = !p->indices ? HUGE_VAL : latent ? 90 : 86;
+  const double longest = per_item < 1 ? 1 : static_cast<double>(per_item);
+  const int64_t rest = items % groups;
+  const double hbm = longest * items / feeds;
+  const double whole = longest * (static_cast<double>(items / groups) * std::max(1.0, groups / feeds) +
+                                  (rest ? std::max(1.0, rest / feeds) : 0.0));
+  const int64_t cuts = std::min(groups / items, per_item);
+  const double cut = cuts > 1 ? std::max(static_cast<double>((per_item + cuts - 1) / cuts), hbm) + (latent ? 2 : 3) : HUGE_VAL;
+  const double equal = std::max(longest * items / groups, hbm) + 5;
   p->whole_items = whole < cut && whole <= equal;
   if (!p->whole_items && cut <= equal) groups = cuts * items;
   const int64_t units = p->whole_items ? items : most;
