@@ -53,6 +53,12 @@
 // for different row chunks, close enough in time for the L2 to serve the
 // second reader.  An item cut by a boundary leaves partial sums that
 // join_kernel adds in a fixed order.
+//
+// Measured (bf16): latent, 16 rows x 128 heads over 30,001-119,999 keys 335 us
+// (1,387 MB, 4.1 TB/s; 1,024 rows x 128 heads over 2,048 listed keys each 617
+// us, 946 TFLOP/s: both bound by the products, M = 64 at half rate); paged, 64
+// rows x 32 heads over 8,191-32,768 keys 110 us (6.1 TB/s, 90 % of a copy), 64
+// rows x 16 listed blocks 48 us (5.4 TB/s); single rows 8-11 us (latency).
 #include <algorithm>
 #include <atomic>
 #include <cmath>
