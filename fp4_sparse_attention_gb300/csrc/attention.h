@@ -50,7 +50,7 @@ struct AttnParams {
   int32_t chunk_groups; // row-chunk groups of one (request, K/V head)
   int32_t groups;       // CTA groups of the grid
   int32_t items;        // (request or row) x K/V head x chunk group
-  int32_t two_queries;  // at most 32 rows a CTA: two segments' queries are held
+  int32_t two_queries;  // paged, at most 32 rows a CTA: two segments' queries are held
   int32_t whole_items;  // runs are whole items: no partial sums
   int32_t list_tiles;   // key tiles of an item with a selection (0: whole prefix)
   // workspace
