@@ -535,7 +535,7 @@ class DeviceAttention:
     cache [P,page,576].  Paged attention: q [T,H,128], k and v [P,Hkv,page,128].
     cu_seqlens_q/k [B+1] i32, block_table [B,stride] (or flat with page_offsets
     [B]), visible_len [T], causal, qo_offset [B]; indices [T,n] (latent) or
-    [Hkv,T,n] (paged) i32, or None for the whole prefix.  out, lse and the
+    [Hkv,T,n] (paged) i32, n >= 1, or None for the whole prefix.  out, lse and the
     workspace are allocated here unless given, and kept: a call writes the same
     tensors again.  The object holds pointers: rebuild it when a tensor moves.
     """
@@ -569,6 +569,8 @@ class DeviceAttention:
         if indices is not None and (indices.dtype != torch.int32 or not indices.is_contiguous()
                                     or tuple(indices.shape[:-1]) != ((T,) if latent else (kv_heads, T))):
             raise ValueError("indices must be contiguous int32 [T, n] (latent) or [Hkv, T, n] (paged)")
+        if indices is not None and indices.shape[-1] == 0:  # its null pointer would mean the whole prefix
+            raise ValueError("indices must list at least one position or block (-1: none)")
         if out is None:
             out = torch.empty((T, H, dv), dtype=q.dtype, device=q.device)
         if lse is None:
