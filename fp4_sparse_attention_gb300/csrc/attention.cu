@@ -251,6 +251,22 @@ __device__ __forceinline__ Segment segment_of(const AttnParams& p, const Item& i
   return s;
 }
 
+// Rows behind the requests' (a batch padded to a fixed row count) belong to no
+// item of a prefix call: zeros and -inf, a (row, head) pair of a CTA at a time.
+template <bool LATENT>
+__device__ __forceinline__ void clear_rows_of_no_request(const AttnParams& p, int lane) {
+  constexpr int kDv = LATENT ? kLatentDim : kPagedDim;
+  const int claimed = max(0, __ldg(p.cu_seqlens_q + p.num_seqs));
+  const int64_t pairs = static_cast<int64_t>(p.num_rows - min(claimed, p.num_rows)) * p.num_heads;
+#pragma unroll 1
+  for (int64_t x = blockIdx.x; x < pairs; x += gridDim.x) {
+    const int t = claimed + static_cast<int>(x / p.num_heads), h = static_cast<int>(x % p.num_heads);
+    uint4* out = reinterpret_cast<uint4*>(p.out + t * p.out_row_stride + h * kDv);
+    for (int i = lane; i < kDv / 8; i += 32) out[i] = make_uint4(0, 0, 0, 0);
+    if (p.lse && lane == 0) p.lse[static_cast<int64_t>(t) * p.num_heads + h] = -INFINITY;
+  }
+}
+
 // Where a segment's queries go: with at most 32 rows a CTA the buffer holds two
 // segments' queries (32 rows each), so the next ones load early.  (The product
 // of the second half reads 64 rows from row 32 on: what lies behind its 32
@@ -498,6 +514,7 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
         __syncwarp();
       }
     }
+    if (!p.indices) clear_rows_of_no_request<LATENT>(p, lane);
   } else if (warp >= kLoadWarp) {
     // ================================================================ loaders
     // Every warp of a team arrives once per part, after its share is issued

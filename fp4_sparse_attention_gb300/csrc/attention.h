@@ -133,8 +133,10 @@ __device__ __forceinline__ int attn_request(const AttnParams& p, int t) {
   }
   return lo;
 }
-// Positions row t of request b sees: [0, the result).
+// Positions row t of request b sees: [0, the result).  A row behind the last
+// request's (a selection's item; attn_request gives it that request) sees none.
 __device__ __forceinline__ int attn_visible(const AttnParams& p, int b, int t) {
+  if (p.indices && t >= __ldg(p.cu_seqlens_q + b + 1)) return 0;
   const int k_len = min(max(0, __ldg(p.cu_seqlens_k + b + 1) - __ldg(p.cu_seqlens_k + b)), p.max_seqlen_k);
   int64_t vis = k_len;
   if (p.visible_len) {

@@ -458,7 +458,9 @@ typedef enum fp4idx_dtype {
  *
  * Visible positions are those of fp4idx_problem_t (visible_len; causal with
  * qo_offset; all keys).  cu_seqlens_q/k, block_table, page_offsets,
- * table_stride, max_seqlen_q/k as there.  A block-table entry outside
+ * table_stride, max_seqlen_q/k as there; num_rows may exceed cu_seqlens_q[B]
+ * (a batch padded to a fixed row count): rows behind the requests' see nothing,
+ * whatever their visible_len and indices say.  A block-table entry outside
  * [0, num_pages) under a visible position sets FP4IDX_ERR_PAGE_RANGE and its
  * keys count as not visible.  Cache contents that no row of the call may see
  * are never used and may hold anything (NaN included); a position that some
