@@ -31,8 +31,8 @@
 //   warps 0-3   softmax: TMEM S as row fragments (four lanes per row), mask,
 //               running maximum, 2^x, P to shared memory; rescale of O^T when
 //               a row's maximum grew by more than 2^8 (until then the older
-//               maximum serves as the reference: weights stay below 2^8 and
-//               the result is the same up to rounding); the output.
+//               maximum serves as the reference: weights stay below 2^8, in
+//               fp16 2^15, and the result is the same up to rounding); the output.
 //   warp 4, 5   MMA issuers of the score and the value products.
 //   warps 6-    loaders: a 64-key run of one page by TMA; listed keys, and a
 //               run that a request ends in, by 16-byte asynchronous copies
@@ -82,6 +82,12 @@ constexpr int kMaxRowsOfRequest = 1 << 20;
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 // A row's reference maximum is raised only when the true one is 2^8 above it.
 constexpr float kRaise = 8.0f;
+// fp16 weights below 2^-14 lose bits and below 2^-25 become 0, while the sum keeps
+// them: the reference lies 2^7 below the maximum, so that weights use the type
+// up to 2^(7 + 8) (65,504 is its largest) and only shares below 2^-32 are lost.
+// bf16 has the range of fp32.
+template <int DTYPE>
+constexpr float kBelow = DTYPE == FP4IDX_FP16 ? 7.0f : 0.0f;
 
 template <bool LATENT>
 struct Cfg {
@@ -971,7 +977,7 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
-            top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2)) * p.scale_log2;
+            top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2)) * p.scale_log2 - kBelow<DTYPE>;
             if (top[e] > m[e] + kRaise) {
               f[e] = ex2(m[e] - top[e]);
               m[e] = top[e];
