@@ -528,6 +528,14 @@ def fp4idx_topk_merge(problem: DeviceProblem, k: int, indices: torch.Tensor, val
 _HALF = (torch.bfloat16, torch.float16)
 
 
+def _require_cuda(*tensors):
+    """All on one CUDA device: a kernel would take another's pointer for an address of its own."""
+    device = tensors[0].get_device()  # -1 for host tensors
+    for t in tensors:
+        if device < 0 or t.get_device() != device:
+            raise ValueError("the tensors must all be on one CUDA device")
+
+
 class DeviceAttention:
     """Device tensors of one attention call plus its fp4idx_attention_t.
 
@@ -538,6 +546,8 @@ class DeviceAttention:
     [Hkv,T,n] (paged) i32, n >= 1, or None for the whole prefix.  out, lse and the
     workspace are allocated here unless given, and kept: a call writes the same
     tensors again.  The object holds pointers: rebuild it when a tensor moves.
+    Calls on one object use its one workspace and must be ordered (one stream, or
+    events between streams); streams that run at the same time need an object each.
     """
 
     def __init__(self, *, q, k, cu_seqlens_q, cu_seqlens_k, block_table, max_seqlen_q: int, max_seqlen_k: int,
@@ -553,6 +563,9 @@ class DeviceAttention:
             raise ValueError("the cache must be [P, page, 576] (latent) or [P, Hkv, page, 128], dense inside a page")
         if not latent and (v.shape != k.shape or v.stride() != k.stride()):
             raise ValueError("k and v must have one shape and one set of strides")
+        for x in (k, v, cu_seqlens_q, cu_seqlens_k, block_table, page_offsets, visible_len, qo_offset, indices, out, lse, workspace):
+            if x is not None and x.device != q.device:
+                raise ValueError("every tensor must be on q's device")
         T, H = q.shape[0], q.shape[1]
         B = int(cu_seqlens_q.shape[0]) - 1
         kv_heads = 1 if latent else int(k.shape[1])
@@ -607,6 +620,8 @@ class DeviceAttention:
 
 def fp4idx_latent_attention(attention: DeviceAttention, stream=None):
     """Absorbed latent attention of every row over its visible or selected keys: (out [T, H, 512], lse [T, H])."""
+    if not attention.q.is_cuda:
+        raise ValueError("the tensors must be on a CUDA device")
     ws, size = attention._ws
     status = load_library().fp4idx_latent_attention(attention._ref, ws, size, _stream(stream))
     if status:
@@ -616,6 +631,8 @@ def fp4idx_latent_attention(attention: DeviceAttention, stream=None):
 
 def fp4idx_paged_attention(attention: DeviceAttention, stream=None):
     """Grouped-query attention of every row over its visible keys or selected blocks: (out [T, H, 128], lse [T, H])."""
+    if not attention.q.is_cuda:
+        raise ValueError("the tensors must be on a CUDA device")
     ws, size = attention._ws
     status = load_library().fp4idx_paged_attention(attention._ref, ws, size, _stream(stream))
     if status:
@@ -637,6 +654,7 @@ def fp4idx_store_latent(latent: torch.Tensor, rope: torch.Tensor, slots: torch.T
         raise ValueError("slots must be a contiguous [N] int32 tensor")
     if cache.dim() != 3 or cache.shape[2] != 576 or cache.stride()[1:] != (576, 1):
         raise ValueError("cache must be [P, page, 576], dense inside a page")
+    _require_cuda(latent, rope, slots, cache)
     if N == 0:
         return
     status = load_library().fp4idx_store_latent(latent.data_ptr(), ls, rope.data_ptr(), rs, slots.data_ptr(), N,
@@ -661,6 +679,7 @@ def fp4idx_store_kv(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tenso
     if k.dim() != 4 or k.shape[1] != Hkv or k.shape[3] != 128 or k.shape != v.shape or k.stride() != v.stride() \
             or k.stride()[1:] != (k.shape[2] * 128, 128, 1):
         raise ValueError("k and v must be [P, Hkv, page, 128], dense inside a page, with one set of strides")
+    _require_cuda(k_new, v_new, slots, k, v)
     if N == 0:
         return
     status = load_library().fp4idx_store_kv(k_new.data_ptr(), k_new.stride(0), v_new.data_ptr(), v_new.stride(0),
@@ -697,6 +716,7 @@ def fp4idx_build_tables(cached_len: torch.Tensor, new_len: torch.Tensor, block_t
                 raise ValueError("out: cu_seqlens_q [B+1], cu_seqlens_k [B+1], visible_len [T], slots [T], "
                                  "pages_taken [1]")
         cu_q, cu_k, visible, slots, taken = out
+    _require_cuda(cached_len, new_len, block_table, free_pages, cu_q, cu_k, visible, slots, taken)
     if num_pages is None:
         num_pages = (2 ** 31 - 1) // page_size if page_size > 0 else 1
     status = load_library().fp4idx_build_tables(

@@ -27,3 +27,33 @@ def test_an_empty_list_is_refused(latent):
     with pytest.raises(ValueError, match="at least one"):
         binding.DeviceAttention(**a, indices=torch.zeros(shape, dtype=torch.int32))
     binding.DeviceAttention(**a, indices=torch.zeros(shape[:-1] + (1,), dtype=torch.int32))
+
+
+@pytest.mark.parametrize("name", ["k", "cu_seqlens_q", "cu_seqlens_k", "block_table", "visible_len", "indices", "out", "lse", "workspace"])
+def test_tensors_of_another_device_are_refused(name):
+    # (the meta device stands for any other device)
+    more = dict(visible_len=torch.zeros((2,), dtype=torch.int32), indices=torch.zeros((2, 5), dtype=torch.int32),
+                out=torch.zeros((2, 4, 512), dtype=torch.bfloat16), lse=torch.zeros((2, 4)),
+                workspace=torch.zeros((1 << 20,), dtype=torch.uint8))
+    a = {**arguments(), **more}
+    binding.DeviceAttention(**a)
+    a[name] = a[name].to("meta")
+    with pytest.raises(ValueError, match="device"):
+        binding.DeviceAttention(**a)
+
+
+def test_host_tensors_are_refused():
+    a = binding.DeviceAttention(**arguments())
+    with pytest.raises(ValueError, match="CUDA"):
+        binding.fp4idx_latent_attention(a)
+    with pytest.raises(ValueError, match="CUDA"):
+        binding.fp4idx_paged_attention(binding.DeviceAttention(**arguments(False)))
+    x = torch.zeros((2, 576), dtype=torch.bfloat16)
+    n = torch.zeros((2,), dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        binding.fp4idx_store_latent(x[:, :512], x[:, 512:], n, torch.zeros((1, 64, 576), dtype=torch.bfloat16))
+    kv = torch.zeros((2, 2, 64, 128), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        binding.fp4idx_store_kv(kv[:, :, 0].contiguous(), kv[:, :, 1].contiguous(), n, kv, kv.clone())
+    with pytest.raises(ValueError, match="CUDA"):
+        binding.fp4idx_build_tables(n, n, torch.zeros((2, 4), dtype=torch.int32), n, 64, 2)
