@@ -536,6 +536,11 @@ def _require_cuda(*tensors):
             raise ValueError("the tensors must all be on one CUDA device")
 
 
+def _step(x, dim, dense):
+    """x's stride along dim; along a dimension of one, where strides mean nothing, the dense one."""
+    return x.stride(dim) if x.shape[dim] != 1 else dense
+
+
 class DeviceAttention:
     """Device tensors of one attention call plus its fp4idx_attention_t.
 
@@ -561,7 +566,7 @@ class DeviceAttention:
             raise ValueError(f"q must be [T, H, {dk}] with dense rows")
         if k.dim() != (3 if latent else 4) or k.shape[-1] != dk or not k[0].is_contiguous():
             raise ValueError("the cache must be [P, page, 576] (latent) or [P, Hkv, page, 128], dense inside a page")
-        if not latent and (v.shape != k.shape or v.stride() != k.stride()):
+        if not latent and (v.shape != k.shape or not v[0].is_contiguous() or _step(v, 0, 0) != _step(k, 0, 0)):
             raise ValueError("k and v must have one shape and one set of strides")
         for x in (k, v, cu_seqlens_q, cu_seqlens_k, block_table, page_offsets, visible_len, qo_offset, indices, out, lse, workspace):
             if x is not None and x.device != q.device:
@@ -588,7 +593,7 @@ class DeviceAttention:
             out = torch.empty((T, H, dv), dtype=q.dtype, device=q.device)
         if lse is None:
             lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-        if tuple(out.shape) != (T, H, dv) or out.dtype != q.dtype or out.stride(2) != 1 or out.stride(1) != dv:
+        if tuple(out.shape) != (T, H, dv) or out.dtype != q.dtype or out.stride(2) != 1 or _step(out, 1, dv) != dv:
             raise ValueError(f"out must be [T, H, {dv}] of q's type with dense rows")
         if tuple(lse.shape) != (T, H) or lse.dtype != torch.float32 or not lse.is_contiguous():
             raise ValueError("lse must be a contiguous [T, H] float32 tensor")
@@ -603,13 +608,14 @@ class DeviceAttention:
         self.c = CAttention(
             dtype=0 if q.dtype == torch.bfloat16 else 1, num_seqs=B, num_rows=T, num_heads=H, num_kv_heads=kv_heads,
             page_size=int(k.shape[-2]), num_pages=int(k.shape[0]),
-            table_stride=int(block_table.stride(0)) if block_table.dim() == 2 else 0, max_seqlen_q=int(max_seqlen_q),
-            max_seqlen_k=int(max_seqlen_k), q=at(q), q_row_stride=int(q.stride(0)), q_head_stride=int(q.stride(1)),
-            k=at(k), v=at(v), page_stride=int(k.stride(0)), cu_seqlens_q=at(cu_seqlens_q),
+            table_stride=_step(block_table, 0, block_table.shape[1]) if block_table.dim() == 2 else 0,
+            max_seqlen_q=int(max_seqlen_q), max_seqlen_k=int(max_seqlen_k), q=at(q),
+            q_row_stride=_step(q, 0, H * _step(q, 1, dk)), q_head_stride=_step(q, 1, dk),
+            k=at(k), v=at(v), page_stride=_step(k, 0, k[0].numel()), cu_seqlens_q=at(cu_seqlens_q),
             cu_seqlens_k=at(cu_seqlens_k), block_table=at(block_table), page_offsets=at(page_offsets),
             visible_len=at(visible_len), qo_offset=at(qo_offset), causal=int(bool(causal)), scale=float(scale),
             indices=at(indices), num_indices=0 if indices is None else int(indices.shape[-1]), out=at(out),
-            out_row_stride=int(out.stride(0)), lse=at(lse))
+            out_row_stride=_step(out, 0, H * dv), lse=at(lse))
         self._ref = ctypes.byref(self.c)
         need = int(load_library().fp4idx_attention_workspace_bytes(self._ref))
         if workspace is None:
@@ -652,14 +658,16 @@ def fp4idx_store_latent(latent: torch.Tensor, rope: torch.Tensor, slots: torch.T
         raise ValueError("latent must be [N, 512] and rope [N, 64] with dense rows")
     if slots.dtype != torch.int32 or slots.numel() != N or not slots.is_contiguous():
         raise ValueError("slots must be a contiguous [N] int32 tensor")
+    if N == 1:  # the stride of a dimension of one means nothing
+        ls, rs = 512, 64
     if cache.dim() != 3 or cache.shape[2] != 576 or cache.stride()[1:] != (576, 1):
         raise ValueError("cache must be [P, page, 576], dense inside a page")
     _require_cuda(latent, rope, slots, cache)
     if N == 0:
         return
     status = load_library().fp4idx_store_latent(latent.data_ptr(), ls, rope.data_ptr(), rs, slots.data_ptr(), N,
-                                                cache.shape[1], cache.shape[0], cache.stride(0), cache.data_ptr(),
-                                                _stream(stream))
+                                                cache.shape[1], cache.shape[0], _step(cache, 0, cache.shape[1] * 576),
+                                                cache.data_ptr(), _stream(stream))
     if status:
         _check(status, "fp4idx_store_latent")
 
@@ -670,21 +678,33 @@ def fp4idx_store_kv(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tenso
     dtype = k_new.dtype
     if dtype not in _HALF or v_new.dtype != dtype or k.dtype != dtype or v.dtype != dtype:
         raise ValueError("k_new, v_new, k and v must all be bfloat16 or all float16")
-    N, Hkv = k_new.shape[0], k_new.shape[1]
-    if k_new.shape != (N, Hkv, 128) or v_new.shape != (N, Hkv, 128) or k_new.stride()[1:] != (128, 1) \
-            or v_new.stride()[1:] != (128, 1):
+    if k_new.dim() != 3 or k_new.shape[2] != 128 or v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must be [N, Hkv, 128] with dense heads")
+    N, Hkv, _ = k_new.shape
+    (kt, kh, k1), (vt, vh, v1) = k_new.stride(), v_new.stride()
+    if Hkv == 1:  # the stride of a dimension of one means nothing
+        kh = vh = 128
+    if N == 1:
+        kt = vt = Hkv * 128
+    if kh != 128 or vh != 128 or k1 != 1 or v1 != 1:
         raise ValueError("k_new and v_new must be [N, Hkv, 128] with dense heads")
     if slots.dtype != torch.int32 or slots.numel() != N or not slots.is_contiguous():
         raise ValueError("slots must be a contiguous [N] int32 tensor")
-    if k.dim() != 4 or k.shape[1] != Hkv or k.shape[3] != 128 or k.shape != v.shape or k.stride() != v.stride() \
-            or k.stride()[1:] != (k.shape[2] * 128, 128, 1):
+    if k.dim() != 4 or k.shape[1] != Hkv or k.shape[3] != 128 or k.shape != v.shape:
+        raise ValueError("k and v must be [P, Hkv, page, 128]")
+    pages, _, page, _ = k.shape
+    (page_stride, *k_in), (v_stride, *v_in) = k.stride(), v.stride()
+    if Hkv == 1:
+        k_in[0] = v_in[0] = page * 128
+    if pages == 1:
+        page_stride = v_stride = Hkv * page * 128
+    if k_in != [page * 128, 128, 1] or v_in != k_in or v_stride != page_stride:
         raise ValueError("k and v must be [P, Hkv, page, 128], dense inside a page, with one set of strides")
     _require_cuda(k_new, v_new, slots, k, v)
     if N == 0:
         return
-    status = load_library().fp4idx_store_kv(k_new.data_ptr(), k_new.stride(0), v_new.data_ptr(), v_new.stride(0),
-                                            slots.data_ptr(), N, Hkv, k.shape[2], k.shape[0], k.stride(0), k.data_ptr(),
-                                            v.data_ptr(), _stream(stream))
+    status = load_library().fp4idx_store_kv(k_new.data_ptr(), kt, v_new.data_ptr(), vt, slots.data_ptr(), N, Hkv, page,
+                                            pages, page_stride, k.data_ptr(), v.data_ptr(), _stream(stream))
     if status:
         _check(status, "fp4idx_store_kv")
 
@@ -699,7 +719,8 @@ def fp4idx_build_tables(cached_len: torch.Tensor, new_len: torch.Tensor, block_t
     if cached_len.dtype != i32 or new_len.dtype != i32 or free_pages.dtype != i32 or block_table.dtype != i32:
         raise ValueError("cached_len, new_len, block_table and free_pages must be int32")
     B = cached_len.shape[0]
-    if cached_len.stride() != (1,) or new_len.stride() != (1,) or free_pages.stride() != (1,):
+    if not (cached_len.dim() == new_len.dim() == free_pages.dim() == 1 and cached_len.is_contiguous()
+            and new_len.is_contiguous() and free_pages.is_contiguous()):
         raise ValueError("cached_len, new_len and free_pages must be contiguous 1-D tensors")
     if new_len.shape[0] != B or block_table.dim() != 2 or block_table.shape[0] != B or block_table.stride(1) != 1:
         raise ValueError("new_len must be [B] and block_table [B, stride] with dense rows")
@@ -721,8 +742,8 @@ def fp4idx_build_tables(cached_len: torch.Tensor, new_len: torch.Tensor, block_t
         num_pages = (2 ** 31 - 1) // page_size if page_size > 0 else 1
     status = load_library().fp4idx_build_tables(
         cached_len.data_ptr(), new_len.data_ptr(), B, num_rows, page_size, num_pages, free_pages.data_ptr(),
-        free_pages.shape[0], block_table.data_ptr(), block_table.stride(0), cu_q.data_ptr(), cu_k.data_ptr(),
-        visible.data_ptr(), slots.data_ptr(), taken.data_ptr(), _stream(stream))
+        free_pages.shape[0], block_table.data_ptr(), _step(block_table, 0, block_table.shape[1]), cu_q.data_ptr(),
+        cu_k.data_ptr(), visible.data_ptr(), slots.data_ptr(), taken.data_ptr(), _stream(stream))
     if status:
         _check(status, "fp4idx_build_tables")
     return cu_q, cu_k, visible, slots, taken

@@ -60,9 +60,13 @@ fp4idx_status_t check_attention(const fp4idx_attention_t* a, bool latent) {
   if (a->q_head_stride < dk || a->q_head_stride % 8 != 0)
     FAIL(FP4IDX_EINVAL, "q_head_stride %lld must be a multiple of 8 and >= %d",
          static_cast<long long>(a->q_head_stride), dk);
-  if (a->q_row_stride < dk + (a->num_heads - 1) * a->q_head_stride || a->q_row_stride % 8 != 0)
-    FAIL(FP4IDX_EINVAL, "q_row_stride %lld must be a multiple of 8 and hold num_heads heads",
-         static_cast<long long>(a->q_row_stride));
+  if (a->q_row_stride < dk || a->q_row_stride % 8 != 0)
+    FAIL(FP4IDX_EINVAL, "q_row_stride %lld must be a multiple of 8 and >= %d", static_cast<long long>(a->q_row_stride), dk);
+  // a row holds its heads, or a head its rows (products computed by head)
+  if (a->num_heads > 1 && a->num_rows > 1 && a->q_head_stride > (a->q_row_stride - dk) / (a->num_heads - 1) &&
+      a->q_row_stride > (a->q_head_stride - dk) / (a->num_rows - 1))
+    FAIL(FP4IDX_EINVAL, "q_row_stride %lld and q_head_stride %lld: the queries of %d rows and %d heads overlap",
+         static_cast<long long>(a->q_row_stride), static_cast<long long>(a->q_head_stride), a->num_rows, a->num_heads);
   if (a->out_row_stride < static_cast<int64_t>(a->num_heads) * dv || a->out_row_stride % 8 != 0)
     FAIL(FP4IDX_EINVAL, "out_row_stride %lld must be a multiple of 8 and >= num_heads * %d",
          static_cast<long long>(a->out_row_stride), dv);

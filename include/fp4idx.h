@@ -467,7 +467,8 @@ typedef enum fp4idx_dtype {
  * row of a request sees must hold finite values for the others, too.
  *
  *   q           element (t,h,d) at q + t*q_row_stride + h*q_head_stride + d
- *               (elements; strides multiples of 8, 16-byte aligned base).
+ *               (elements; strides multiples of 8, 16-byte aligned base; heads
+ *               inside rows or rows inside heads).
  *   k, v        page p at k + p*page_stride (elements; a multiple of 8, at
  *               least one page's content; 16-byte aligned bases; a cache may
  *               be one layer's slice of a larger allocation and exceed 2^31

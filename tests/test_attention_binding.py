@@ -57,3 +57,43 @@ def test_host_tensors_are_refused():
         binding.fp4idx_store_kv(kv[:, :, 0].contiguous(), kv[:, :, 1].contiguous(), n, kv, kv.clone())
     with pytest.raises(ValueError, match="CUDA"):
         binding.fp4idx_build_tables(n, n, torch.zeros((2, 4), dtype=torch.int32), n, 64, 2)
+
+
+# ---------------------------------------------------------------- strides
+def accepted(a, latent=True):
+    """The C call gets past its argument checks (there is no workspace, so it never launches)."""
+    f = binding.load_library().fp4idx_latent_attention if latent else binding.load_library().fp4idx_paged_attention
+    return f(a._ref, None, 0, None) not in (1, 2)
+
+
+@pytest.mark.parametrize("latent", [True, False])
+@pytest.mark.parametrize("rows,heads", [(1, 1), (1, 4), (3, 1), (3, 4)])
+def test_queries_by_head_are_accepted(rows, heads, latent):
+    # [H, T, d] products seen as [T, H, d]; with one row such a view is contiguous and cannot be made more so
+    a = arguments(latent, rows=rows, heads=heads, kv_heads=1)
+    a["q"] = torch.zeros((heads, rows, a["q"].shape[2]), dtype=torch.bfloat16).transpose(0, 1)
+    assert accepted(binding.DeviceAttention(**a), latent)
+
+
+def test_strides_of_dimensions_of_one_do_not_count():
+    for latent in (True, False):
+        a = arguments(latent, rows=1, heads=1, kv_heads=1, reqs=1)
+        d, dv = a["q"].shape[2], 512 if latent else 128
+        a["q"] = torch.zeros((d,), dtype=torch.bfloat16).as_strided((1, 1, d), (3, 5, 1))
+        a["out"] = torch.zeros((dv,), dtype=torch.bfloat16).as_strided((1, 1, dv), (3, 5, 1))
+        a["block_table"] = torch.zeros((2,), dtype=torch.int32).as_strided((1, 2), (1, 1))
+        page = (1, 64, d) if latent else (1, 1, 64, d)
+        strides = (7, d, 1) if latent else (7, 3, d, 1)
+        a["k"] = torch.zeros((64 * d,), dtype=torch.bfloat16).as_strided(page, strides)
+        if not latent:
+            a["v"] = torch.zeros((64 * d,), dtype=torch.bfloat16).as_strided(page, (9, 4, d, 1))
+        x = binding.DeviceAttention(**a)
+        assert accepted(x, latent)
+        assert x.c.table_stride == 2 and x.c.page_stride == 64 * d
+
+
+def test_overlapping_queries_are_refused():
+    a = arguments(True, rows=3, heads=4)
+    for strides in ((576, 576, 1), (0, 576, 1), (2 * 576, 576, 1), (576, 2 * 576, 1), (576, 3 * 576 - 8, 1)):
+        a["q"] = torch.zeros((1 << 14,), dtype=torch.bfloat16).as_strided((3, 4, 576), strides)
+        assert not accepted(binding.DeviceAttention(**a))
