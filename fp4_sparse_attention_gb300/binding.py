@@ -582,6 +582,8 @@ class DeviceAttention:
             raise ValueError("block_table must be int32 with dense rows")
         if block_table.dim() == 2 and block_table.shape[0] < B:
             raise ValueError("block_table must have a row for every request")
+        if block_table.dim() == 2 and page_offsets is None and block_table.shape[1] * k.shape[-2] < max_seqlen_k:
+            raise ValueError("block_table must have an entry for every page of max_seqlen_k")
         if block_table.dim() != 2 and page_offsets is None:
             raise ValueError("a flat block_table needs page_offsets")
         if indices is not None and (indices.dtype != torch.int32 or not indices.is_contiguous()
@@ -724,6 +726,8 @@ def fp4idx_build_tables(cached_len: torch.Tensor, new_len: torch.Tensor, block_t
         raise ValueError("cached_len, new_len and free_pages must be contiguous 1-D tensors")
     if new_len.shape[0] != B or block_table.dim() != 2 or block_table.shape[0] != B or block_table.stride(1) != 1:
         raise ValueError("new_len must be [B] and block_table [B, stride] with dense rows")
+    if B > 1 and block_table.stride(0) != block_table.shape[1]:  # a row's end is known by the next one's start
+        raise ValueError("block_table must not be a view of wider rows: new pages are bounded by the rows' distance")
     if out is None:
         dev = cached_len.device
         cu_q = torch.empty((B + 1,), dtype=i32, device=dev)

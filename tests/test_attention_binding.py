@@ -97,3 +97,30 @@ def test_overlapping_queries_are_refused():
     for strides in ((576, 576, 1), (0, 576, 1), (2 * 576, 576, 1), (576, 2 * 576, 1), (576, 3 * 576 - 8, 1)):
         a["q"] = torch.zeros((1 << 14,), dtype=torch.bfloat16).as_strided((3, 4, 576), strides)
         assert not accepted(binding.DeviceAttention(**a))
+
+
+# ---------------------------------------------------------------- block tables
+def test_a_table_too_narrow_for_its_lengths_is_refused():
+    # entries behind a row's width belong to something else, however far apart the rows are
+    a = arguments()
+    wide = torch.zeros((2, 8), dtype=torch.int32)
+    for table in (wide[:, :1], wide[:, 7:]):
+        a["block_table"] = table
+        with pytest.raises(ValueError, match="block_table"):
+            binding.DeviceAttention(**a)
+    a["block_table"] = wide[:, 3:5]  # as many as max_seqlen_k needs
+    assert accepted(binding.DeviceAttention(**a))
+    a["block_table"], a["max_seqlen_k"] = wide[:, :1], 64
+    assert accepted(binding.DeviceAttention(**a))
+
+
+def test_tables_are_built_in_whole_rows_only():
+    # the device bounds a request's pages by the distance of two rows: behind a narrower view it would write past it
+    n = torch.zeros((2,), dtype=torch.int32)
+    wide = torch.zeros((2, 8), dtype=torch.int32)
+    with pytest.raises(ValueError, match="block_table"):
+        binding.fp4idx_build_tables(n, n, wide[:, 4:], n, 64, 2)
+    with pytest.raises(ValueError, match="CUDA"):  # (past that check)
+        binding.fp4idx_build_tables(n, n, wide, n, 64, 2)
+    with pytest.raises(ValueError, match="CUDA"):
+        binding.fp4idx_build_tables(n[:1], n[:1], wide[:1, 4:], n, 64, 2)
