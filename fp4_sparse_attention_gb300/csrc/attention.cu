@@ -49,7 +49,8 @@
 //
 // Work split: the tiles of all items (request or row, K/V head, row chunk)
 // are concatenated and cut into equal runs, one per CTA group, so long and
-// short requests balance; the `members` CTAs of a group walk the same keys
+// short requests balance (lists and short prefixes also stay whole:
+// plan_attention); the `members` CTAs of a group walk the same keys
 // for different row chunks, close enough in time for the L2 to serve the
 // second reader.  An item cut by a boundary leaves partial sums that
 // join_kernel adds in a fixed order.
@@ -80,6 +81,8 @@ constexpr int kMaxMembers = 8;
 constexpr int kGroupShift = 40;
 constexpr int kMaxRowsOfRequest = 1 << 20;
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
+// Whole prefix items are for runs of at most this many tiles (plan_attention).
+constexpr int kWholeTiles = 12;
 // A row's reference maximum is raised only when the true one is 2^8 above it.
 constexpr float kRaise = 8.0f;
 // fp16 weights below 2^-14 lose bits and below 2^-25 become 0, while the sum keeps
@@ -1337,7 +1340,19 @@ bool plan_attention(AttnParams* p, int sms) {
   //   equal runs over all items: every group busy, but most CTAs also cross from
   //     one item to the next, five tiles in all.
   // Lists have one length, so that HBM, which feeds as many CTAs as `feeds`,
-  // bounds each form from below; a prefix may be far shorter than max_seqlen_k.
+  // bounds each form from below.  (Rows of one request find much of their keys in
+  // L2, but gain nothing by equal runs: 77 / 100 / 130 rows x 64 heads of one
+  // 32,768-key request, 2,048 listed keys each, 55 / 57 / 57 us whole, 51 / 57 / 66
+  // in equal runs.)  Of a prefix only the largest length is known here, and every
+  // other item may be a single tile: whole items are taken up to kWholeTiles,
+  // where one long item among single-tile ones costs no more than equal runs (152
+  // items, one of 8 / 12 paged tiles 19.6 / 22.5 against 20.5 / 21.0 us, of 12
+  // latent ones 28.6 against 28.6).  Longer ones are cut by the lengths that the
+  // device finds: 38 requests x 4 K/V heads of 1,024-32,768 keys 119 us (whole
+  // 209), one of 32,768 keys among 37 of 1,024 48 us (238), 152 requests x 64
+  // latent heads of 1,024-65,536 keys 392 us (1,142), a prompt of 1,024 rows
+  // among 18 decodes 1.4 ms (17.2).  Items of one length pay a join for it: 152 of
+  // 16 paged tiles 45.3 us (43.0), of 16 latent ones 51.8 (49.2).
   // Measured, whole against cut: one request of 2 / 3 / 4 latent tiles 10.4 /
   // 11.5 / 12.6 against 10.4 / 10.5 / 10.6 us, of 3 / 4 / 5 paged tiles 8.4 / 9.1
   // / 9.9 against 9.7 / 9.4 / 9.2 us, 64 requests of 3 / 12 latent tiles 11.7 /
@@ -1353,7 +1368,7 @@ bool plan_attention(AttnParams* p, int sms) {
   const int64_t cuts = std::min(groups / items, per_item);
   const double cut = cuts > 1 ? std::max(static_cast<double>((per_item + cuts - 1) / cuts), hbm) + (latent ? 2 : 3) : HUGE_VAL;
   const double equal = std::max(longest * items / groups, hbm) + 5;
-  p->whole_items = whole < cut && whole <= equal;
+  p->whole_items = whole < cut && whole <= equal && (p->indices || whole <= kWholeTiles);
   if (!p->whole_items && cut <= equal) groups = cuts * items;
   const int64_t units = p->whole_items ? items : most;
   p->groups = static_cast<int32_t>(units < groups ? units : groups);
