@@ -105,6 +105,7 @@ struct TablesParams {
   int32_t* slots;
   int32_t* pages_taken;
   int32_t reqs_per_cta;
+  int32_t shares;       // parts of a request's first rows (launch_tables)
   uint32_t* err;
 };
 
