@@ -137,7 +137,7 @@ __device__ __forceinline__ int attn_request(const AttnParams& p, int t) {
 // Positions row t of request b sees: [0, the result).  A row behind the last
 // request's (a selection's item; attn_request gives it that request) sees none.
 __device__ __forceinline__ int attn_visible(const AttnParams& p, int b, int t) {
-  if (p.indices && t >= __ldg(p.cu_seqlens_q + b + 1)) return 0;
+  const int end = p.indices ? __ldg(p.cu_seqlens_q + b + 1) : INT32_MAX;
   const int k_len = min(max(0, __ldg(p.cu_seqlens_k + b + 1) - __ldg(p.cu_seqlens_k + b)), p.max_seqlen_k);
   int64_t vis = k_len;
   if (p.visible_len) {
@@ -148,7 +148,7 @@ __device__ __forceinline__ int attn_visible(const AttnParams& p, int b, int t) {
                                     : static_cast<int64_t>(k_len) - q_len;
     vis = static_cast<int64_t>(t - q0) + off + 1;
   }
-  vis = vis < 0 ? 0 : vis;
+  vis = vis < 0 || t >= end ? 0 : vis;
   return static_cast<int>(vis > k_len ? k_len : vis);
 }
 __device__ __forceinline__ int64_t attn_table_base(const AttnParams& p, int b) {
