@@ -526,14 +526,8 @@ def fp4idx_topk_merge(problem: DeviceProblem, k: int, indices: torch.Tensor, val
 
 
 _HALF = (torch.bfloat16, torch.float16)
-
-
-def _require_cuda(*tensors):
-    """All on one CUDA device: a kernel would take another's pointer for an address of its own."""
-    device = tensors[0].get_device()  # -1 for host tensors
-    for t in tensors:
-        if device < 0 or t.get_device() != device:
-            raise ValueError("the tensors must all be on one CUDA device")
+# A kernel would take another device's pointer for an address of its own.
+_ONE_DEVICE = "the tensors must all be on one CUDA device"
 
 
 def _step(x, dim, dense):
@@ -654,22 +648,28 @@ def fp4idx_store_latent(latent: torch.Tensor, rope: torch.Tensor, slots: torch.T
     dtype = latent.dtype
     if dtype not in _HALF or rope.dtype != dtype or cache.dtype != dtype:
         raise ValueError("latent, rope and cache must all be bfloat16 or all float16")
-    N = latent.shape[0]
+    shape = latent.shape
+    N = shape[0]
     (ls, l1), (rs, r1) = latent.stride(), rope.stride()
-    if latent.shape != (N, 512) or rope.shape != (N, 64) or l1 != 1 or r1 != 1:
+    if shape != (N, 512) or rope.shape != (N, 64) or l1 != 1 or r1 != 1:
         raise ValueError("latent must be [N, 512] and rope [N, 64] with dense rows")
     if slots.dtype != torch.int32 or slots.numel() != N or not slots.is_contiguous():
         raise ValueError("slots must be a contiguous [N] int32 tensor")
-    if N == 1:  # the stride of a dimension of one means nothing
-        ls, rs = 512, 64
-    if cache.dim() != 3 or cache.shape[2] != 576 or cache.stride()[1:] != (576, 1):
+    if cache.dim() != 3:
         raise ValueError("cache must be [P, page, 576], dense inside a page")
-    _require_cuda(latent, rope, slots, cache)
-    if N == 0:
-        return
-    status = load_library().fp4idx_store_latent(latent.data_ptr(), ls, rope.data_ptr(), rs, slots.data_ptr(), N,
-                                                cache.shape[1], cache.shape[0], _step(cache, 0, cache.shape[1] * 576),
-                                                cache.data_ptr(), _stream(stream))
+    (pages, page, width), (page_stride, c1, c2) = cache.shape, cache.stride()
+    if width != 576 or c1 != 576 or c2 != 1:
+        raise ValueError("cache must be [P, page, 576], dense inside a page")
+    if not (slots.get_device() == latent.get_device() == rope.get_device() == cache.get_device() >= 0):  # -1: host
+        raise ValueError(_ONE_DEVICE)
+    if N <= 1:  # the stride of a dimension of one means nothing
+        if N == 0:
+            return
+        ls, rs = 512, 64
+    if pages == 1:
+        page_stride = page * 576
+    status = load_library().fp4idx_store_latent(latent.data_ptr(), ls, rope.data_ptr(), rs, slots.data_ptr(), N, page, pages,
+                                                page_stride, cache.data_ptr(), _stream(stream))
     if status:
         _check(status, "fp4idx_store_latent")
 
@@ -702,7 +702,8 @@ def fp4idx_store_kv(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tenso
         page_stride = v_stride = Hkv * page * 128
     if k_in != [page * 128, 128, 1] or v_in != k_in or v_stride != page_stride:
         raise ValueError("k and v must be [P, Hkv, page, 128], dense inside a page, with one set of strides")
-    _require_cuda(k_new, v_new, slots, k, v)
+    if not (slots.get_device() == k_new.get_device() == v_new.get_device() == k.get_device() == v.get_device() >= 0):
+        raise ValueError(_ONE_DEVICE)
     if N == 0:
         return
     status = load_library().fp4idx_store_kv(k_new.data_ptr(), kt, v_new.data_ptr(), vt, slots.data_ptr(), N, Hkv, page,
@@ -720,14 +721,19 @@ def fp4idx_build_tables(cached_len: torch.Tensor, new_len: torch.Tensor, block_t
     i32 = torch.int32
     if cached_len.dtype != i32 or new_len.dtype != i32 or free_pages.dtype != i32 or block_table.dtype != i32:
         raise ValueError("cached_len, new_len, block_table and free_pages must be int32")
-    B = cached_len.shape[0]
     if not (cached_len.dim() == new_len.dim() == free_pages.dim() == 1 and cached_len.is_contiguous()
             and new_len.is_contiguous() and free_pages.is_contiguous()):
         raise ValueError("cached_len, new_len and free_pages must be contiguous 1-D tensors")
-    if new_len.shape[0] != B or block_table.dim() != 2 or block_table.shape[0] != B or block_table.stride(1) != 1:
+    (B,), (free,) = cached_len.shape, free_pages.shape
+    if new_len.numel() != B or block_table.dim() != 2:
         raise ValueError("new_len must be [B] and block_table [B, stride] with dense rows")
-    if B > 1 and block_table.stride(0) != block_table.shape[1]:  # a row's end is known by the next one's start
+    (table_rows, width), (table_stride, one) = block_table.shape, block_table.stride()
+    if table_rows != B or one != 1:
+        raise ValueError("new_len must be [B] and block_table [B, stride] with dense rows")
+    if B > 1 and table_stride != width:  # a row's end is known by the next one's start
         raise ValueError("block_table must not be a view of wider rows: new pages are bounded by the rows' distance")
+    if not (cached_len.get_device() == new_len.get_device() == block_table.get_device() == free_pages.get_device() >= 0):
+        raise ValueError(_ONE_DEVICE)  # -1: host
     if out is None:
         dev = cached_len.device
         cu_q = torch.empty((B + 1,), dtype=i32, device=dev)
@@ -737,17 +743,16 @@ def fp4idx_build_tables(cached_len: torch.Tensor, new_len: torch.Tensor, block_t
         taken = torch.empty((1,), dtype=i32, device=dev)
     else:
         for x, n in zip(out, (B + 1, B + 1, num_rows, num_rows, 1)):
-            if x.dtype != i32 or x.numel() != n or not x.is_contiguous():
+            if x.dtype != i32 or x.numel() != n or not x.is_contiguous() or x.get_device() != cached_len.get_device():
                 raise ValueError("out: cu_seqlens_q [B+1], cu_seqlens_k [B+1], visible_len [T], slots [T], "
-                                 "pages_taken [1]")
+                                 "pages_taken [1], on the device of the lengths")
         cu_q, cu_k, visible, slots, taken = out
-    _require_cuda(cached_len, new_len, block_table, free_pages, cu_q, cu_k, visible, slots, taken)
     if num_pages is None:
         num_pages = (2 ** 31 - 1) // page_size if page_size > 0 else 1
     status = load_library().fp4idx_build_tables(
         cached_len.data_ptr(), new_len.data_ptr(), B, num_rows, page_size, num_pages, free_pages.data_ptr(),
-        free_pages.shape[0], block_table.data_ptr(), _step(block_table, 0, block_table.shape[1]), cu_q.data_ptr(),
-        cu_k.data_ptr(), visible.data_ptr(), slots.data_ptr(), taken.data_ptr(), _stream(stream))
+        free, block_table.data_ptr(), width, cu_q.data_ptr(), cu_k.data_ptr(), visible.data_ptr(), slots.data_ptr(),
+        taken.data_ptr(), _stream(stream))
     if status:
         _check(status, "fp4idx_build_tables")
     return cu_q, cu_k, visible, slots, taken
