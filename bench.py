@@ -50,32 +50,32 @@ def unit_of(spec) -> str:
 L2_BYTES = 129 * 1024 * 1024
 
 # DRAM bytes per launch from ncu captures, valid only for the kernel sources
-# they were taken on: sha256, first 16 hex digits, of the units that hold the
-# recorded kernels and the headers those include.
-RECORDED_UNITS = ("block_kernel.cu", "formats.cuh", "internal.h", "ptx.cuh", "score_kernel.cuh", "score_mx.cu",
-                  "score_nv.cu", "topk_merge.cu", "topk_smem.cuh")
+# they were taken on: sha256, first 16 hex digits, of the csrc/ files (api.cu
+# plans the recorded launches), without the units of attention, its cache
+# writers and the step tables, which no recorded launch runs.
+OTHER_UNITS = ("api_attention.cu", "attention.cu", "attention.h", "attn_ptx.cuh", "build_tables.cu", "store_rows.cu")
 RECORDED_TRAFFIC: dict = {
     # ncu --metrics dram__bytes_read.sum,dram__bytes_write.sum (one pass), one launch of
     # the GQA NVFP4 block-score kernel: read 52,000,256 B + write 84,906,240 B (the
     # [32, 64, 16,384] fp32 scores).
-    ("block_scores", "block_scores"): {"sha": "9928ee637fef129d", "bytes": 136906496},
-    ("block_topk", "block_scores"): {"sha": "9928ee637fef129d", "bytes": 136906496},
+    ("block_scores", "block_scores"): {"sha": "6cfa7deeb19b90ac", "bytes": 136906496},
+    ("block_topk", "block_scores"): {"sha": "6cfa7deeb19b90ac", "bytes": 136906496},
     # ncu --metrics dram__bytes_read.sum,dram__bytes_write.sum (one pass), one launch on
     # the full workload: read 157,189,376 B (inputs: q 142.6 MB, w 8.4 MB, K 2.2 MB) +
     # write 504,214,528 B (every CTA's candidates at or above its k-th bucket, for the merge).
-    ("prefill", "scorer_topk"): {"sha": "9928ee637fef129d", "bytes": 661403904},
+    ("prefill", "scorer_topk"): {"sha": "6cfa7deeb19b90ac", "bytes": 661403904},
     # the same for the long batched decode: read 290,656,256 B (272.1 MB of K) + write
     # 23,139,584 B (partial lists).
-    ("long_decode", "scorer_topk"): {"sha": "9928ee637fef129d", "bytes": 313795840},
+    ("long_decode", "scorer_topk"): {"sha": "6cfa7deeb19b90ac", "bytes": 313795840},
     # the same, prefill 8k: read 39,348,736 B + write 64,539,136 B.
-    ("prefill_8k", "scorer_topk"): {"sha": "9928ee637fef129d", "bytes": 103887872},
+    ("prefill_8k", "scorer_topk"): {"sha": "6cfa7deeb19b90ac", "bytes": 103887872},
 }
 
 
 def source_sha() -> str:
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "fp4_sparse_attention_gb300", "csrc")
-    for fn in RECORDED_UNITS:
+    for fn in sorted(set(os.listdir(csrc)) - set(OTHER_UNITS)):
         with open(os.path.join(csrc, fn), "rb") as f:
             h.update(fn.encode())
             h.update(f.read())
