@@ -55,11 +55,12 @@
 // second reader.  An item cut by a boundary leaves partial sums that
 // join_kernel adds in a fixed order.
 //
-// Measured (bf16): latent, 16 rows x 128 heads over 30,001-119,999 keys 335 us
-// (1,387 MB, 4.1 TB/s; 1,024 rows x 128 heads over 2,048 listed keys each 617
-// us, 946 TFLOP/s: both bound by the products, M = 64 at half rate); paged, 64
-// rows x 32 heads over 8,191-32,768 keys 110 us (6.1 TB/s, 90 % of a copy), 64
-// rows x 16 listed blocks 48 us (5.4 TB/s); single rows 8-11 us (latency).
+// Measured (bf16): latent, 16 rows x 128 heads over 30,001-119,999 keys 310 us
+// at 2,070 MHz (1,387 MB, 4.5 TB/s), 333 in a loop at the power limit (1,807
+// MHz); 1,024 rows x 128 heads over 2,048 listed keys each 609 us, 959 TFLOP/s:
+// both bound by the products, M = 64 at half rate; paged, 64 rows x 32 heads
+// over 8,191-32,768 keys 110 us (6.1 TB/s, 90 % of a copy), 64 rows x 16 listed
+// blocks 48 us (5.3 TB/s); single rows 8-11 us (latency).
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -624,6 +625,10 @@ __global__ void __launch_bounds__(Cfg<LATENT>::kThreads, 1) attention_kernel(con
             rot[n] = have ? __ldg(reinterpret_cast<const uint4*>(src + C::kQPieces * 64)) : make_uint4(0, 0, 0, 0);
           }
           cp_async_commit();
+          // (The parity cannot pass for the segment before the last one: after a
+          // segment of one tile the same team takes the queries and has waited for
+          // that one; after a longer one this place was free only once the last
+          // segment's queries were in TMEM, which they wait for.)
           ok = warp_try(smem_u32(&ctl.qempty[0]), (seg & 1) ^ 1, abort_flag, p.err);
           if (!ok) return;
 #pragma unroll

@@ -484,7 +484,9 @@ typedef enum fp4idx_dtype {
  * and is the same from call to call.  No allocation, no synchronisation;
  * graph-capturable; replays see updated device metadata.
  * Supported: page_size 64 or 128; num_indices <= 2^20; num_heads <= 1024;
- * max_seqlen_q <= 2^20; max_seqlen_k <= 2^30.
+ * max_seqlen_q <= 2^20; max_seqlen_k <= 2^30; fewer than 2^31 tiles of 64
+ * (latent) or 128 keys in all, counting max_seqlen_k keys (or the list) for
+ * every request (or listed row), K/V head and 512 (row, head) pairs.
  */
 typedef struct fp4idx_attention {
   int32_t dtype;            /* fp4idx_dtype_t */
@@ -527,8 +529,8 @@ fp4idx_status_t fp4idx_paged_attention(const fp4idx_attention_t* attention, void
 /*
  * Write 16-bit rows into the caches of fp4idx_attention_t by slot (token i at
  * page slots[i] / page_size, offset slots[i] % page_size; a negative slot is
- * skipped, one past the cache is skipped and sets FP4IDX_ERR_PAGE_RANGE; two
- * tokens with one slot: either may win).  The values are copied unchanged.
+ * skipped, one past the cache is skipped and sets FP4IDX_ERR_PAGE_RANGE; of
+ * two tokens with one slot each 16 bytes come from either).  The values are copied unchanged.
  *   fp4idx_store_latent  latent [N][512] and rope [N][64] (element strides
  *       latent_stride, rope_stride between tokens) into cache
  *       [num_pages][page_size][576].
