@@ -16,6 +16,11 @@ The functions keep the C names:
     fp4idx_paged_attention(attention, stream=None) -> (out [T, H, 128], lse [T, H])
     fp4idx_store_latent / fp4idx_store_kv(...)  -- the 16-bit caches' writers
     fp4idx_build_tables(...) -> (cu_seqlens_q, cu_seqlens_k, visible_len, slots, pages_taken)
+    fp4idx_shared_prefix_attention(shared, stream=None) -> (out [T, H, 128], lse [T, H])
+    fp4idx_fork_requests(...) -> (copy_src, copy_dst, pages_taken)
+    fp4idx_copy_pages(pages, src, dst, count=None, stream=None)
+    fp4idx_release_pages(...) -> (free_pages, num_free)
+    fp4idx_compact_pages(...) -> (new_table, copy_src, copy_dst, num_moves, extent)
     fp4idx_get_error(clear=True, stream=None) -> int
 """
 from __future__ import annotations
@@ -37,6 +42,7 @@ ERR_PAGE_RANGE = 0x1
 ERR_TIMEOUT = 0x2
 ERR_TOKEN_TABLE = 0x4
 ERR_LENGTHS = 0x8
+ERR_REQUESTS = 0x10
 KV_SPLIT = 0
 KV_FUSED = 1
 
@@ -60,6 +66,13 @@ EXPORTED = (
     "fp4idx_store_latent",
     "fp4idx_store_kv",
     "fp4idx_build_tables",
+    "fp4idx_shared_attention_workspace_bytes",
+    "fp4idx_shared_prefix_attention",
+    "fp4idx_fork_requests",
+    "fp4idx_copy_pages",
+    "fp4idx_pages_workspace_bytes",
+    "fp4idx_release_pages",
+    "fp4idx_compact_pages",
     "fp4idx_get_error",
     "fp4idx_status_string",
     "fp4idx_last_error_message",
@@ -135,6 +148,24 @@ class CAttention(ctypes.Structure):
     ]
 
 
+class CSharedAttention(ctypes.Structure):
+    """Mirror of fp4idx_shared_attention_t."""
+
+    _fields_ = [
+        ("attention", CAttention),
+        ("group_offsets", ctypes.c_void_p),
+        ("prefix_len", ctypes.c_void_p),
+        ("num_groups", ctypes.c_int32),
+        ("max_group_rows", ctypes.c_int32),
+    ]
+
+
+class CPageSpan(ctypes.Structure):
+    """Mirror of fp4idx_page_span_t."""
+
+    _fields_ = [("base", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("page_bytes", ctypes.c_int64)]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -198,6 +229,21 @@ def load_library(path: str = LIB_PATH):
         lib.fp4idx_store_kv.restype = i32
         lib.fp4idx_build_tables.argtypes = [vp, vp, i32, i32, i32, i64, vp, i32, vp, i64, vp, vp, vp, vp, vp, vp]
         lib.fp4idx_build_tables.restype = i32
+        S = ctypes.POINTER(CSharedAttention)
+        lib.fp4idx_shared_attention_workspace_bytes.argtypes = [S]
+        lib.fp4idx_shared_attention_workspace_bytes.restype = sz
+        lib.fp4idx_shared_prefix_attention.argtypes = [S, vp, sz, vp]
+        lib.fp4idx_shared_prefix_attention.restype = i32
+        lib.fp4idx_fork_requests.argtypes = [vp, vp, vp, i32, i32, i32, i64, vp, i32, vp, vp, i64, vp, vp, vp, vp]
+        lib.fp4idx_fork_requests.restype = i32
+        lib.fp4idx_copy_pages.argtypes = [ctypes.POINTER(CPageSpan), i32, i64, vp, vp, i32, vp, vp]
+        lib.fp4idx_copy_pages.restype = i32
+        lib.fp4idx_pages_workspace_bytes.argtypes = [i64]
+        lib.fp4idx_pages_workspace_bytes.restype = sz
+        lib.fp4idx_release_pages.argtypes = [vp, vp, i32, i32, i32, i64, vp, vp, i64, vp, vp, vp, sz, vp]
+        lib.fp4idx_release_pages.restype = i32
+        lib.fp4idx_compact_pages.argtypes = [vp, i32, i32, i64, vp, i64, i32, vp, i64, i32, vp, vp, vp, vp, vp, sz, vp]
+        lib.fp4idx_compact_pages.restype = i32
         lib.fp4idx_get_error.argtypes = [ctypes.POINTER(u32), i32, vp]
         lib.fp4idx_get_error.restype = i32
         lib.fp4idx_status_string.argtypes = [i32]
@@ -612,16 +658,22 @@ class DeviceAttention:
             visible_len=at(visible_len), qo_offset=at(qo_offset), causal=int(bool(causal)), scale=float(scale),
             indices=at(indices), num_indices=0 if indices is None else int(indices.shape[-1]), out=at(out),
             out_row_stride=_step(out, 0, H * dv), lse=at(lse))
-        self._ref = ctypes.byref(self.c)
-        need = int(load_library().fp4idx_attention_workspace_bytes(self._ref))
+        need = self._describe()
         if workspace is None:
             workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=q.device)
         self.workspace = workspace
         self._ws = (workspace.data_ptr(), workspace.numel() * workspace.element_size())
 
+    def _describe(self):
+        """The C call's argument; returns the workspace it needs."""
+        self._ref = ctypes.byref(self.c)
+        return int(load_library().fp4idx_attention_workspace_bytes(self._ref))
+
 
 def fp4idx_latent_attention(attention: DeviceAttention, stream=None):
     """Absorbed latent attention of every row over its visible or selected keys: (out [T, H, 512], lse [T, H])."""
+    if not isinstance(attention, DeviceAttention) or isinstance(attention, DeviceSharedAttention):
+        raise ValueError("a DeviceAttention is required")
     if not attention.q.is_cuda:
         raise ValueError("the tensors must be on a CUDA device")
     ws, size = attention._ws
@@ -633,6 +685,8 @@ def fp4idx_latent_attention(attention: DeviceAttention, stream=None):
 
 def fp4idx_paged_attention(attention: DeviceAttention, stream=None):
     """Grouped-query attention of every row over its visible keys or selected blocks: (out [T, H, 128], lse [T, H])."""
+    if not isinstance(attention, DeviceAttention) or isinstance(attention, DeviceSharedAttention):
+        raise ValueError("a DeviceAttention is required")
     if not attention.q.is_cuda:
         raise ValueError("the tensors must be on a CUDA device")
     ws, size = attention._ws
@@ -756,6 +810,213 @@ def fp4idx_build_tables(cached_len: torch.Tensor, new_len: torch.Tensor, block_t
     if status:
         _check(status, "fp4idx_build_tables")
     return cu_q, cu_k, visible, slots, taken
+
+
+class DeviceSharedAttention(DeviceAttention):
+    """Device tensors of one call over requests that share a prefix plus its fp4idx_shared_attention_t.
+
+    The arguments of DeviceAttention for a K/V cache without indices, and group_offsets [G+1] i32 (group g is the
+    requests group_offsets[g] .. group_offsets[g+1]), prefix_len [G] i32 (positions that a group's requests share) and
+    the host bound max_group_rows of a group's query rows.
+    """
+
+    def __init__(self, *, q, k, v, group_offsets, prefix_len, max_group_rows: int, workspace=None, **rest):
+        if v is None or rest.get("indices") is not None:
+            raise ValueError("a shared prefix is attended to whole, in K/V caches")
+        for name, x in (("group_offsets", group_offsets), ("prefix_len", prefix_len)):
+            if x.dtype != torch.int32 or x.dim() != 1 or not x.is_contiguous() or x.device != q.device:
+                raise ValueError(f"{name} must be a contiguous 1-D int32 tensor on q's device")
+        G = int(prefix_len.shape[0])
+        if G < 1 or group_offsets.shape[0] != G + 1:
+            raise ValueError("group_offsets must be [G+1] and prefix_len [G], G >= 1")
+        self.group_offsets, self.prefix_len, self.max_group_rows = group_offsets, prefix_len, int(max_group_rows)
+        super().__init__(q=q, k=k, v=v, workspace=workspace, **rest)
+
+    def _describe(self):
+        self.shared = CSharedAttention(attention=self.c, group_offsets=self.group_offsets.data_ptr(),
+                                       prefix_len=self.prefix_len.data_ptr(), num_groups=int(self.prefix_len.shape[0]),
+                                       max_group_rows=self.max_group_rows)
+        self._ref = ctypes.byref(self.shared)
+        return int(load_library().fp4idx_shared_attention_workspace_bytes(self._ref))
+
+
+def fp4idx_shared_prefix_attention(shared: DeviceSharedAttention, stream=None):
+    """Grouped-query attention of requests whose groups share a prefix: (out [T, H, 128], lse [T, H])."""
+    if not isinstance(shared, DeviceSharedAttention):
+        raise ValueError("a DeviceSharedAttention is required")
+    if not shared.q.is_cuda:
+        raise ValueError("the tensors must be on a CUDA device")
+    _on_current(shared.q.get_device())
+    ws, size = shared._ws
+    status = load_library().fp4idx_shared_prefix_attention(shared._ref, ws, size, _stream(stream))
+    if status:
+        _check(status, "fp4idx_shared_prefix_attention")
+    return shared.out, shared.lse
+
+
+def _lists(named, device, dim=1):
+    """Contiguous int32 tensors of one number of dimensions on the current device, or a ValueError."""
+    for name, x in named:
+        if x is not None and (x.dtype != torch.int32 or x.dim() != dim or not x.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {dim}-D int32 tensor")
+    for _, x in named:
+        if x is not None and (x.get_device() != device or device < 0):  # -1: host
+            raise ValueError(_ONE_DEVICE)
+    _on_current(device)
+
+
+def _on_current(device):
+    """The library launches on the current device: another one's addresses mean nothing there."""
+    if device != (torch.cuda.current_device() if _raw_device is None else _raw_device()):
+        raise ValueError("the tensors must be on the current CUDA device")
+
+
+def _table(table, reqs, name="block_table"):
+    """Row width of a table [reqs, width] that may be written to or read up to its rows' ends."""
+    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != reqs or table.shape[1] < 1 or table.stride(1) != 1:
+        raise ValueError(f"{name} must be int32 [B, stride] with dense rows")
+    if _step(table, 0, table.shape[1]) != table.shape[1]:
+        raise ValueError(f"{name} must not be a view of wider rows")
+    return int(table.shape[1])
+
+
+def _outputs(out, named, device):
+    """The tensors of ``out``, judged, or new ones; named: (name, entries)."""
+    if out is None:
+        return [torch.empty((n,), dtype=torch.int32, device=device) for _, n in named]
+    if len(out) != len(named):
+        raise ValueError("out: " + ", ".join(name for name, _ in named))
+    for x, (name, n) in zip(out, named):
+        if x.dtype != torch.int32 or x.numel() != n or not x.is_contiguous() or x.device != device:
+            raise ValueError(f"out: {name} must be a contiguous int32 tensor of {n} entries on the device of the table")
+    return list(out)
+
+
+def fp4idx_fork_requests(parent: torch.Tensor, child: torch.Tensor, cached_len: torch.Tensor, block_table: torch.Tensor,
+                         free_pages: torch.Tensor, page_size: int, fork_len: Optional[torch.Tensor] = None,
+                         num_pages: Optional[int] = None, out=None, stream=None):
+    """Requests child [N] continue requests parent [N] (the first fork_len [N] tokens, default all): their rows of
+    block_table [B, stride] and entries of cached_len [B] are written in place, unfinished pages taken from free_pages [F].
+    Returns (copy_src [N], copy_dst [N], pages_taken [1]): the unfinished pages to copy (fp4idx_copy_pages), -1 for none.
+    ``num_pages`` bounds the page ids (default: any); ``out`` may give the three tensors."""
+    dev = cached_len.get_device()
+    _lists((("parent", parent), ("child", child), ("cached_len", cached_len), ("free_pages", free_pages), ("fork_len", fork_len)), dev)
+    N, B = parent.shape[0], cached_len.shape[0]
+    if child.shape[0] != N or (fork_len is not None and fork_len.shape[0] != N):
+        raise ValueError("parent, child and fork_len must have one length")
+    width = _table(block_table, B)
+    if block_table.get_device() != dev:
+        raise ValueError(_ONE_DEVICE)
+    src, dst, taken = _outputs(out, (("copy_src", N), ("copy_dst", N), ("pages_taken", 1)), cached_len.device)
+    if num_pages is None:
+        num_pages = (2 ** 31 - 1) // page_size if page_size > 0 else 1
+    status = load_library().fp4idx_fork_requests(
+        parent.data_ptr(), child.data_ptr(), None if fork_len is None else fork_len.data_ptr(), N, B, page_size, num_pages,
+        free_pages.data_ptr(), free_pages.shape[0], cached_len.data_ptr(), block_table.data_ptr(), width, src.data_ptr(),
+        dst.data_ptr(), taken.data_ptr(), _stream(stream))
+    if status:
+        _check(status, "fp4idx_fork_requests")
+    return src, dst, taken
+
+
+class DevicePages:
+    """The caches of one block table, for fp4idx_copy_pages: tensors [P, ...] of any type, dense inside a page (a layer's
+    slice of a larger allocation, a split index cache's codes and scales, a fused table).  Holds pointers: rebuild it
+    when a cache moves."""
+
+    def __init__(self, caches):
+        self.caches = list(caches)
+        if not self.caches:
+            raise ValueError("at least one cache is required")
+        self.num_pages, self.device = int(self.caches[0].shape[0]), self.caches[0].device
+        spans = (CPageSpan * len(self.caches))()
+        for x, span in zip(self.caches, spans):
+            if x.dim() < 2 or x.shape[0] != self.num_pages or self.num_pages < 1 or not x[0].is_contiguous():
+                raise ValueError("every cache must be [P, ...] with one P, dense inside a page")
+            if x.device != self.device:
+                raise ValueError(_ONE_DEVICE)
+            size = x[0].numel() * x.element_size()
+            span.base, span.page_bytes, span.page_stride = x.data_ptr(), size, _step(x, 0, x[0].numel()) * x.element_size()
+        self.spans = spans
+
+
+def fp4idx_copy_pages(pages: DevicePages, src: torch.Tensor, dst: torch.Tensor, count: Optional[torch.Tensor] = None,
+                      stream=None) -> None:
+    """Copy page src[i] to page dst[i] in every cache of ``pages`` (int32 lists; negative entries are skipped).
+    ``count`` [1] int32: only that many entries, read on the device."""
+    if not pages.device.type == "cuda":
+        raise ValueError("the tensors must be on a CUDA device")
+    _lists((("src", src), ("dst", dst), ("count", count)), pages.device.index or 0)
+    if src.shape != dst.shape or (count is not None and count.numel() != 1):
+        raise ValueError("src and dst must have one length and count one entry")
+    status = load_library().fp4idx_copy_pages(pages.spans, len(pages.caches), pages.num_pages, src.data_ptr(), dst.data_ptr(),
+                                              src.shape[0], None if count is None else count.data_ptr(), _stream(stream))
+    if status:
+        _check(status, "fp4idx_copy_pages")
+
+
+def fp4idx_pages_workspace_bytes(num_pages: int) -> int:
+    return int(load_library().fp4idx_pages_workspace_bytes(int(num_pages)))
+
+
+def _pages_workspace(workspace, num_pages, device):
+    if workspace is None:
+        return torch.empty((max(1, fp4idx_pages_workspace_bytes(num_pages)),), dtype=torch.uint8, device=device)
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous, on the device of the table")
+    return workspace
+
+
+def fp4idx_release_pages(requests: Optional[torch.Tensor], cached_len: torch.Tensor, block_table: torch.Tensor, page_size: int,
+                         num_pages: int, keep_len: Optional[torch.Tensor] = None, out=None, workspace=None, stream=None):
+    """Requests [N] (None: none) keep their first keep_len [N] tokens (default 0; cached_len [B] in place); returns
+    (free_pages [num_pages], num_free [1]): the pages that no held entry of block_table [B, stride] names, ascending, -1
+    behind them.  ``out`` may give the two tensors, ``workspace`` fp4idx_pages_workspace_bytes(num_pages) bytes."""
+    dev = cached_len.get_device()
+    _lists((("cached_len", cached_len), ("requests", requests), ("keep_len", keep_len)), dev)
+    B, N = cached_len.shape[0], 0 if requests is None else requests.shape[0]
+    if keep_len is not None and keep_len.shape[0] != N:
+        raise ValueError("requests and keep_len must have one length")
+    width = _table(block_table, B)
+    if block_table.get_device() != dev:
+        raise ValueError(_ONE_DEVICE)
+    free, count = _outputs(out, (("free_pages", num_pages), ("num_free", 1)), cached_len.device)
+    workspace = _pages_workspace(workspace, num_pages, cached_len.device)
+    status = load_library().fp4idx_release_pages(
+        None if N == 0 else requests.data_ptr(), None if keep_len is None else keep_len.data_ptr(), N, B, page_size, num_pages,
+        cached_len.data_ptr(), block_table.data_ptr(), width, free.data_ptr(), count.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream(stream))
+    if status:
+        _check(status, "fp4idx_release_pages")
+    return free, count
+
+
+def fp4idx_compact_pages(cached_len: torch.Tensor, block_table: torch.Tensor, page_size: int, num_pages: int, max_moves: int,
+                         out_table: Optional[torch.Tensor] = None, out=None, workspace=None, stream=None):
+    """Up to max_moves moves of the highest pages in use into the lowest free ones: (new_table, copy_src [max_moves],
+    copy_dst [max_moves], num_moves [1], extent [1]).  The rows go to ``out_table`` (default: block_table itself); the
+    pages' contents are moved by fp4idx_copy_pages(pages, copy_src, copy_dst, count=num_moves).  ``out`` may give the
+    last four tensors, ``workspace`` fp4idx_pages_workspace_bytes(num_pages) bytes."""
+    dev = cached_len.get_device()
+    _lists((("cached_len", cached_len),), dev)
+    B = cached_len.shape[0]
+    width = _table(block_table, B)
+    to = block_table if out_table is None else out_table
+    new_width = _table(to, B, "out_table")
+    if block_table.get_device() != dev or to.get_device() != dev:
+        raise ValueError(_ONE_DEVICE)
+    if new_width < width:
+        raise ValueError("out_table must be at least as wide as block_table")
+    src, dst, moves, extent = _outputs(out, (("copy_src", max_moves), ("copy_dst", max_moves), ("num_moves", 1), ("extent", 1)),
+                                       cached_len.device)
+    workspace = _pages_workspace(workspace, num_pages, cached_len.device)
+    status = load_library().fp4idx_compact_pages(
+        cached_len.data_ptr(), B, page_size, num_pages, block_table.data_ptr(), width, width, to.data_ptr(), new_width, max_moves,
+        src.data_ptr(), dst.data_ptr(), moves.data_ptr(), extent.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream(stream))
+    if status:
+        _check(status, "fp4idx_compact_pages")
+    return to, src, dst, moves, extent
 
 
 def fp4idx_get_error(clear: bool = True, stream=None) -> int:

@@ -1,6 +1,6 @@
 """Build libfp4idx.so (the CUDA library behind include/fp4idx.h) for sm_103a.
 
-Each translation unit under csrc/ is compiled by nvcc in parallel into
+Each translation unit under csrc/ and csrc_shared/ is compiled by nvcc in parallel into
 _build/, then linked into fp4_sparse_attention_gb300/libfp4idx.so.  A unit is
 recompiled only when it or a header is newer than its object file.
 
@@ -17,13 +17,14 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
+CSRC_SHARED = os.path.join(PKG, "csrc_shared")  # requests that share a prefix: no part of the indexer's launches
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfp4idx.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
-              "-I", INCLUDE, "-I", CSRC]
+              "-I", INCLUDE, "-I", CSRC, "-I", CSRC_SHARED]
 
 
 def _nvcc() -> str:
@@ -34,8 +35,7 @@ def _nvcc() -> str:
 
 
 def _headers():
-    return glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
-        glob.glob(os.path.join(INCLUDE, "*.h"))
+    return [h for d in (CSRC, CSRC_SHARED, INCLUDE) for kind in ("*.cuh", "*.h") for h in glob.glob(os.path.join(d, kind))]
 
 
 def _compile(src: str, obj: str, force: bool, verbose: bool) -> str:
@@ -57,7 +57,7 @@ def _compile(src: str, obj: str, force: bool, verbose: bool) -> str:
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile and link libfp4idx.so; return its path."""
     os.makedirs(BUILD, exist_ok=True)
-    srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu"))) + sorted(glob.glob(os.path.join(CSRC_SHARED, "*.cu")))
     objs = [os.path.join(BUILD, os.path.basename(s)[:-3] + ".o") for s in srcs]
     with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
         list(ex.map(lambda so: _compile(so[0], so[1], force, verbose), zip(srcs, objs)))

@@ -27,6 +27,8 @@ fp4idx_status_t cuda_status(cudaError_t e, const char* what) {
   FAIL(FP4IDX_ECUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+}  // namespace
+
 // Arguments of either attention call.
 fp4idx_status_t check_attention(const fp4idx_attention_t* a, bool latent) {
   if (!a) FAIL(FP4IDX_EINVAL, "attention is NULL");
@@ -138,6 +140,8 @@ fp4idx_status_t cache_maps(const fp4idx_attention_t* a, bool latent, AttnMaps* m
   if (s != FP4IDX_OK || latent) return s;
   return call_tensor_map16(&maps->v, a->v, 4, dims, strides, box);
 }
+
+namespace {
 
 fp4idx_status_t attention_any(const fp4idx_attention_t* a, bool latent, void* workspace, size_t workspace_bytes,
                               void* stream) {

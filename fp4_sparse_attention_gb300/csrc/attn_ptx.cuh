@@ -50,7 +50,7 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-__device__ __noinline__ bool warp_try_again(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* err) {
+static __device__ __noinline__ bool warp_try_again(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* err) {
   const uint64_t t0 = globaltimer();
   bool ok = false;
   for (;;) {

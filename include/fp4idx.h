@@ -82,6 +82,9 @@ typedef enum fp4idx_status {
 #define FP4IDX_ERR_LENGTHS 0x8u     /* fp4idx_build_tables: a negative length, more rows
                                        than the caller's row count, a request longer than
                                        its table row, or too few free pages         */
+#define FP4IDX_ERR_REQUESTS 0x10u   /* fp4idx_fork_requests, fp4idx_release_pages: a request
+                                       number past the table; a fork's child that an earlier
+                                       fork names or that is some fork's parent     */
 
 /* Key-cache layouts (fp4idx_problem_t.kv_layout). */
 #define FP4IDX_KV_SPLIT 0  /* k [P][Hkv][page][64] and k_scale [P][Hkv][page][G]     */
@@ -577,6 +580,160 @@ fp4idx_status_t fp4idx_build_tables(const int32_t* cached_len, const int32_t* ne
                                     const int32_t* free_pages, int32_t num_free, int32_t* block_table,
                                     int64_t table_stride, int32_t* cu_seqlens_q, int32_t* cu_seqlens_k,
                                     int32_t* visible_len, int32_t* slots, int32_t* pages_taken, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Requests that share a prefix: attention that reads it once, and the page
+ * operations that make and undo the sharing.
+ *
+ * Requests share pages by naming them in more than one block-table row.  No
+ * counts are kept: the held entries of the tables -- the first
+ * ceil(cached_len[b] / page_size) of row b -- are all that says which pages
+ * are in use, so the calls can be repeated and nothing can drift.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * Grouped-query attention of requests that share a prefix.  The result is that
+ * of fp4idx_paged_attention on `attention` (v given, indices NULL); the keys
+ * that a group's requests share are read once for the rows of all of them.
+ *   group_offsets [num_groups + 1] int32, device: group g is the requests
+ *             [group_offsets[g], group_offsets[g+1]); it does not decrease, starts at 0
+ *             and ends at num_seqs.  (Values outside [0, num_seqs] count as the
+ *             nearer end.  Requests before the first or behind the last group
+ *             are in none: their rows get out = 0 and lse = -inf.)
+ *   prefix_len    [num_groups] int32, device: the first prefix_len[g] positions
+ *             are the same keys and values for every request of the group, and
+ *             are read through the table row of its first request, whose key
+ *             count bounds them (negative: 0).  Any length; the other requests'
+ *             own entries below it are read only for the 64 positions that it
+ *             ends in and must be valid there.
+ *   max_group_rows  host upper bound of a group's query rows; it must hold for
+ *             the device data.
+ * Everything else as for fp4idx_attention_t: visibility of each row, rows
+ * behind the requests', page errors, values that nobody may see.  A position
+ * below prefix_len that some row of the group sees must hold finite values for
+ * all of them.
+ * Workspace: fp4idx_shared_attention_workspace_bytes(), 16-byte aligned,
+ * uninitialised.  The result is the same from call to call.  No allocation, no
+ * synchronisation; graph-capturable; replays see updated device metadata.
+ * Supported: as fp4idx_paged_attention, up to 2^20 groups and at most 2^20 rows
+ * a group; num_groups * ceil(max_group_rows * H / Hkv / 256) at most 2^20.
+ */
+typedef struct fp4idx_shared_attention {
+  fp4idx_attention_t attention;
+  const int32_t* group_offsets;
+  const int32_t* prefix_len;
+  int32_t num_groups;
+  int32_t max_group_rows;
+} fp4idx_shared_attention_t;
+
+size_t fp4idx_shared_attention_workspace_bytes(const fp4idx_shared_attention_t* shared);
+fp4idx_status_t fp4idx_shared_prefix_attention(const fp4idx_shared_attention_t* shared, void* workspace,
+                                               size_t workspace_bytes, void* stream);
+
+/*
+ * Children that continue a parent.  Fork i makes request child[i] hold the
+ * first L = min(fork_len[i], cached_len[parent[i]]) tokens of request parent[i]
+ * (fork_len NULL: all of them):
+ *   block_table row child[i], in place: the parent's entries of the
+ *             floor(L / page_size) full pages; when L ends inside a page, then a
+ *             page of its own, taken from free_pages in the order of the forks.
+ *             Entries behind them are not touched.
+ *   cached_len  [num_reqs] int32, in place: entry child[i] becomes L.
+ *   copy_src, copy_dst  [num_forks] int32: the unfinished page and the child's
+ *             own one (fp4idx_copy_pages' input), or -1 and -1.
+ *   pages_taken [1] the number of free pages used.
+ * The children's rows must hold nothing that is still wanted (release them
+ * first).  A negative parent or child is no fork (padding of a fixed-size
+ * call).  Refused, with -1 and -1 and the child left as it was:
+ * FP4IDX_ERR_REQUESTS -- a number not below num_reqs; a child that an earlier
+ * fork of the call names (counted as taking its page) or that is the parent of
+ * any fork; FP4IDX_ERR_LENGTHS -- a parent longer than its table row.  Without a free page left the child's
+ * unfinished page is entered as -1 and FP4IDX_ERR_LENGTHS is set.  A parent's
+ * unfinished page outside [0, num_pages) gives -1 and -1 and
+ * FP4IDX_ERR_PAGE_RANGE (full pages are shared as they are).  Negative lengths
+ * count as 0.  A call repeated on its own results enters the same pages again.
+ * One launch, no workspace, graph-capturable.  Supported: page_size 64 or 128,
+ * num_pages * page_size < 2^31.
+ */
+fp4idx_status_t fp4idx_fork_requests(const int32_t* parent, const int32_t* child, const int32_t* fork_len,
+                                     int32_t num_forks, int32_t num_reqs, int32_t page_size, int64_t num_pages,
+                                     const int32_t* free_pages, int32_t num_free, int32_t* cached_len,
+                                     int32_t* block_table, int64_t table_stride, int32_t* copy_src,
+                                     int32_t* copy_dst, int32_t* pages_taken, void* stream);
+
+/*
+ * Copy pages inside each of several caches (the layers' latent, K, V and index
+ * caches that one block table addresses): page dst[i] becomes page src[i] in
+ * every span.
+ *   spans     [num_spans], HOST memory, read during the call: page p of a span
+ *             is the page_bytes bytes at base + p * page_stride (bytes; all
+ *             three multiples of 16, page_stride >= page_bytes).
+ *   src, dst  [num_copies] int32, device.  An entry with a negative src or dst
+ *             is skipped, one with either >= num_pages is skipped and sets
+ *             FP4IDX_ERR_PAGE_RANGE.
+ *   count     [1] int32, device, or NULL: only the first count[0] entries.
+ * The sources are read and the destinations written in no order: a page that is
+ * both gives either content, and of two copies into one page each 16 bytes come
+ * from either.  (The lists of the two calls around this one name no page as
+ * both, and no destination twice.)
+ * One launch (none without copies), no workspace, graph-capturable.
+ * Supported: up to 256 spans, fewer than 2^31 copies.
+ */
+typedef struct fp4idx_page_span {
+  void* base;
+  int64_t page_stride;
+  int64_t page_bytes;
+} fp4idx_page_span_t;
+
+fp4idx_status_t fp4idx_copy_pages(const fp4idx_page_span_t* spans, int32_t num_spans, int64_t num_pages,
+                                  const int32_t* src, const int32_t* dst, int32_t num_copies, const int32_t* count,
+                                  void* stream);
+
+/*
+ * Requests dropped or cut back, and the pages that nobody holds.
+ *   requests  [num_released] int32, device: cached_len[requests[i]] becomes
+ *             min(itself, keep_len[i]) (keep_len NULL or negative: 0).  Negative
+ *             numbers are skipped, those not below num_reqs skipped with
+ *             FP4IDX_ERR_REQUESTS; a request named twice keeps the least.
+ *   free_pages  [num_pages] int32: every page of [0, num_pages) that no held
+ *             entry of the block table names after that, ascending, then -1.
+ *   num_free  [1] their number.
+ * (num_released 0: the list alone.)  Table entries are not written.  A held
+ * entry outside [0, num_pages), or behind table_stride, names no page and sets
+ * FP4IDX_ERR_PAGE_RANGE (FP4IDX_ERR_LENGTHS).
+ * Workspace: fp4idx_pages_workspace_bytes(num_pages), 16-byte aligned,
+ * uninitialised, shared with fp4idx_compact_pages.  Graph-capturable, no
+ * synchronisation.  Supported: page_size 64 or 128, num_pages * page_size < 2^31.
+ */
+size_t fp4idx_pages_workspace_bytes(int64_t num_pages);
+fp4idx_status_t fp4idx_release_pages(const int32_t* requests, const int32_t* keep_len, int32_t num_released,
+                                     int32_t num_reqs, int32_t page_size, int64_t num_pages, int32_t* cached_len,
+                                     const int32_t* block_table, int64_t table_stride, int32_t* free_pages,
+                                     int32_t* num_free, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Moves that bring the pages in use together at the pool's start.  With n pages
+ * in use (named by a held entry), the ones at or above n, highest first, go to
+ * the free ones below n, lowest first; max_moves bounds their number (a step's
+ * budget), so that a larger job is done over several calls.
+ *   copy_src, copy_dst  [max_moves] int32: the moves, then -1: the input of
+ *             fp4idx_copy_pages, to run before any reader of new_table.  No page
+ *             is both a source and a destination.
+ *   new_table [num_reqs][new_stride] int32: block_table with every held entry
+ *             at its page's new place; the other entries of the row copied
+ *             unchanged.  May be block_table itself (new_stride = table_stride).
+ *   num_moves [1] the number of moves.
+ *   extent    [1] 1 + the highest page in use afterwards (n when all moves fit):
+ *             the pool can be cut to that many pages.
+ * width = entries of a row that are copied (<= both strides).  Held entries
+ * outside [0, num_pages) or behind `width` as in fp4idx_release_pages (kept as
+ * they are).  Workspace as there.  Graph-capturable, no synchronisation.
+ */
+fp4idx_status_t fp4idx_compact_pages(const int32_t* cached_len, int32_t num_reqs, int32_t page_size,
+                                     int64_t num_pages, const int32_t* block_table, int64_t table_stride,
+                                     int32_t width, int32_t* new_table, int64_t new_stride, int32_t max_moves,
+                                     int32_t* copy_src, int32_t* copy_dst, int32_t* num_moves, int32_t* extent,
+                                     void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Device error word of the current device (FP4IDX_ERR_* bits).  Synchronises
