@@ -127,6 +127,8 @@ AttnParams attention_params(const fp4idx_attention_t* a) {
   return p;
 }
 
+namespace {
+
 // Tensor maps of the caches (selected latent rows are copied without one).
 fp4idx_status_t cache_maps(const fp4idx_attention_t* a, bool latent, AttnMaps* maps) {
   std::memset(maps, 0, sizeof(*maps));
@@ -140,8 +142,6 @@ fp4idx_status_t cache_maps(const fp4idx_attention_t* a, bool latent, AttnMaps* m
   if (s != FP4IDX_OK || latent) return s;
   return call_tensor_map16(&maps->v, a->v, 4, dims, strides, box);
 }
-
-namespace {
 
 fp4idx_status_t attention_any(const fp4idx_attention_t* a, bool latent, void* workspace, size_t workspace_bytes,
                               void* stream) {

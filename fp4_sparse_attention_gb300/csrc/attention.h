@@ -116,11 +116,10 @@ fp4idx_status_t call_device(int* sms, uint32_t** err);
 fp4idx_status_t call_tensor_map16(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
                                   const cuuint64_t* strides, const cuuint32_t* box);
 
-// Checks, parameters (without the error word and the work split) and tensor
-// maps of an attention call (api_attention.cu).
+// Checks and parameters (without the error word and the work split) of an
+// attention call (api_attention.cu).
 fp4idx_status_t check_attention(const fp4idx_attention_t* a, bool latent);
 AttnParams attention_params(const fp4idx_attention_t* a);
-fp4idx_status_t cache_maps(const fp4idx_attention_t* a, bool latent, AttnMaps* maps);
 
 // Fills the work split of p; false if it does not fit the counters.
 bool plan_attention(AttnParams* p, int sms);

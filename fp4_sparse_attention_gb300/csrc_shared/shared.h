@@ -84,8 +84,12 @@ struct SharedParams {
   const int32_t* prefix_len;
   int32_t num_groups;
   int32_t max_group_rows;
+  // work split (plan_shared)
+  int32_t blocks_per_group;
+  int32_t ctas;
 };
 
+// Fills the work split; false if it does not fit the counters.
 bool plan_shared(SharedParams* p, int sms);
 size_t shared_workspace(const SharedParams& p);
 cudaError_t launch_shared(SharedParams p, const AttnMaps& maps, int dtype, void* workspace, cudaStream_t stream);
