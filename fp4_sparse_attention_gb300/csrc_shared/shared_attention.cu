@@ -22,12 +22,16 @@
 // on the other's: with more than 128 pairs the two hold the block's halves and
 // share each tile; with fewer they hold the same rows and take tiles in turn,
 // and the end adds them up.  A softmax thread owns a row, so it needs no other
-// thread's maximum, sum or factor.
+// thread's maximum, sum or factor.  It takes the weights of a tile relative to
+// the reference of the tiles before and looks at their sum: only where that is
+// too large (or there is no reference yet) does it go over the scores for a
+// maximum, so that a tile's scores are read once.
 //
 // Roles: warps 0-3 and 4-7 softmax of the two accumulators, queries and output;
-// warp 8 MMA issuer; warp 9 loader (TMA; 16-byte copies, which can leave zeros
-// where a value may be anything, for the values of a run that ends inside);
-// warp 10 planner, which looks up the tiles' pages ahead of all of them.
+// warps 8 and 9 issue the products of one accumulator each; warp 10 loader
+// (TMA; 16-byte copies, which can leave zeros where a value may be anything,
+// for the values of a run that ends inside); warp 11 planner, which looks up
+// the tiles' pages ahead of all of them and hands them out in chunks.
 #include <algorithm>
 #include <atomic>
 #include <cstddef>
@@ -43,20 +47,22 @@ constexpr int kTile = 128;                 // keys of a tile: two runs of 64, ea
 constexpr int kRows = 128;                 // rows of an accumulator
 constexpr int kBlockPairs = 2 * kRows;
 constexpr int kSoftmaxWarps = 4;           // of one accumulator
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kPlanWarp = 10;
-constexpr int kThreads = 352;
+constexpr int kMmaWarp = 2 * kSoftmaxWarps, kLoadWarp = kMmaWarp + 2, kPlanWarp = kMmaWarp + 3;
+constexpr int kThreads = 32 * (kPlanWarp + 1);
 constexpr int kStages = 5;
 constexpr uint32_t kStage = 32768, kPiece = 128 * 128, kRun = 64 * 128;
 constexpr uint32_t kQBytes = 2 * kPiece;   // 128 rows x 128 values
-constexpr int kDescs = 16;                 // tiles that the planner may be ahead
+constexpr int kChunks = 6, kChunkTiles = 12;  // chunks that the planner may be ahead, tiles of a chunk
 constexpr uint32_t kTmemCols = 512, kOCol = 256;
 constexpr int kGroupShift = 40;            // pair / group as (pair * ceil(2^40 / group)) >> 40 (attention.cu)
-// A row's reference maximum is raised only when the true one is 2^8 above it, and
-// in fp16 lies another 2^7 lower, so that shares down to 2^-32 are kept
-// (attention.cu has the same two).
-constexpr float kRaise = 8.0f;
+// A row's reference is its maximum when it is set, in fp16 2^7 less, so that
+// shares down to 2^-32 are kept (attention.cu).  It is set anew when a tile's
+// weights add up to more than the limit: in fp16 the type's range (the sum
+// bounds each weight), in bf16 far below that of fp32.
 template <int DTYPE>
 constexpr float kBelow = DTYPE == FP4IDX_FP16 ? 7.0f : 0.0f;
+template <int DTYPE>
+constexpr float kLimit = DTYPE == FP4IDX_FP16 ? 32768.0f : 16777216.0f;
 
 // ---------------------------------------------------------------- plan
 struct Block {
@@ -227,26 +233,27 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
 }
 
 // ---------------------------------------------------------------- main kernel
-enum : int32_t { kSlot0 = 1, kSlot1 = 2, kFirst = 4, kLast = 8, kEnd = 16, kTail = 32, kTwo = 64, kWhole = 128 };
+enum : int32_t { kFirst = 1, kLast = 2, kEnd = 4, kTwo = 8, kWhole = 16, kHole0 = 32, kHole1 = 64, kTail = 128, kOdd = 256, kSlot0 = 512, kSlot1 = 1024 };
 
-// One tile, and with its first one what a segment (a run of one block's tiles) is.
-struct Desc {
-  int32_t flags;
-  int32_t page[2];       // of its runs; -1: no keys
-  int32_t pos0, lo, hi;  // position of its first key; keys that count
+// Up to kChunkTiles consecutive tiles of one span; a tile with a page that is
+// not there, or a run that ends inside, is a chunk of its own.
+struct Chunk {
+  int32_t flags;         // kFirst / kLast: holds the first / last tile of a segment (a run of one block's tiles)
+  int32_t tiles;
+  int32_t pos0, lo, hi;  // position of the first key; keys that count
   int32_t p0, p1;        // pairs of the block that they count for
   int32_t row0, pair0, pairs, hk;
-  int32_t part;          // slot of its partial sums
-  int32_t pad[3];
+  int32_t part;          // slot of the segment's partial sums
+  int32_t page[kChunkTiles][2];  // -1: no keys
 };
 
 struct Control {
-  uint64_t dfull[kDescs], dempty[kDescs];
+  uint64_t cfull[kChunks], cempty[kChunks];
   uint64_t kfull[kStages], kempty[kStages];
-  uint64_t sfull[2], pfull[2], odone[2], ofree[2], qfull[2];
-  uint64_t qfree, mfull, drain;
-  Desc desc[kDescs];
-  float2 other[kRows];   // the second accumulator's maximum and sum, when both hold the same rows
+  uint64_t sfull[2], pfull[2], odone[2], qfull[2];
+  uint64_t turn[2], mfull, mfree, drain;
+  Chunk chunk[kChunks];
+  float2 other[kRows];   // the second accumulator's reference and sum, when both hold the same rows
   int32_t warp_sum[kThreads / 32];
   int32_t run_hk, run_block, run_start, run_lo, run_hi, per_head;
   uint32_t tmem;
@@ -313,24 +320,24 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
     return;
   }
   if (tid == 0) {
-    for (int k = 0; k < kDescs; ++k) {
-      mbar_init(smem_u32(&ctl.dfull[k]), 1);
-      mbar_init(smem_u32(&ctl.dempty[k]), 2 * kSoftmaxWarps + 2);
+    for (int k = 0; k < kChunks; ++k) {
+      mbar_init(smem_u32(&ctl.cfull[k]), 1);
+      mbar_init(smem_u32(&ctl.cempty[k]), kPlanWarp);
     }
     for (int k = 0; k < kStages; ++k) {
       mbar_init(smem_u32(&ctl.kfull[k]), 1);
-      mbar_init(smem_u32(&ctl.kempty[k]), 1);
+      mbar_init(smem_u32(&ctl.kempty[k]), 2);
     }
     for (int k = 0; k < 2; ++k) {
       mbar_init(smem_u32(&ctl.sfull[k]), 1);
       mbar_init(smem_u32(&ctl.pfull[k]), kSoftmaxWarps);
       mbar_init(smem_u32(&ctl.odone[k]), 1);
-      mbar_init(smem_u32(&ctl.ofree[k]), kSoftmaxWarps);
+      mbar_init(smem_u32(&ctl.turn[k]), 1);
       mbar_init(smem_u32(&ctl.qfull[k]), kSoftmaxWarps);
     }
-    mbar_init(smem_u32(&ctl.qfree), 1);
     mbar_init(smem_u32(&ctl.mfull), kSoftmaxWarps);
-    mbar_init(smem_u32(&ctl.drain), 1);
+    mbar_init(smem_u32(&ctl.mfree), kSoftmaxWarps);
+    mbar_init(smem_u32(&ctl.drain), 2);
     ctl.abort = 0;
     fence_barrier_init();
   }
@@ -391,31 +398,17 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
   const uint32_t tmem = ctl.tmem;
   pdl_launch_dependents();  // the join may take its place; it waits for this grid's end
 
-  // Calls f(tile, n) for every tile of this CTA, in order, n counting them;
-  // whole warps.  f returns whether to go on.
-  const auto for_tiles = [&](auto&& f) {
-    for (uint32_t n = 0;; ++n) {
-      const uint32_t slot = n % kDescs;
-      if (!warp_try(smem_u32(&ctl.dfull[slot]), (n / kDescs) & 1, abort_flag, p.err)) return false;
-      const Desc& d = ctl.desc[slot];
-      if (d.flags & kEnd) return true;
-      const bool ok = f(d, n);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ctl.dempty[slot]));
-      if (!ok) return false;
-    }
-  };
-
   if (warp == kPlanWarp) {
     // ================================================================ planner
-    uint32_t n = 0;  // tiles published
+    uint32_t n = 0;  // chunks published
     bool ok = true;
     const int hi = ctl.run_hi, per_head = ctl.per_head;
     int at = ctl.run_lo, hk = ctl.run_hk, block = ctl.run_block, start = ctl.run_start;
     while (ok && at < hi) {
       const Block b = pl.block[block];
       const int from = at - start, to = min(b.tiles, hi - start);  // tiles of the block
-      const bool two = b.pairs > kRows, whole = from == 0 && to == b.tiles;
+      const bool two = b.pairs > kRows;
+      const int segment = (two ? kTwo : 0) | (from == 0 && to == b.tiles ? kWhole : 0);
       int done = from;
       for (int s0 = 0; ok && done < to && s0 < b.spans; s0 += 32) {
         Span mine = {};
@@ -429,47 +422,59 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
           const int k_hi = __shfl_sync(0xffffffffu, mine.hi, x);
           const int p0 = __shfl_sync(0xffffffffu, mine.p0, x), p1 = __shfl_sync(0xffffffffu, mine.p1, x);
           const int64_t table = attn_table_base(p, req);
-          for (; ok && done < s_end; ) {
-            const int count = min(32, s_end - done);
-            Desc d = {};
-            const int tile = done + lane;
-            bool range = false;
-            d.pos0 = pos0 + (tile - s_start) * kTile;
+          while (ok && done < s_end) {
+            // a lane looks up a tile's pages
+            const int most = min(32, s_end - done), pos = pos0 + (done + lane - s_start) * kTile;
+            int32_t page[2] = {-1, -1};
+            int odd = 0;  // what makes a tile a chunk of its own
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              const int pos = d.pos0 + 64 * r;
-              d.page[r] = -1;
-              if (lane < count && pos < k_hi) {
-                d.page[r] = __ldg(p.block_table + table + (pos >> p.page_shift));
-                if (d.page[r] < 0 || d.page[r] >= p.num_pages) {
-                  range = true;
-                  d.page[r] = -1;
-                }
+              if (lane >= most || pos + 64 * r >= k_hi) continue;
+              page[r] = __ldg(p.block_table + table + ((pos + 64 * r) >> p.page_shift));
+              if (page[r] < 0 || page[r] >= p.num_pages) {
+                atomicOr(p.err, kErrPageRange);
+                page[r] = -1;
+                odd |= r ? kHole1 : kHole0;
               }
             }
-            if (range) atomicOr(p.err, kErrPageRange);
-            d.lo = k_lo;
-            d.hi = k_hi;
-            d.p0 = p0;
-            d.p1 = p1;
-            d.row0 = b.row0;
-            d.pair0 = b.pair0;
-            d.pairs = b.pairs;
-            d.hk = hk;
-            d.part = 2 * blockIdx.x + (from == 0);
-            d.flags = two ? kTwo | (p0 < kRows ? kSlot0 : 0) | (p1 > kRows ? kSlot1 : 0) : ((tile - from) & 1 ? kSlot1 : kSlot0);
-            d.flags |= (tile == from ? kFirst : 0) | (tile == to - 1 ? kLast : 0) | (whole ? kWhole : 0);
             // a run that ends inside: its values may hold anything behind the end
-            if (k_hi > d.pos0 && k_hi < d.pos0 + kTile && (k_hi & 63)) d.flags |= kTail;
-            for (int k = 0; ok && k < count; ++k, ++n) {
-              const uint32_t slot = n % kDescs;
-              ok = n < kDescs || warp_try(smem_u32(&ctl.dempty[slot]), (n / kDescs - 1) & 1, abort_flag, p.err);
-              if (ok && lane == k) {
-                ctl.desc[slot] = d;
-                mbar_arrive(smem_u32(&ctl.dfull[slot]));
+            if (lane < most && k_hi > pos && k_hi < pos + kTile && (k_hi & 63)) odd |= kTail;
+            const uint32_t odds = __ballot_sync(0xffffffffu, odd != 0);
+            // chunks: up to kChunkTiles tiles, odd ones alone
+            for (int first = 0; ok && first < most;) {
+              const uint32_t ahead = odds >> first;
+              int count = min(kChunkTiles, most - first);
+              if (ahead) count = min(count, (ahead & 1) ? 1 : __ffs(ahead) - 1);
+              const uint32_t slot = n % kChunks;
+              ok = n < kChunks || warp_try(smem_u32(&ctl.cempty[slot]), (n / kChunks - 1) & 1, abort_flag, p.err);
+              if (!ok) break;
+              Chunk& c = ctl.chunk[slot];
+              if (lane >= first && lane < first + count) {
+                c.page[lane - first][0] = page[0];
+                c.page[lane - first][1] = page[1];
               }
+              if (lane == first) {
+                const int tile = done + first;
+                c.flags = segment | odd | (tile == from ? kFirst : 0) | (tile + count == to ? kLast : 0) | ((tile - from) & 1 ? kOdd : 0) |
+                          (p0 < kRows ? kSlot0 : 0) | (p1 > kRows ? kSlot1 : 0);
+                c.tiles = count;
+                c.pos0 = pos;
+                c.lo = k_lo;
+                c.hi = k_hi;
+                c.p0 = p0;
+                c.p1 = p1;
+                c.row0 = b.row0;
+                c.pair0 = b.pair0;
+                c.pairs = b.pairs;
+                c.hk = hk;
+                c.part = 2 * blockIdx.x + (from == 0);
+              }
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_u32(&ctl.cfull[slot]));
+              ++n;
+              first += count;
             }
-            done += count;
+            done += most;
           }
         }
       }
@@ -496,53 +501,65 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
       }
     }
     if (ok) {
-      const uint32_t slot = n % kDescs;
-      ok = n < kDescs || warp_try(smem_u32(&ctl.dempty[slot]), (n / kDescs - 1) & 1, abort_flag, p.err);
+      const uint32_t slot = n % kChunks;
+      ok = n < kChunks || warp_try(smem_u32(&ctl.cempty[slot]), (n / kChunks - 1) & 1, abort_flag, p.err);
       if (ok && lane == 0) {
-        ctl.desc[slot].flags = kEnd;
-        mbar_arrive(smem_u32(&ctl.dfull[slot]));
+        ctl.chunk[slot].flags = kEnd;
+        mbar_arrive(smem_u32(&ctl.cfull[slot]));
       }
     }
     clear_other_rows(sp, lane);
   } else if (warp == kLoadWarp) {
     // ================================================================ loader
     uint32_t issued = 0;  // stages
-    const bool ok = for_tiles([&](const Desc& d, uint32_t) {
+    bool ok = true;
+    for (uint32_t n = 0; ok; ++n) {
+      const uint32_t slot = n % kChunks;
+      ok = warp_try(smem_u32(&ctl.cfull[slot]), (n / kChunks) & 1, abort_flag, p.err);
+      if (!ok) break;
+      const Chunk& c = ctl.chunk[slot];
+      if (c.flags & kEnd) break;
+      const int tiles = c.tiles, pos0 = c.pos0, hi = c.hi, head = c.hk * p.page_size;
+      const bool tails = c.flags & kTail;
+      const int32_t beyond = static_cast<int32_t>(p.num_pages);  // past the cache: zeros
+      for (int i = 0; ok && i < tiles; ++i) {
+        const int pos = pos0 + i * kTile;
+        const int r = lane & 1, row = head + ((pos + 64 * r) & (p.page_size - 1));  // lanes 0-3: run, piece
+        const int32_t here = c.page[i][r], page = here < 0 ? beyond : here;
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {  // keys, values
-        const uint32_t st = issued % kStages, bar = smem_u32(&ctl.kfull[st]), dst = base + st * kStage;
-        if (issued >= kStages && !warp_try(smem_u32(&ctl.kempty[st]), (issued / kStages - 1) & 1, abort_flag, p.err)) return false;
-        const int32_t beyond = static_cast<int32_t>(p.num_pages);  // past the cache: zeros
-        const auto page = [&](int r) { return d.page[r] < 0 ? beyond : d.page[r]; };
-        const auto row = [&](int r) { return d.hk * p.page_size + ((d.pos0 + 64 * r) & (p.page_size - 1)); };
-        if (v == 0) {
-          if (lane == 0) mbar_arrive_expect_tx(bar, kStage);
-          __syncwarp();
-          if (lane < 4) {
-            const int r = lane & 1, c = lane >> 1;
-            tma_load_4d(dst + c * kPiece + r * kRun, &maps.k, 0, row(r), c, page(r), bar);
-          }
-        } else {
-          // runs of the tile that end inside are copied, with zeros behind the end
-          const int tail = d.flags & kTail ? (d.hi - d.pos0) >> 6 : -1;
-          if (tail >= 0) {
-            const int keys = d.page[tail] < 0 ? 0 : d.hi - d.pos0 - 64 * tail;
-            const uint16_t* src = p.v + (d.page[tail] < 0 ? 0 : d.page[tail]) * p.page_stride + static_cast<int64_t>(row(tail)) * kPagedDim;
-            const int u = lane & 7, c = (lane >> 3) & 1, k0 = lane >> 4;  // 16-byte unit, piece, key
-#pragma unroll 4
-            for (int k = k0; k < 64; k += 2)
-              cp_async_16_or_zero(dst + tail * 2 * kRun + c * kRun + k * 128 + ((u ^ (k & 7)) << 4), src + (k < keys ? k : 0) * kPagedDim + c * 64 + u * 8, k < keys);
-            cp_async_arrive_extra(bar);
+        for (int v = 0; v < 2; ++v) {  // keys, values
+          const uint32_t st = issued % kStages, bar = smem_u32(&ctl.kfull[st]), dst = base + st * kStage;
+          ok = issued < kStages || warp_try(smem_u32(&ctl.kempty[st]), (issued / kStages - 1) & 1, abort_flag, p.err);
+          if (!ok) break;
+          if (v == 0) {
+            if (lane == 0) mbar_arrive_expect_tx(bar, kStage);
             __syncwarp();
+            if (lane < 4) tma_load_4d(dst + (lane >> 1) * kPiece + r * kRun, &maps.k, 0, row, lane >> 1, page, bar);
+          } else {
+            // a run that ends inside is copied, with zeros behind the end
+            const int tail = tails ? (hi - pos) >> 6 : -1;
+            if (tail >= 0) {
+              const int32_t its = __shfl_sync(0xffffffffu, here, tail), at = __shfl_sync(0xffffffffu, row, tail);
+              const int keys = its < 0 ? 0 : hi - pos - 64 * tail;
+              const uint16_t* src = p.v + (its < 0 ? 0 : its) * p.page_stride + static_cast<int64_t>(at) * kPagedDim;
+              const int u = lane & 7, piece = (lane >> 3) & 1;  // 16-byte unit
+#pragma unroll 4
+              for (int k = lane >> 4; k < 64; k += 2)
+                cp_async_16_or_zero(dst + tail * 2 * kRun + piece * kRun + k * 128 + ((u ^ (k & 7)) << 4),
+                                    src + (k < keys ? k : 0) * kPagedDim + piece * 64 + u * 8, k < keys);
+              cp_async_arrive_extra(bar);
+              __syncwarp();
+            }
+            if (lane == 0) mbar_arrive_expect_tx(bar, tail >= 0 ? kStage / 2 : kStage);
+            __syncwarp();
+            if (lane < 2 && lane != tail) tma_load_4d(dst + lane * 2 * kRun, &maps.v, 0, row, 0, page, bar);
           }
-          if (lane == 0) mbar_arrive_expect_tx(bar, tail >= 0 ? kStage / 2 : kStage);
-          __syncwarp();
-          if (lane < 2 && lane != tail) tma_load_4d(dst + lane * 2 * kRun, &maps.v, 0, row(lane), 0, page(lane), bar);
+          ++issued;
         }
-        ++issued;
       }
-      return true;
-    });
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl.cempty[slot]));
+    }
     cp_async_wait_all();
     if (!ok && lane == 0) {  // after a time-out: what was issued lands before the CTA can exit
       int never = 0;
@@ -550,122 +567,130 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
         mbar_wait(smem_u32(&ctl.kfull[(x - 1) % kStages]), ((x - 1) / kStages) & 1, &never, p.err);
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
-    // ================================================================ MMA issuer
-    // Steps: the accumulators of each tile.  The score product of a step is
-    // issued before the value product of the step before it, when that is the
-    // other accumulator's; P lies over S, so one accumulator's products follow
-    // one another in order.
-    const uint32_t tm = uniform(tmem);
+  } else if (warp >= kMmaWarp) {
+    // ================================================================ MMA issuers
+    // A warp issues the products of one accumulator: a tile's value product and
+    // the next tile's score product together.  The score product may overwrite P
+    // where the value product before it reads it, since one thread's products
+    // are carried out in order.  The two warps take turns, tile by tile: left
+    // to themselves they fall into step, both accumulators in the softmax at one
+    // time and both in the tensor pipe at the other (3,900 cycles a tile; in
+    // turn, one's softmax runs beside the other's products).
+    const uint32_t tm = uniform(tmem), acc = uniform(warp - kMmaWarp);
     const uint32_t s_idesc = uniform(idesc_f16(128, 128, DTYPE == FP4IDX_BF16, false, p.negate != 0));
     const uint32_t o_idesc = uniform(idesc_f16(128, 128, DTYPE == FP4IDX_BF16, false, false) | 1u << 16);
-    struct Step {
-      uint32_t tile, slot;
-      bool two, last_of_tile, first, last, tail;  // first / last of the segment
-    };
-    uint32_t n = 0;          // tiles read
-    uint32_t segs = 0;       // segments begun
-    uint32_t steps[2] = {};  // value products issued
-    uint32_t started = 0;    // accumulators with a product in this segment
-    uint32_t left = 0;       // accumulators of the current tile to come
-    int32_t flags = 0;
+    const uint32_t s_tmem = tm + acc * kTile, o_tmem = tm + kOCol + acc * kTile;
+    const uint32_t my_turn = smem_u32(&ctl.turn[acc]), its_turn = smem_u32(&ctl.turn[acc ^ 1]);
+    const uint32_t p_bar = smem_u32(&ctl.pfull[acc]), s_bar = smem_u32(&ctl.sfull[acc]);
+    uint32_t tile = 0, segs = 0, steps = 0;  // tiles and segments begun; value products issued
+    uint32_t turns = 0;
     bool ok = true;
-    const auto next = [&](Step& s) {  // false: no more steps (or a wait that failed)
-      if (left == 0) {
-        const uint32_t slot = n % kDescs;
-        if (!warp_try(smem_u32(&ctl.dfull[slot]), (n / kDescs) & 1, abort_flag, p.err)) {
-          ok = false;
-          return false;
-        }
-        flags = static_cast<int32_t>(uniform(static_cast<uint32_t>(ctl.desc[slot].flags)));
-        if (flags & kEnd) return false;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctl.dempty[slot]));
-        left = flags & (kSlot0 | kSlot1);
-        s.first = flags & kFirst;
-        ++n;
-      } else {
-        s.first = false;
-      }
-      s.tile = n - 1;
-      s.slot = left & 1 ? 0 : 1;
-      s.two = flags & kTwo;
-      left &= left - 1;
-      s.last_of_tile = left == 0;
-      s.last = s.last_of_tile && (flags & kLast);
-      s.tail = flags & kTail;
-      return true;
+    // A tile whose value product is to come: its number, its values' stage,
+    // whether copies filled it and whether its product adds to the output.
+    bool open = false;
+    uint32_t open_tile = 0, v_st = 0, v_use = 0, v_tail = 0, more = 0;
+    uint32_t begun = 0;                      // this accumulator has had a tile of the segment
+    // (the other's first turn is behind this one's first)
+    const auto take_turn = [&] {
+      if (acc == 1 || turns > 0) ok = ok && warp_try(my_turn, (turns - (acc ^ 1)) & 1, abort_flag, p.err);
+      ++turns;
     };
-    const auto score = [&](const Step& s) {
-      const uint32_t stage = 2 * s.tile, st = uniform(stage % kStages);
-      if (s.first) {
-        ok = ok && warp_try(smem_u32(&ctl.qfull[0]), segs & 1, abort_flag, p.err);
-        ok = ok && warp_try(smem_u32(&ctl.qfull[1]), segs & 1, abort_flag, p.err);
+    const auto values = [&] {
+      const uint64_t v = desc_sw128(base + v_st * kStage, kRun);
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        tc_mma_f16_tmem(o_tmem, s_tmem + x * 8, v + (x >> 2) * (2 * kRun >> 4) + (x & 3) * 128, o_idesc, x > 0 ? 1u : more);
+      tc_commit(smem_u32(&ctl.kempty[v_st]));
+    };
+    const auto weights = [&] {  // the open tile's values and weights are there
+      ok = ok && warp_try(smem_u32(&ctl.kfull[v_st]), v_use & 1, abort_flag, p.err);
+      if (v_tail) fence_proxy_async_smem();
+      ok = ok && warp_try(p_bar, steps & 1, abort_flag, p.err);
+      ++steps;
+    };
+    for (uint32_t n = 0; ok; ++n) {
+      const uint32_t slot = n % kChunks;
+      ok = warp_try(smem_u32(&ctl.cfull[slot]), (n / kChunks) & 1, abort_flag, p.err);
+      if (!ok) break;
+      const uint32_t flags = uniform(ctl.chunk[slot].flags), tiles = uniform(ctl.chunk[slot].tiles);
+      __syncwarp();
+      if (flags & kEnd) break;
+      if (lane == 0) mbar_arrive(smem_u32(&ctl.cempty[slot]));
+      const bool two = flags & kTwo;
+      if (flags & kFirst) {
+        ok = warp_try(smem_u32(&ctl.qfull[0]), segs & 1, abort_flag, p.err);
+        if (acc == 1) ok = ok && warp_try(smem_u32(&ctl.qfull[1]), segs & 1, abort_flag, p.err);
         ++segs;
+        begun = 0;
       }
-      ok = ok && warp_try(smem_u32(&ctl.kfull[st]), (stage / kStages) & 1, abort_flag, p.err);
-      if (!ok) return;
-      tc_fence_after();
-      const uint32_t slot = uniform(s.slot);
-      if (elect_one()) {
-        const uint64_t a = desc_sw128(base + kOff_Q + (s.two ? slot * kQBytes : 0), 16), b = desc_sw128(base + st * kStage, 16);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int at = (k >> 2) * (kPiece >> 4) + (k & 3) * 2;
-          tc_mma_f16(tm + slot * kTile, a + at, b + at, s_idesc, k > 0);
+      const uint64_t q = desc_sw128(base + kOff_Q + (two ? acc * kQBytes : 0), 16);
+#pragma unroll 1
+      for (uint32_t i = 0; ok && i < tiles; ++i, ++tile) {
+        const bool mine = two ? flags & (acc ? kSlot1 : kSlot0) : (((flags & kOdd ? 1 : 0) + i) & 1) == acc;
+        const uint32_t k_st = uniform(2 * tile % kStages), k_use = 2 * tile / kStages;
+        const uint32_t next_v = uniform((2 * tile + 1) % kStages), next_use = (2 * tile + 1) / kStages;
+        ok = warp_try(smem_u32(&ctl.kfull[k_st]), k_use & 1, abort_flag, p.err);
+        if (!mine) {  // (its arrival is for this use of the stages, so it waits for them)
+          ok = ok && warp_try(smem_u32(&ctl.kfull[next_v]), next_use & 1, abort_flag, p.err);
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&ctl.kempty[k_st]));
+            mbar_arrive(smem_u32(&ctl.kempty[next_v]));
+          }
+          // a value product waits for its accumulator's next score product, but
+          // not so long that the loader runs out of stages
+          const bool close = open && tile - open_tile >= 2;
+          if (close) weights();
+          take_turn();
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            if (close) values();
+            mbar_arrive(its_turn);
+          }
+          __syncwarp();
+          if (close) open = false;
+          continue;
         }
-        tc_commit(smem_u32(&ctl.sfull[slot]));
-        if (s.last_of_tile) tc_commit(smem_u32(&ctl.kempty[st]));
-        if (s.last) tc_commit(smem_u32(&ctl.qfree));
-      }
-      __syncwarp();
-    };
-    const auto value = [&](const Step& s) {
-      const uint32_t stage = 2 * s.tile + 1, st = uniform(stage % kStages);
-      const uint32_t slot = uniform(s.slot);
-      if (s.first) started = 0;
-      const bool more = started >> slot & 1;
-      ok = ok && warp_try(smem_u32(&ctl.kfull[st]), (stage / kStages) & 1, abort_flag, p.err);
-      ok = ok && warp_try(smem_u32(&ctl.pfull[slot]), steps[slot] & 1, abort_flag, p.err);
-      // The output of the segment before has been read (segs counts this one).
-      // Its own warps have done so when P is there, so that this wait is never
-      // for a phase further back than the last one; the other ones may not have.
-      if (!more && segs > 1) ok = ok && warp_try(smem_u32(&ctl.ofree[slot]), segs & 1, abort_flag, p.err);
-      if (!ok) return;
-      if (s.tail) fence_proxy_async_smem();
-      tc_fence_after();
-      ++steps[slot];
-      started |= 1u << slot;
-      if (elect_one()) {
-        const uint64_t b = desc_sw128(base + st * kStage, kRun);
+        const bool was_open = open;
+        if (was_open) weights();
+        take_turn();
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          if (was_open) values();
+          const uint64_t k = desc_sw128(base + k_st * kStage, 16);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          tc_mma_f16_tmem(tm + kOCol + slot * kTile, tm + slot * kTile + k * 8, b + (k >> 2) * (2 * kRun >> 4) + (k & 3) * 128, o_idesc,
-                          k > 0 || more);
-        if (s.last_of_tile) tc_commit(smem_u32(&ctl.kempty[st]));
-        if (s.last) {
-          tc_commit(smem_u32(&ctl.odone[0]));
-          tc_commit(smem_u32(&ctl.odone[1]));
+          for (int x = 0; x < 8; ++x) {
+            const int at = (x >> 2) * (kPiece >> 4) + (x & 3) * 2;
+            tc_mma_f16(s_tmem, q + at, k + at, s_idesc, x > 0);
+          }
+          mbar_arrive(its_turn);
+          tc_commit(s_bar);
+          tc_commit(smem_u32(&ctl.kempty[k_st]));
         }
+        __syncwarp();
+        more = begun;
+        begun = 1;
+        open = true;
+        open_tile = tile;
+        v_st = next_v;
+        v_use = next_use;
+        v_tail = flags & kTail;
       }
-      __syncwarp();
-    };
-    Step now, then;
-    bool have = next(now);
-    if (have) score(now);
-    while (ok && have) {
-      const bool more = !now.last && next(then);
-      const bool early = more && then.slot != now.slot;
-      if (early) score(then);
-      if (ok) value(now);
-      if (now.last) {
-        have = ok && next(now);
-        if (have) score(now);
-        continue;
+      if (ok && (flags & kLast)) {
+        const bool was_open = open;
+        if (was_open) weights();
+        take_turn();
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          if (was_open) values();
+          mbar_arrive(its_turn);
+          tc_commit(smem_u32(&ctl.odone[acc]));
+        }
+        __syncwarp();
+        open = false;
       }
-      if (ok && more && !early) score(then);
-      now = then;
-      have = more;
     }
     // no product is in flight when TMEM is freed
     if (elect_one()) tc_commit(smem_u32(&ctl.drain));
@@ -675,112 +700,156 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
       mbar_wait(smem_u32(&ctl.drain), 0, &never, p.err);
     }
     __syncwarp();
-  } else if (warp < 2 * kSoftmaxWarps) {
+  } else {
     // ================================================================ softmax
-    const int slot = warp / kSoftmaxWarps, r = tid & (kRows - 1);  // accumulator, row of it
+    const int acc = warp / kSoftmaxWarps, r = tid & (kRows - 1);  // accumulator, row of it
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
-    const uint32_t s_at = tmem + lanes + slot * kTile, o_at = tmem + lanes + kOCol + slot * kTile;
+    const uint32_t s_at = tmem + lanes + acc * kTile, o_at = tmem + lanes + kOCol + acc * kTile;
     uint32_t segs = 0, steps = 0;   // segments begun; tiles of this accumulator
     uint32_t merged = 0;            // segments whose two accumulators were added up
+    bool merging = false;           // the last one was
     int steps_of_seg = 0;
-    int vis = 0, pair = 0;          // of this thread's row
+    int vis = 0;                    // of this thread's row
     bool valid = false, ok = true;
-    float m = -INFINITY;            // reference maximum, in powers of two
-    float2 l[2] = {};
-    for_tiles([&](const Desc& d, uint32_t) {
-      const int off = d.flags & kTwo ? slot * kRows : 0;  // first pair of this accumulator
-      if (d.flags & kFirst) {
-        pair = d.pair0 + off + r;
+    float m = -INFINITY;            // reference, in powers of two
+    float l = 0.0f;
+    for (uint32_t n = 0; ok; ++n) {
+      const uint32_t slot = n % kChunks;
+      ok = warp_try(smem_u32(&ctl.cfull[slot]), (n / kChunks) & 1, abort_flag, p.err);
+      if (!ok) break;
+      const Chunk& d = ctl.chunk[slot];
+      const int flags = d.flags;
+      if (flags & kEnd) break;
+      const bool two = flags & kTwo;
+      const int off = two ? acc * kRows : 0;  // first pair of this accumulator
+      if (flags & kFirst) {
+        // (the products that read the queries before are done: this warp has
+        // waited for its own, and through mfull for the other issuer's)
+        const int pair = d.pair0 + off + r, t = d.row0 + group_div(p, pair);
         valid = off + r < d.pairs;
-        const int t = d.row0 + group_div(p, pair);
-        if (segs > 0) ok = warp_try(smem_u32(&ctl.qfree), (segs - 1) & 1, abort_flag, p.err);
-        if (!ok) return false;
         if (valid) {
           vis = pl.row_vis[t];
-          if (slot == 0 || (d.flags & kTwo)) {
+          if (acc == 0 || two) {
             const int h = d.hk * p.group + pair - group_div(p, pair) * p.group;
             const uint4* src = reinterpret_cast<const uint4*>(p.q + t * p.q_row_stride + h * p.q_head_stride);
             uint4 q[16];
 #pragma unroll
             for (int u = 0; u < 16; ++u) q[u] = __ldg(src + u);
-            uint8_t* dst = smem + kOff_Q + slot * kQBytes + r * 128;
+            uint8_t* dst = smem + kOff_Q + acc * kQBytes + r * 128;
 #pragma unroll
             for (int u = 0; u < 16; ++u) *reinterpret_cast<uint4*>(dst + (u >> 3) * kPiece + (((u & 7) ^ (r & 7)) << 4)) = q[u];
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctl.qfull[slot]));
+        if (lane == 0) mbar_arrive(smem_u32(&ctl.qfull[acc]));
+        // the other accumulator's warps have read this one's output and sums
+        if (acc == 1 && merging) ok = warp_try(smem_u32(&ctl.mfree), (merged - 1) & 1, abort_flag, p.err);
+        if (!ok) break;
         ++segs;
         steps_of_seg = 0;
         m = -INFINITY;
-        l[0] = l[1] = make_float2(0.0f, 0.0f);
+        l = 0.0f;
       }
-      if (d.flags >> slot & 1) {
-        ok = warp_try(smem_u32(&ctl.sfull[slot]), steps & 1, abort_flag, p.err);
-        if (!ok) return false;
-        tc_fence_after();
-        // columns [c_lo, c_lo + c_len) of this row count
-        const bool mine = valid && off + r >= d.p0 && off + r < d.p1;
-        int c_lo = max(0, d.lo - d.pos0), c_hi = mine ? min(min(vis, d.hi) - d.pos0, kTile) : 0;
-        if (d.page[0] < 0) c_lo = max(c_lo, 64);
-        if (d.page[1] < 0) c_hi = min(c_hi, 64);
-        const int c_len = max(0, c_hi - c_lo);
-        if (__any_sync(0xffffffffu, c_len > 0)) {
-          uint32_t x[kTile];
-          tmem_ld(s_at, x);
-          tmem_wait_ld();
-          reg_fence(x);
-          if (__any_sync(0xffffffffu, c_len < kTile)) {
-#pragma unroll
-            for (int c = 0; c < kTile; ++c)
-              if (static_cast<uint32_t>(c - c_lo) >= static_cast<uint32_t>(c_len)) x[c] = 0xff800000u;  // -inf
-          }
-          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int c = 0; c < kTile; c += 8) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              top[k] = fmaxf(fmaxf(top[k], __uint_as_float(x[c + 2 * k])), __uint_as_float(x[c + 2 * k + 1]));
-          }
-          const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2 - kBelow<DTYPE>;
-          const bool raise = most > m + kRaise;
-          if (__any_sync(0xffffffffu, raise)) {
-            const float f = raise ? ex2(m - most) : 1.0f;
-            if (raise) m = most;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              l[k].x *= f;
-              l[k].y *= f;
-            }
-            if (steps_of_seg > 0) {  // (the score product followed the last value product, so that is complete)
+      const int tiles = d.tiles;
+      const bool mine = valid && off + r >= d.p0 && off + r < d.p1;
+      // keys [lo, hi) count for this row, relative to the chunk's first
+      int lo = d.lo - d.pos0, hi = mine ? min(vis, d.hi) - d.pos0 : 0;
+      if (flags & kHole0) lo = max(lo, kTile / 2);
+      if (flags & kHole1) hi = min(hi, kTile / 2);
+      const int turn = flags & kOdd ? 1 : 0;
+      const bool active = !two || (flags & (acc ? kSlot1 : kSlot0));
 #pragma unroll 1
-              for (int c = 0; c < kPagedDim; c += 16) {
-                uint32_t o[16];
-                tmem_ld(o_at + c, o);
-                tmem_wait_ld();
-                reg_fence(o);
+      for (int i = two ? 0 : turn ^ acc; active && i < tiles; i += two ? 1 : 2) {
+        // columns [c_lo, c_lo + c_len) count
+        const int c_lo = max(0, lo - i * kTile), c_len = max(0, min(hi - i * kTile, kTile) - c_lo);
+        const bool some = __any_sync(0xffffffffu, c_len > 0), full = __all_sync(0xffffffffu, c_len == kTile);
+        ok = warp_try(smem_u32(&ctl.sfull[acc]), steps & 1, abort_flag, p.err);
+        if (!ok) break;
+        tc_fence_after();
+        if (some) {
+          const auto masked = [&](auto& x, int c) {
+            if (full) return;
+            // a bit for each of the columns from c on; the empty asm keeps the
+            // tests of all columns from being worked out (and spilled) at once
+            const int from = min(max(c_lo - c, 0), 32), to = min(max(c_lo + c_len - c, 0), 32);
+            uint32_t bits = static_cast<uint32_t>((uint64_t{1} << to) - 1) & ~static_cast<uint32_t>((uint64_t{1} << from) - 1);
+            asm volatile("" : "+r"(bits));
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st_x16(o_at + c, o);
+            for (int k = 0; k < static_cast<int>(sizeof(x) / 4); ++k)
+              if (!(bits >> k & 1)) x[k] = 0xff800000u;  // -inf
+          };
+          uint32_t w[kTile / 2];
+          bool raise = c_len > 0 && m == -INFINITY;
+          bool again = __any_sync(0xffffffffu, raise);
+          float sum = 0.0f;
+#pragma unroll 1
+          for (bool once = false;; once = true) {
+            if (again) {  // a new reference
+              float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+              for (int c = 0; c < kTile; c += 32) {
+                uint32_t x[32];
+                tmem_ld(s_at + c, x);
+                tmem_wait_ld();
+                reg_fence(x);
+                masked(x, c);
+#pragma unroll
+                for (int k = 0; k < 32; k += 2)
+                  top[k / 2 & 3] = fmaxf(fmaxf(top[k / 2 & 3], __uint_as_float(x[k])), __uint_as_float(x[k + 1]));
+              }
+              const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2 - kBelow<DTYPE>;
+              const float f = raise && most > m ? ex2(m - most) : 1.0f;
+              if (raise && most > m) m = most;
+              l *= f;
+              if (steps_of_seg > 0) {  // (the score product came behind the last value product)
+#pragma unroll 1
+                for (int c = 0; c < kPagedDim; c += 16) {
+                  uint32_t o[16];
+                  tmem_ld(o_at + c, o);
+                  tmem_wait_ld();
+                  reg_fence(o);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                  tmem_st_x16(o_at + c, o);
+                }
+                tmem_wait_st();
               }
             }
-          }
-          // weights, their sum in fp32, and P in 16 bits (the MMA's operand type:
-          // each weight is rounded once, the sum is of unrounded ones)
-          const float2 scale = make_float2(p.scale_log2, p.scale_log2);
-          const float2 ref = m == -INFINITY ? make_float2(0.0f, 0.0f) : make_float2(-m, -m);
+            // weights, their sum in fp32, and P in 16 bits (the MMA's operand type:
+            // each weight is rounded once, the sum is of unrounded ones)
+            const float2 scale = make_float2(p.scale_log2, p.scale_log2);
+            const float2 ref = m == -INFINITY ? make_float2(0.0f, 0.0f) : make_float2(-m, -m);
+            float2 part[2] = {};
+            uint32_t x[2][16];
+            tmem_ld(s_at, x[0]);
 #pragma unroll
-          for (int c = 0; c < kTile; c += 32) {
-            uint32_t w[16];
+            for (int c = 0; c < kTile; c += 16) {
+              uint32_t(&y)[16] = x[c / 16 & 1];
+              tmem_wait_ld();
+              reg_fence(y);
+              if (c + 16 < kTile) tmem_ld(s_at + c + 16, x[(c / 16 & 1) ^ 1]);
+              masked(y, c);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              float2 a = fma2(make_float2(__uint_as_float(x[c + 2 * k]), __uint_as_float(x[c + 2 * k + 1])), scale, ref);
-              a = make_float2(ex2(a.x), ex2(a.y));
-              l[k & 1] = add2(l[k & 1], a);
-              w[k] = pack2<DTYPE>(a.x, a.y);
+              for (int k = 0; k < 8; ++k) {
+                float2 a = fma2(make_float2(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1])), scale, ref);
+                a = make_float2(ex2(a.x), ex2(a.y));
+                part[k & 1] = add2(part[k & 1], a);
+                w[c / 2 + k] = pack2<DTYPE>(a.x, a.y);
+              }
             }
-            tmem_st_x16(s_at + c / 2, w);
+            sum = (part[0].x + part[1].x) + (part[0].y + part[1].y);
+            raise = sum > kLimit<DTYPE>;
+            again = !once && __any_sync(0xffffffffu, raise);
+            if (!again) break;
+          }
+          l += sum;
+#pragma unroll
+          for (int c = 0; c < kTile / 2; c += 16) {
+            uint32_t v[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] = w[c + k];
+            tmem_st_x16(s_at + c, v);
           }
         } else {  // none of the warp's rows sees a key of this tile
           uint32_t w[16] = {};
@@ -790,92 +859,86 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctl.pfull[slot]));
+        if (lane == 0) mbar_arrive(smem_u32(&ctl.pfull[acc]));
         ++steps;
         ++steps_of_seg;
       }
-      if (d.flags & kLast) {
+      if (!ok) break;
+      if (flags & kLast) {
         // ---- output of the segment
-        float sum = (l[0].x + l[1].x) + (l[0].y + l[1].y);
-        const bool two = d.flags & kTwo;
-        const uint32_t parity = (segs - 1) & 1;
-        ok = warp_try(smem_u32(&ctl.odone[slot]), parity, abort_flag, p.err);
-        if (!ok) return false;
+        ok = warp_try(smem_u32(&ctl.odone[acc]), (segs - 1) & 1, abort_flag, p.err);
+        if (!ok) break;
         tc_fence_after();
-        if (!two && slot == 1) {
-          // the other accumulator's warps read this one's output, once they have
-          // read that of the segment before
-          ok = segs < 2 || warp_try(smem_u32(&ctl.ofree[1]), parity ^ 1, abort_flag, p.err);
-          if (!ok) return false;
-          ctl.other[r] = make_float2(m, sum);
+        merging = !two;
+        if (merging && acc == 1) {  // the other accumulator's warps add this one up
+          ctl.other[r] = make_float2(m, l);
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&ctl.mfull));
-          return true;
-        }
-        // out = f0 O (+ f1 O of the other accumulator)
-        float f0 = steps_of_seg > 0 ? 1.0f : 0.0f, f1 = 0.0f;
-        if (!two) {
-          // (the commit that this warp has waited for covers both accumulators)
-          ok = warp_try(smem_u32(&ctl.mfull), merged++ & 1, abort_flag, p.err);
-          if (!ok) return false;
-          const float2 b = ctl.other[r];
-          const float most = fmaxf(m, b.x), at = most == -INFINITY ? 0.0f : most;
-          f0 = ex2(m - at);  // (accumulator 0 takes a segment's first tile)
-          f1 = ex2(b.x - at);
-          sum = f0 * sum + f1 * b.y;
-          m = most;
-        }
-        const bool both = !two && __any_sync(0xffffffffu, f1 != 0.0f);
-        const int t = d.row0 + group_div(p, pair), h = d.hk * p.group + pair - group_div(p, pair) * p.group;
-        const bool whole = d.flags & kWhole;
-        if (whole) {
-          const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-          f0 = sum == 0.0f ? 0.0f : f0 * inv;
-          f1 *= inv;
-        }
-        const int row = off + r;  // of the block
-        uint4* out = reinterpret_cast<uint4*>(p.out + t * p.out_row_stride + static_cast<int64_t>(h) * kPagedDim);
-        float4* part = pl.partial + static_cast<int64_t>(d.part) * (kPagedDim / 4) * kBlockPairs + row;
+        } else {
+          // out = f0 O (+ f1 O of the other accumulator)
+          float f0 = steps_of_seg > 0 ? 1.0f : 0.0f, f1 = 0.0f, sum = l;
+          if (merging) {
+            ok = warp_try(smem_u32(&ctl.mfull), merged & 1, abort_flag, p.err);
+            if (!ok) break;
+            tc_fence_after();
+            const float2 b = ctl.other[r];
+            const float top = fmaxf(m, b.x), at = top == -INFINITY ? 0.0f : top;
+            f0 = ex2(m - at);  // (accumulator 0 takes a segment's first tile)
+            f1 = ex2(b.x - at);
+            sum = f0 * l + f1 * b.y;
+            m = top;
+          }
+          const bool both = merging && __any_sync(0xffffffffu, f1 != 0.0f);
+          const int pair = d.pair0 + off + r, t = d.row0 + group_div(p, pair), h = d.hk * p.group + pair - group_div(p, pair) * p.group;
+          const bool whole = flags & kWhole;
+          if (whole) {
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            f0 = sum == 0.0f ? 0.0f : f0 * inv;
+            f1 *= inv;
+          }
+          const int row = off + r;  // of the block
+          uint4* out = reinterpret_cast<uint4*>(p.out + t * p.out_row_stride + static_cast<int64_t>(h) * kPagedDim);
+          float4* part = pl.partial + static_cast<int64_t>(d.part) * (kPagedDim / 4) * kBlockPairs + row;
 #pragma unroll 1
-        for (int c = 0; c < kPagedDim; c += 32) {
-          uint32_t o[32];
-          __syncwarp();
-          tmem_ld(o_at + c, o);
-          tmem_wait_ld();
-          reg_fence(o);
-          float y[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) y[e] = f0 == 0.0f ? 0.0f : __uint_as_float(o[e]) * f0;
-          if (both) {
-            tmem_ld(o_at + kTile + c, o);
+          for (int c = 0; c < kPagedDim; c += 32) {
+            uint32_t o[32];
+            __syncwarp();
+            tmem_ld(o_at + c, o);
             tmem_wait_ld();
             reg_fence(o);
+            float y[32];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) y[e] = f1 == 0.0f ? y[e] : fmaf(__uint_as_float(o[e]), f1, y[e]);
+            for (int e = 0; e < 32; ++e) y[e] = f0 == 0.0f ? 0.0f : __uint_as_float(o[e]) * f0;
+            if (both) {
+              tmem_ld(o_at + kTile + c, o);
+              tmem_wait_ld();
+              reg_fence(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) y[e] = f1 == 0.0f ? y[e] : fmaf(__uint_as_float(o[e]), f1, y[e]);
+            }
+            if (valid && whole) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 8)
+                out[(c + e) / 8] = make_uint4(pack2<DTYPE>(y[e], y[e + 1]), pack2<DTYPE>(y[e + 2], y[e + 3]),
+                                              pack2<DTYPE>(y[e + 4], y[e + 5]), pack2<DTYPE>(y[e + 6], y[e + 7]));
+            } else if (valid) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) part[(c + e) / 4 * kBlockPairs] = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+            }
           }
-          if (valid && whole) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              out[(c + e) / 8] = make_uint4(pack2<DTYPE>(y[e], y[e + 1]), pack2<DTYPE>(y[e + 2], y[e + 3]), pack2<DTYPE>(y[e + 4], y[e + 5]),
-                                            pack2<DTYPE>(y[e + 6], y[e + 7]));
-          } else if (valid) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) part[(c + e) / 4 * kBlockPairs] = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+          if (valid) {
+            if (!whole) pl.stats[static_cast<int64_t>(d.part) * kBlockPairs + row] = make_float2(m, sum);
+            else if (p.lse) p.lse[static_cast<int64_t>(t) * p.num_heads + h] = row_lse(m, sum);
           }
+          tc_fence_before();
+          __syncwarp();
+          if (merging && lane == 0) mbar_arrive(smem_u32(&ctl.mfree));
         }
-        if (valid) {
-          if (!whole) pl.stats[static_cast<int64_t>(d.part) * kBlockPairs + row] = make_float2(m, sum);
-          else if (p.lse) p.lse[static_cast<int64_t>(t) * p.num_heads + h] = row_lse(m, sum);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(smem_u32(&ctl.ofree[slot]));
-          if (!two) mbar_arrive(smem_u32(&ctl.ofree[1]));
-        }
+        merged += merging;
       }
-      return true;
-    });
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl.cempty[slot]));
+    }
     tc_fence_before();
   }
   __syncthreads();
@@ -887,41 +950,44 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
 
 // ---------------------------------------------------------------- join
 // out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over the partial sums of
-// a block that crosses run boundaries, in the order of its tiles.  blockIdx.x
-// counts run boundaries; the first one inside a block does its work.  A CTA
-// takes 32 rows and 32 columns, a lane a row; its warps take parts in turn and
+// a block that crosses run boundaries, in the order of its tiles.  A warp takes
+// 32 rows (a lane a row) and 32 columns.  With few parts (BY_ITEM false:
+// blockIdx.x counts run boundaries, the first one inside a block does its work)
+// it adds all of them, and a CTA's warps take 64 rows; with many (BY_ITEM:
+// blockIdx.x is the block of a K/V head) the CTA's warps take parts in turn and
 // are added in order.
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinCols = 32;
 
-template <int DTYPE>
+template <int DTYPE, bool BY_ITEM>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Plan pl) {
-  __shared__ float4 sums[kJoinWarps][kJoinCols / 4][32];
+  __shared__ float4 sums[BY_ITEM ? kJoinWarps : 1][kJoinCols / 4][32];
   __shared__ float2 part[kJoinWarps][32];
+  __shared__ RunInfo its;
+  __shared__ int first_cta;
   pdl_wait();
   pdl_launch_dependents();
   const AttnParams& p = pl.sp.a;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x + 1;  // the boundary before CTA c's run
-  const int total = pl.info[0].total, used = used_ctas(total, pl.ctas);
-  const auto inside = [&](int x, int item) {
-    return x > 0 && x < used && pl.info[x].item == item && pl.info[x].start < run_begin(total, x, used);
-  };
-  if (c >= used) return;
-  const RunInfo info = pl.info[c];
-  if (!inside(c, info.item) || inside(c - 1, info.item)) return;
-  const int row = blockIdx.y * 32 + lane, cols = blockIdx.z * kJoinCols;
-  if (static_cast<int>(blockIdx.y) * 32 >= info.pairs) return;
-  int parts = 2;
-  for (;;) {  // 32 boundaries at a time
-    const uint32_t in = __ballot_sync(0xffffffffu, inside(c + parts - 1 + lane, info.item));
-    const int n = in == 0xffffffffu ? 32 : __ffs(~in) - 1;
-    parts += n;
-    if (n < 32) break;
-  }
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // a CTA of the first kernel per thread (plan_shared)
+  RunInfo info = {};
+  if (tid < pl.ctas) info = pl.info[tid];
+  const int item = BY_ITEM ? blockIdx.x : pl.info[blockIdx.x + 1].item, total = pl.info[0].total;
+  if (tid == 0) first_cta = INT32_MAX;
+  __syncthreads();
+  // the CTAs whose run begins inside the block: consecutive ones
+  const int used = used_ctas(total, pl.ctas);
+  const bool inside = tid > 0 && tid < used && info.item == item && info.start < run_begin(total, tid, used);
+  if (inside) atomicMin(&first_cta, tid);
+  const int parts = 1 + __syncthreads_count(inside);
+  const int c = first_cta;  // the first boundary; the part before it is the previous CTA's
+  if (parts == 1 || (!BY_ITEM && c != static_cast<int>(blockIdx.x) + 1)) return;
+  if (tid == c) its = info;
+  __syncthreads();
+  const int row = (BY_ITEM ? blockIdx.y : blockIdx.y * 2 + (warp >> 2)) * 32 + lane, cols = (BY_ITEM ? blockIdx.z : warp & 3) * kJoinCols;
+  if (row - lane >= its.pairs) return;  // (BY_ITEM: the whole CTA)
   float4 acc[kJoinCols / 4] = {};
   float m = -INFINITY, l = 0.0f;
-#pragma unroll 2
-  for (int i = warp; i < parts; i += kJoinWarps) {
+  for (int i = BY_ITEM ? warp : 0; i < parts; i += BY_ITEM ? kJoinWarps : 1) {
     // part i is CTA c - 1 + i's; of the first one its last segment, of the others their first
     const int64_t at = 2 * (c - 1 + i) + (i == 0);
     const float2 s = pl.stats[at * kBlockPairs + row];
@@ -940,35 +1006,39 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
       acc[v].w = acc[v].w * keep + w * o[v].w;
     }
   }
+  if constexpr (BY_ITEM) {
 #pragma unroll
-  for (int v = 0; v < kJoinCols / 4; ++v) sums[warp][v][lane] = acc[v];
-  part[warp][lane] = make_float2(m, l);
-  __syncthreads();
-  // warp v adds the warps' shares of four columns
-  static_assert(kJoinWarps == kJoinCols / 4, "four columns a warp");
-  m = part[0][lane].x;
+    for (int v = 0; v < kJoinCols / 4; ++v) sums[warp][v][lane] = acc[v];
+    part[warp][lane] = make_float2(m, l);
+    __syncthreads();
+    // warp v adds the warps' shares of four columns
+    static_assert(kJoinWarps == kJoinCols / 4, "four columns a warp");
+    m = part[0][lane].x;
 #pragma unroll
-  for (int w = 1; w < kJoinWarps; ++w) m = fmaxf(m, part[w][lane].x);
-  const float ref = m == -INFINITY ? 0.0f : m;
-  l = 0.0f;
-  float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int w = 1; w < kJoinWarps; ++w) m = fmaxf(m, part[w][lane].x);
+    const float ref = m == -INFINITY ? 0.0f : m;
+    l = 0.0f;
+    acc[0] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) {
-    const float4 o = sums[w][warp][lane];
-    const float f = ex2(part[w][lane].x - ref);
-    l = fmaf(f, part[w][lane].y, l);
-    y.x = fmaf(f, o.x, y.x);
-    y.y = fmaf(f, o.y, y.y);
-    y.z = fmaf(f, o.z, y.z);
-    y.w = fmaf(f, o.w, y.w);
+    for (int w = 0; w < kJoinWarps; ++w) {
+      const float4 o = sums[w][warp][lane];
+      const float f = ex2(part[w][lane].x - ref);
+      l = fmaf(f, part[w][lane].y, l);
+      acc[0].x = fmaf(f, o.x, acc[0].x);
+      acc[0].y = fmaf(f, o.y, acc[0].y);
+      acc[0].z = fmaf(f, o.z, acc[0].z);
+      acc[0].w = fmaf(f, o.w, acc[0].w);
+    }
   }
-  if (row >= info.pairs) return;
-  const int pair = info.pair0 + row, t = info.row0 + group_div(p, pair);
-  const int h = info.hk * p.group + pair - group_div(p, pair) * p.group;
+  if (row >= its.pairs) return;
+  const int pair = its.pair0 + row, t = its.row0 + group_div(p, pair);
+  const int h = its.hk * p.group + pair - group_div(p, pair) * p.group;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   uint2* out = reinterpret_cast<uint2*>(p.out + t * p.out_row_stride + static_cast<int64_t>(h) * kPagedDim + cols);
-  out[warp] = make_uint2(pack2<DTYPE>(y.x * inv, y.y * inv), pack2<DTYPE>(y.z * inv, y.w * inv));
-  if (p.lse && warp == 0 && blockIdx.z == 0) p.lse[static_cast<int64_t>(t) * p.num_heads + h] = row_lse(m, l);
+#pragma unroll
+  for (int v = 0; v < (BY_ITEM ? 1 : kJoinCols / 4); ++v)
+    out[BY_ITEM ? warp : v] = make_uint2(pack2<DTYPE>(acc[v].x * inv, acc[v].y * inv), pack2<DTYPE>(acc[v].z * inv, acc[v].w * inv));
+  if (p.lse && cols == 0 && (!BY_ITEM || warp == 0)) p.lse[static_cast<int64_t>(t) * p.num_heads + h] = row_lse(m, l);
 }
 
 // ---------------------------------------------------------------- host
@@ -1031,13 +1101,18 @@ cudaError_t launch(const Plan& pl, const AttnMaps& maps, cudaStream_t stream) {
   cfg.dynamicSmemBytes = kSmem;
   if ((e = cudaLaunchKernelEx(&cfg, shared_kernel<DTYPE>, pl, maps)) != cudaSuccess) return e;
   if (pl.ctas < 2) return cudaSuccess;
-  // rows that a block can have
+  // rows that a block can have, and more than four parts of each on average?
   const int64_t pairs = static_cast<int64_t>(pl.sp.max_group_rows) * pl.sp.a.group;
   const unsigned rows = static_cast<unsigned>(std::min<int64_t>(pairs, kBlockPairs));
-  cfg.gridDim = dim3(static_cast<unsigned>(pl.ctas - 1), (rows + 31) / 32, kPagedDim / kJoinCols);
+  const int64_t items = static_cast<int64_t>(pl.blocks) * pl.sp.a.num_kv_heads;
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, join_kernel<DTYPE>, pl);
+  if (pl.ctas > 4 * items) {
+    cfg.gridDim = dim3(static_cast<unsigned>(items), (rows + 31) / 32, kPagedDim / kJoinCols);
+    return cudaLaunchKernelEx(&cfg, join_kernel<DTYPE, true>, pl);
+  }
+  cfg.gridDim = dim3(static_cast<unsigned>(pl.ctas - 1), (rows + 63) / 64);
+  return cudaLaunchKernelEx(&cfg, join_kernel<DTYPE, false>, pl);
 }
 
 }  // namespace
@@ -1054,7 +1129,8 @@ bool plan_shared(SharedParams* p, int sms) {
   const int64_t spans = 2 * blocks + a.num_seqs;
   if (tiles * spans > INT32_MAX / a.num_kv_heads) return false;
   p->blocks_per_group = static_cast<int32_t>(per);
-  p->ctas = static_cast<int32_t>(std::min<int64_t>(sms, tiles * spans * a.num_kv_heads));
+  // (the join looks at one CTA per thread)
+  p->ctas = static_cast<int32_t>(std::min<int64_t>(std::min(sms, kJoinThreads), tiles * spans * a.num_kv_heads));
   return true;
 }
 
