@@ -15,23 +15,24 @@
 // its values:
 //
 //   S [128 rows x 128 keys] = Q K^T      tcgen05, Q and K in shared memory
-//   P = 2^(S - m)                        registers; 16 bits, over S's columns in TMEM
+//   P = 2^(S - m)                        registers; 16 bits, over S's columns in TMEM (each 64 keys' over their own)
 //   O [128 rows x 128]     += P V        tcgen05, P in TMEM, V in shared memory
 //
 // While one accumulator's rows go through the softmax, the tensor pipe works
 // on the other's: with more than 128 pairs the two hold the block's halves and
 // share each tile; with fewer they hold the same rows and take tiles in turn,
-// and the end adds them up.  A softmax thread owns a row, so it needs no other
-// thread's maximum, sum or factor.  It takes the weights of a tile relative to
-// the reference of the tiles before and looks at their sum: only where that is
-// too large (or there is no reference yet) does it go over the scores for a
-// maximum, so that a tile's scores are read once.
+// and the end adds them up.  Two threads share a row, 64 keys of a tile each.
+// They take a tile's weights relative to the reference of the tiles before and
+// look at their sum: only where that is too large (or there is no reference
+// yet) do they go over the scores for a maximum, so that a tile's scores are
+// read once and all that the two have to agree on is that neither wants to.
 //
-// Roles: warps 0-3 and 4-7 softmax of the two accumulators, queries and output;
-// warps 8 and 9 issue the products of one accumulator each; warp 10 loader
-// (TMA; 16-byte copies, which can leave zeros where a value may be anything,
-// for the values of a run that ends inside); warp 11 planner, which looks up
-// the tiles' pages ahead of all of them and hands them out in chunks.
+// Roles: warps 0-7 and 8-15 softmax of the two accumulators, queries and output
+// (four of a lane quarter, by halves of the keys); warps 16 and 17 issue the
+// products of one accumulator each; warp 18 loader (TMA; 16-byte copies, which
+// can leave zeros where a value may be anything, for the values of a run that
+// ends inside); warp 19 planner, which looks up the tiles' pages ahead of all
+// of them and hands them out in chunks.
 #include <algorithm>
 #include <atomic>
 #include <cstddef>
@@ -46,13 +47,14 @@ namespace {
 constexpr int kTile = 128;                 // keys of a tile: two runs of 64, each inside one page
 constexpr int kRows = 128;                 // rows of an accumulator
 constexpr int kBlockPairs = 2 * kRows;
-constexpr int kSoftmaxWarps = 4;           // of one accumulator
+constexpr int kHalf = kTile / 2;           // keys of a tile, or columns of an output, that a softmax thread has
+constexpr int kSoftmaxWarps = 8;           // of one accumulator
 constexpr int kMmaWarp = 2 * kSoftmaxWarps, kLoadWarp = kMmaWarp + 2, kPlanWarp = kMmaWarp + 3;
 constexpr int kThreads = 32 * (kPlanWarp + 1);
 constexpr int kStages = 5;
 constexpr uint32_t kStage = 32768, kPiece = 128 * 128, kRun = 64 * 128;
 constexpr uint32_t kQBytes = 2 * kPiece;   // 128 rows x 128 values
-constexpr int kChunks = 6, kChunkTiles = 12;  // chunks that the planner may be ahead, tiles of a chunk
+constexpr int kChunks = 4, kChunkTiles = 12;  // chunks that the planner may be ahead, tiles of a chunk
 constexpr uint32_t kTmemCols = 512, kOCol = 256;
 constexpr int kGroupShift = 40;            // pair / group as (pair * ceil(2^40 / group)) >> 40 (attention.cu)
 // A row's reference is its maximum when it is set, in fp16 2^7 less, so that
@@ -253,7 +255,7 @@ struct Control {
   uint64_t sfull[2], pfull[2], odone[2], qfull[2];
   uint64_t turn[2], mfull, mfree, drain;
   Chunk chunk[kChunks];
-  float2 other[kRows];   // the second accumulator's reference and sum, when both hold the same rows
+  float row[2][2][kRows];  // exchange between the threads of a row
   int32_t warp_sum[kThreads / 32];
   int32_t run_hk, run_block, run_start, run_lo, run_hi, per_head;
   uint32_t tmem;
@@ -590,23 +592,27 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
     bool open = false;
     uint32_t open_tile = 0, v_st = 0, v_use = 0, v_tail = 0, more = 0;
     uint32_t begun = 0;                      // this accumulator has had a tile of the segment
-    // (the other's first turn is behind this one's first)
-    const auto take_turn = [&] {
-      if (acc == 1 || turns > 0) ok = ok && warp_try(my_turn, (turns - (acc ^ 1)) & 1, abort_flag, p.err);
-      ++turns;
-    };
     const auto values = [&] {
       const uint64_t v = desc_sw128(base + v_st * kStage, kRun);
 #pragma unroll
       for (int x = 0; x < 8; ++x)
-        tc_mma_f16_tmem(o_tmem, s_tmem + x * 8, v + (x >> 2) * (2 * kRun >> 4) + (x & 3) * 128, o_idesc, x > 0 ? 1u : more);
+        tc_mma_f16_tmem(o_tmem, s_tmem + (x >> 2) * kHalf + (x & 3) * 8, v + (x >> 2) * (2 * kRun >> 4) + (x & 3) * 128, o_idesc, x > 0 ? 1u : more);
       tc_commit(smem_u32(&ctl.kempty[v_st]));
     };
-    const auto weights = [&] {  // the open tile's values and weights are there
+    const auto wait_weights = [&] {  // of the open tile, and its values
       ok = ok && warp_try(smem_u32(&ctl.kfull[v_st]), v_use & 1, abort_flag, p.err);
       if (v_tail) fence_proxy_async_smem();
       ok = ok && warp_try(p_bar, steps & 1, abort_flag, p.err);
       ++steps;
+      tc_fence_after();
+    };
+    // Waits for this warp's turn, and behind it for the weights: they come
+    // latest when all runs smoothly.
+    const auto wait_turn = [&](bool product) {
+      if (acc == 1 || turns > 0) ok = ok && warp_try(my_turn, (turns - (acc ^ 1)) & 1, abort_flag, p.err);
+      ++turns;  // (the other's first turn is behind this one's first)
+      if (product) wait_weights();
+      tc_fence_after();
     };
     for (uint32_t n = 0; ok; ++n) {
       const uint32_t slot = n % kChunks;
@@ -629,33 +635,39 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
         const bool mine = two ? flags & (acc ? kSlot1 : kSlot0) : (((flags & kOdd ? 1 : 0) + i) & 1) == acc;
         const uint32_t k_st = uniform(2 * tile % kStages), k_use = 2 * tile / kStages;
         const uint32_t next_v = uniform((2 * tile + 1) % kStages), next_use = (2 * tile + 1) / kStages;
-        ok = warp_try(smem_u32(&ctl.kfull[k_st]), k_use & 1, abort_flag, p.err);
-        if (!mine) {  // (its arrival is for this use of the stages, so it waits for them)
-          ok = ok && warp_try(smem_u32(&ctl.kfull[next_v]), next_use & 1, abort_flag, p.err);
-          if (lane == 0) {
-            mbar_arrive(smem_u32(&ctl.kempty[k_st]));
-            mbar_arrive(smem_u32(&ctl.kempty[next_v]));
-          }
-          // a value product waits for its accumulator's next score product, but
-          // not so long that the loader runs out of stages
-          const bool close = open && tile - open_tile >= 2;
-          if (close) weights();
-          take_turn();
+        // A value product is issued with its accumulator's next score product,
+        // unless the keys are what all wait for.
+        if (open && !__any_sync(0xffffffffu, mbar_test_wait(smem_u32(&ctl.kfull[k_st]), k_use & 1))) {
+          wait_weights();
           if (!ok) break;
-          tc_fence_after();
+          if (elect_one()) values();
+          __syncwarp();
+          open = false;
+        }
+        if (!mine) {
+          // (nor so long that the loader runs out of stages)
+          const bool close = open && tile - open_tile >= 2;
+          wait_turn(close);
+          if (!ok) break;
           if (elect_one()) {
             if (close) values();
             mbar_arrive(its_turn);
           }
           __syncwarp();
           if (close) open = false;
+          // (its arrivals are for this use of the stages, so it waits for them)
+          ok = warp_try(smem_u32(&ctl.kfull[k_st]), k_use & 1, abort_flag, p.err) &&
+               warp_try(smem_u32(&ctl.kfull[next_v]), next_use & 1, abort_flag, p.err);
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&ctl.kempty[k_st]));
+            mbar_arrive(smem_u32(&ctl.kempty[next_v]));
+          }
           continue;
         }
+        ok = warp_try(smem_u32(&ctl.kfull[k_st]), k_use & 1, abort_flag, p.err);
         const bool was_open = open;
-        if (was_open) weights();
-        take_turn();
+        wait_turn(was_open);
         if (!ok) break;
-        tc_fence_after();
         if (elect_one()) {
           if (was_open) values();
           const uint64_t k = desc_sw128(base + k_st * kStage, 16);
@@ -679,10 +691,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
       }
       if (ok && (flags & kLast)) {
         const bool was_open = open;
-        if (was_open) weights();
-        take_turn();
+        wait_turn(was_open);
         if (!ok) break;
-        tc_fence_after();
         if (elect_one()) {
           if (was_open) values();
           mbar_arrive(its_turn);
@@ -702,21 +712,24 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
     __syncwarp();
   } else {
     // ================================================================ softmax
-    const int acc = warp / kSoftmaxWarps, r = tid & (kRows - 1);  // accumulator, row of it
+    // After a failed wait a chunk's tiles are walked without waiting, so that
+    // the named barriers still meet; nothing is written then.
+    const int acc = warp / kSoftmaxWarps, half = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;  // accumulator, keys and columns of it, row
+    const uint32_t pair_bar = 1 + acc * 4 + (warp & 3);
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
-    const uint32_t s_at = tmem + lanes + acc * kTile, o_at = tmem + lanes + kOCol + acc * kTile;
+    const uint32_t s_at = tmem + lanes + acc * kTile + half * kHalf, o_at = tmem + lanes + kOCol + acc * kTile + half * kHalf;
     uint32_t segs = 0, steps = 0;   // segments begun; tiles of this accumulator
     uint32_t merged = 0;            // segments whose two accumulators were added up
     bool merging = false;           // the last one was
     int steps_of_seg = 0;
     int vis = 0;                    // of this thread's row
     bool valid = false, ok = true;
-    float m = -INFINITY;            // reference, in powers of two
-    float l = 0.0f;
-    for (uint32_t n = 0; ok; ++n) {
+    float m = -INFINITY;            // the row's reference, in powers of two
+    float l = 0.0f;                 // this thread's share of the sum
+    for (uint32_t n = 0;; ++n) {
       const uint32_t slot = n % kChunks;
-      ok = warp_try(smem_u32(&ctl.cfull[slot]), (n / kChunks) & 1, abort_flag, p.err);
-      if (!ok) break;
+      ok = ok && warp_try(smem_u32(&ctl.cfull[slot]), (n / kChunks) & 1, abort_flag, p.err);
+      if (bar_red_or(pair_bar, 64, !ok)) break;
       const Chunk& d = ctl.chunk[slot];
       const int flags = d.flags;
       if (flags & kEnd) break;
@@ -731,13 +744,13 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
           vis = pl.row_vis[t];
           if (acc == 0 || two) {
             const int h = d.hk * p.group + pair - group_div(p, pair) * p.group;
-            const uint4* src = reinterpret_cast<const uint4*>(p.q + t * p.q_row_stride + h * p.q_head_stride);
-            uint4 q[16];
+            const uint4* src = reinterpret_cast<const uint4*>(p.q + t * p.q_row_stride + h * p.q_head_stride) + half * 8;
+            uint4 q[8];
 #pragma unroll
-            for (int u = 0; u < 16; ++u) q[u] = __ldg(src + u);
-            uint8_t* dst = smem + kOff_Q + acc * kQBytes + r * 128;
+            for (int u = 0; u < 8; ++u) q[u] = __ldg(src + u);
+            uint8_t* dst = smem + kOff_Q + acc * kQBytes + half * kPiece + r * 128;
 #pragma unroll
-            for (int u = 0; u < 16; ++u) *reinterpret_cast<uint4*>(dst + (u >> 3) * kPiece + (((u & 7) ^ (r & 7)) << 4)) = q[u];
+            for (int u = 0; u < 8; ++u) *reinterpret_cast<uint4*>(dst + ((u ^ (r & 7)) << 4)) = q[u];
           }
         }
         fence_proxy_async_smem();
@@ -745,7 +758,6 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
         if (lane == 0) mbar_arrive(smem_u32(&ctl.qfull[acc]));
         // the other accumulator's warps have read this one's output and sums
         if (acc == 1 && merging) ok = warp_try(smem_u32(&ctl.mfree), (merged - 1) & 1, abort_flag, p.err);
-        if (!ok) break;
         ++segs;
         steps_of_seg = 0;
         m = -INFINITY;
@@ -755,40 +767,39 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
       const bool mine = valid && off + r >= d.p0 && off + r < d.p1;
       // keys [lo, hi) count for this row, relative to the chunk's first
       int lo = d.lo - d.pos0, hi = mine ? min(vis, d.hi) - d.pos0 : 0;
-      if (flags & kHole0) lo = max(lo, kTile / 2);
-      if (flags & kHole1) hi = min(hi, kTile / 2);
+      if (flags & kHole0) lo = max(lo, kHalf);
+      if (flags & kHole1) hi = min(hi, kHalf);
       const int turn = flags & kOdd ? 1 : 0;
       const bool active = !two || (flags & (acc ? kSlot1 : kSlot0));
 #pragma unroll 1
       for (int i = two ? 0 : turn ^ acc; active && i < tiles; i += two ? 1 : 2) {
-        // columns [c_lo, c_lo + c_len) count
-        const int c_lo = max(0, lo - i * kTile), c_len = max(0, min(hi - i * kTile, kTile) - c_lo);
-        const bool some = __any_sync(0xffffffffu, c_len > 0), full = __all_sync(0xffffffffu, c_len == kTile);
-        ok = warp_try(smem_u32(&ctl.sfull[acc]), steps & 1, abort_flag, p.err);
-        if (!ok) break;
+        // keys [k_lo, k_lo + k_len) of the tile count
+        const int k_lo = max(0, lo - i * kTile), k_len = max(0, min(hi - i * kTile, kTile) - k_lo);
+        const bool some = __any_sync(0xffffffffu, k_len > 0), full = __all_sync(0xffffffffu, k_len == kTile);
+        bool raise = k_len > 0 && m == -INFINITY;  // (alike in the two threads of a row)
+        bool again = __any_sync(0xffffffffu, raise);
+        if (ok) ok = warp_try(smem_u32(&ctl.sfull[acc]), steps & 1, abort_flag, p.err);
         tc_fence_after();
         if (some) {
-          const auto masked = [&](auto& x, int c) {
+          const auto masked = [&](uint32_t (&x)[32], int c) {
             if (full) return;
             // a bit for each of the columns from c on; the empty asm keeps the
             // tests of all columns from being worked out (and spilled) at once
-            const int from = min(max(c_lo - c, 0), 32), to = min(max(c_lo + c_len - c, 0), 32);
+            const int at = half * kHalf + c, from = min(max(k_lo - at, 0), 32), to = min(max(k_lo + k_len - at, 0), 32);
             uint32_t bits = static_cast<uint32_t>((uint64_t{1} << to) - 1) & ~static_cast<uint32_t>((uint64_t{1} << from) - 1);
             asm volatile("" : "+r"(bits));
 #pragma unroll
-            for (int k = 0; k < static_cast<int>(sizeof(x) / 4); ++k)
+            for (int k = 0; k < 32; ++k)
               if (!(bits >> k & 1)) x[k] = 0xff800000u;  // -inf
           };
-          uint32_t w[kTile / 2];
-          bool raise = c_len > 0 && m == -INFINITY;
-          bool again = __any_sync(0xffffffffu, raise);
+          uint32_t w[kHalf / 2];
           float sum = 0.0f;
 #pragma unroll 1
           for (bool once = false;; once = true) {
             if (again) {  // a new reference
               float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-              for (int c = 0; c < kTile; c += 32) {
+              for (int c = 0; c < kHalf; c += 32) {
                 uint32_t x[32];
                 tmem_ld(s_at + c, x);
                 tmem_wait_ld();
@@ -798,13 +809,18 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
                 for (int k = 0; k < 32; k += 2)
                   top[k / 2 & 3] = fmaxf(fmaxf(top[k / 2 & 3], __uint_as_float(x[k])), __uint_as_float(x[k + 1]));
               }
-              const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2 - kBelow<DTYPE>;
-              const float f = raise && most > m ? ex2(m - most) : 1.0f;
-              if (raise && most > m) m = most;
+              // the row's, and whether either of its threads asked for it
+              const float mine_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2 - kBelow<DTYPE>;
+              bar_sync(pair_bar, 64);  // what was exchanged before has been read
+              ctl.row[acc][half][r] = mine_top;
+              bar_sync(pair_bar, 64);
+              const float most = fmaxf(mine_top, ctl.row[acc][half ^ 1][r]);
+              const float f = most > m ? ex2(m - most) : 1.0f;
+              if (most > m) m = most;
               l *= f;
               if (steps_of_seg > 0) {  // (the score product came behind the last value product)
 #pragma unroll 1
-                for (int c = 0; c < kPagedDim; c += 16) {
+                for (int c = 0; c < kHalf; c += 16) {
                   uint32_t o[16];
                   tmem_ld(o_at + c, o);
                   tmem_wait_ld();
@@ -821,31 +837,28 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
             const float2 scale = make_float2(p.scale_log2, p.scale_log2);
             const float2 ref = m == -INFINITY ? make_float2(0.0f, 0.0f) : make_float2(-m, -m);
             float2 part[2] = {};
-            uint32_t x[2][16];
-            tmem_ld(s_at, x[0]);
 #pragma unroll
-            for (int c = 0; c < kTile; c += 16) {
-              uint32_t(&y)[16] = x[c / 16 & 1];
+            for (int c = 0; c < kHalf; c += 32) {
+              uint32_t x[32];
+              tmem_ld(s_at + c, x);
               tmem_wait_ld();
-              reg_fence(y);
-              if (c + 16 < kTile) tmem_ld(s_at + c + 16, x[(c / 16 & 1) ^ 1]);
-              masked(y, c);
+              reg_fence(x);
+              masked(x, c);
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                float2 a = fma2(make_float2(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1])), scale, ref);
+              for (int k = 0; k < 16; ++k) {
+                float2 a = fma2(make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), scale, ref);
                 a = make_float2(ex2(a.x), ex2(a.y));
                 part[k & 1] = add2(part[k & 1], a);
                 w[c / 2 + k] = pack2<DTYPE>(a.x, a.y);
               }
             }
             sum = (part[0].x + part[1].x) + (part[0].y + part[1].y);
-            raise = sum > kLimit<DTYPE>;
-            again = !once && __any_sync(0xffffffffu, raise);
+            again = !once && bar_red_or(pair_bar, 64, sum > kLimit<DTYPE>);
             if (!again) break;
           }
           l += sum;
 #pragma unroll
-          for (int c = 0; c < kTile / 2; c += 16) {
+          for (int c = 0; c < kHalf / 2; c += 16) {
             uint32_t v[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) v[k] = w[c + k];
@@ -854,7 +867,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
         } else {  // none of the warp's rows sees a key of this tile
           uint32_t w[16] = {};
 #pragma unroll
-          for (int c = 0; c < kTile / 2; c += 16) tmem_st_x16(s_at + c, w);
+          for (int c = 0; c < kHalf / 2; c += 16) tmem_st_x16(s_at + c, w);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -863,29 +876,31 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
         ++steps;
         ++steps_of_seg;
       }
-      if (!ok) break;
       if (flags & kLast) {
         // ---- output of the segment
-        ok = warp_try(smem_u32(&ctl.odone[acc]), (segs - 1) & 1, abort_flag, p.err);
-        if (!ok) break;
+        bar_sync(pair_bar, 64);  // what was exchanged before has been read
+        ctl.row[acc][half][r] = l;
+        bar_sync(pair_bar, 64);
+        float sum = ctl.row[acc][0][r] + ctl.row[acc][1][r];
+        if (ok) ok = warp_try(smem_u32(&ctl.odone[acc]), (segs - 1) & 1, abort_flag, p.err);
         tc_fence_after();
         merging = !two;
         if (merging && acc == 1) {  // the other accumulator's warps add this one up
-          ctl.other[r] = make_float2(m, l);
+          bar_sync(pair_bar, 64);
+          ctl.row[1][half][r] = half ? sum : m;
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&ctl.mfull));
         } else {
           // out = f0 O (+ f1 O of the other accumulator)
-          float f0 = steps_of_seg > 0 ? 1.0f : 0.0f, f1 = 0.0f, sum = l;
+          float f0 = steps_of_seg > 0 ? 1.0f : 0.0f, f1 = 0.0f;
           if (merging) {
-            ok = warp_try(smem_u32(&ctl.mfull), merged & 1, abort_flag, p.err);
-            if (!ok) break;
+            if (ok) ok = warp_try(smem_u32(&ctl.mfull), merged & 1, abort_flag, p.err);
             tc_fence_after();
-            const float2 b = ctl.other[r];
-            const float top = fmaxf(m, b.x), at = top == -INFINITY ? 0.0f : top;
+            const float m1 = ctl.row[1][0][r], l1 = ctl.row[1][1][r];
+            const float top = fmaxf(m, m1), at = top == -INFINITY ? 0.0f : top;
             f0 = ex2(m - at);  // (accumulator 0 takes a segment's first tile)
-            f1 = ex2(b.x - at);
-            sum = f0 * l + f1 * b.y;
+            f1 = ex2(m1 - at);
+            sum = f0 * sum + f1 * l1;
             m = top;
           }
           const bool both = merging && __any_sync(0xffffffffu, f1 != 0.0f);
@@ -897,36 +912,38 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
             f1 *= inv;
           }
           const int row = off + r;  // of the block
-          uint4* out = reinterpret_cast<uint4*>(p.out + t * p.out_row_stride + static_cast<int64_t>(h) * kPagedDim);
-          float4* part = pl.partial + static_cast<int64_t>(d.part) * (kPagedDim / 4) * kBlockPairs + row;
+          uint4* out = reinterpret_cast<uint4*>(p.out + t * p.out_row_stride + static_cast<int64_t>(h) * kPagedDim + half * kHalf);
+          float4* part = pl.partial + (static_cast<int64_t>(d.part) * (kPagedDim / 4) + half * (kHalf / 4)) * kBlockPairs + row;
 #pragma unroll 1
-          for (int c = 0; c < kPagedDim; c += 32) {
-            uint32_t o[32];
+          for (int c = 0; c < kHalf; c += 16) {
+            uint32_t o[16];
             __syncwarp();
             tmem_ld(o_at + c, o);
             tmem_wait_ld();
             reg_fence(o);
-            float y[32];
+            float y[16];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) y[e] = f0 == 0.0f ? 0.0f : __uint_as_float(o[e]) * f0;
+            for (int e = 0; e < 16; ++e) y[e] = f0 == 0.0f ? 0.0f : __uint_as_float(o[e]) * f0;
             if (both) {
               tmem_ld(o_at + kTile + c, o);
               tmem_wait_ld();
               reg_fence(o);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) y[e] = f1 == 0.0f ? y[e] : fmaf(__uint_as_float(o[e]), f1, y[e]);
+              for (int e = 0; e < 16; ++e) y[e] = f1 == 0.0f ? y[e] : fmaf(__uint_as_float(o[e]), f1, y[e]);
             }
-            if (valid && whole) {
+            if (valid && ok) {
+              if (whole) {
 #pragma unroll
-              for (int e = 0; e < 32; e += 8)
-                out[(c + e) / 8] = make_uint4(pack2<DTYPE>(y[e], y[e + 1]), pack2<DTYPE>(y[e + 2], y[e + 3]),
-                                              pack2<DTYPE>(y[e + 4], y[e + 5]), pack2<DTYPE>(y[e + 6], y[e + 7]));
-            } else if (valid) {
+                for (int e = 0; e < 16; e += 8)
+                  out[(c + e) / 8] = make_uint4(pack2<DTYPE>(y[e], y[e + 1]), pack2<DTYPE>(y[e + 2], y[e + 3]),
+                                                pack2<DTYPE>(y[e + 4], y[e + 5]), pack2<DTYPE>(y[e + 6], y[e + 7]));
+              } else {
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) part[(c + e) / 4 * kBlockPairs] = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                for (int e = 0; e < 16; e += 4) part[(c + e) / 4 * kBlockPairs] = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+              }
             }
           }
-          if (valid) {
+          if (valid && ok && half == 0) {
             if (!whole) pl.stats[static_cast<int64_t>(d.part) * kBlockPairs + row] = make_float2(m, sum);
             else if (p.lse) p.lse[static_cast<int64_t>(t) * p.num_heads + h] = row_lse(m, sum);
           }
