@@ -6,9 +6,9 @@
 // A group's (row, head) pairs of one K/V head are taken 256 at a time: a block.
 // Its keys are what each of its requests has behind the prefix, then the
 // prefix itself, once, for all of its rows: one list of 128-key tiles.  The
-// tiles of all blocks and K/V heads are concatenated and cut into equal runs,
-// one per CTA; a block cut by a boundary leaves partial sums that join_kernel
-// adds in a fixed order.
+// tiles of all blocks and K/V heads are concatenated and cut into runs, one per
+// CTA: equal ones, or, where that loses little, each block's own.  A block cut
+// by a boundary leaves partial sums that join_kernel adds in a fixed order.
 //
 // A CTA holds two score accumulators, two outputs (128 rows x 128 columns each,
 // all 512 TMEM columns) and a ring of five 32 KB stages, each a tile's keys or
@@ -82,10 +82,12 @@ struct Span {
   int32_t start, tiles;  // tiles of the block before it; its own
   int32_t p0, p1;
 };
-// The first block of a CTA's run (for the join).
+// Where a CTA's run begins (for the join).
 struct RunInfo {
-  int32_t item, start, total;  // K/V head * blocks + block; first tile of it; tiles of all
-  int32_t row0, pair0, pairs, hk, pad;
+  int32_t item;    // K/V head * blocks + block, -1: it has no tiles
+  int32_t inside;  // behind the block's first tile
+  int32_t row0, pair0, pairs, hk;
+  int32_t pad[2];
 };
 
 struct Plan {
@@ -131,18 +133,24 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   const int64_t pair0 = static_cast<int64_t>(i - g * pl.blocks_per_group) * kBlockPairs;
   const int64_t pairs = min(static_cast<int64_t>(rows) * p.group - pair0, static_cast<int64_t>(kBlockPairs));
   if (pairs <= 0) {
-    if (lane == 0) pl.block_tiles[i] = 0;
+    if (lane == 0) {
+      pl.block[i] = blk;
+      pl.block_tiles[i] = 0;
+    }
     return;
   }
   blk.pair0 = static_cast<int>(pair0);
   blk.pairs = static_cast<int>(pairs);
   const int r0 = blk.row0 + group_div(p, pair0), r1 = blk.row0 + group_div(p, pair0 + pairs - 1) + 1;  // its rows
-  // the requests of its first and last row
-  const auto request_of = [&](int t) {
-    int lo = reqs.x, hi = reqs.y - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (__ldg(p.cu_seqlens_q + mid) <= t) lo = mid; else hi = mid - 1;
+  // the request of a row, 32 tests at a time
+  const auto request_of = [&](int row) {
+    int lo = reqs.x, n = reqs.y - reqs.x;
+    while (n > 1) {
+      const int step = (n + 31) >> 5, at = lane * step;
+      const uint32_t before = __ballot_sync(0xffffffffu, at < n && __ldg(p.cu_seqlens_q + lo + (at < n ? at : 0)) <= row);
+      const int skip = max(0, __popc(before) - 1) * step;
+      lo += skip;
+      n = min(step, n - skip);
     }
     return lo;
   };
@@ -256,8 +264,8 @@ struct Control {
   uint64_t turn[2], mfull, mfree, drain;
   Chunk chunk[kChunks];
   float row[2][2][kRows];  // exchange between the threads of a row
-  int32_t warp_sum[kThreads / 32];
-  int32_t run_hk, run_block, run_start, run_lo, run_hi, per_head;
+  Block first;           // the block that this CTA's run begins in
+  int32_t run_hk, run_block, run_start, run_lo, run_hi, per_head, worst;
   uint32_t tmem;
   int abort;
 };
@@ -265,10 +273,10 @@ constexpr uint32_t kOff_Q = kStages * kStage, kOff_Ctl = kOff_Q + 2 * kQBytes;
 constexpr uint32_t kSmem = kOff_Ctl + sizeof(Control);
 static_assert(kSmem <= 232448, "227 KB per CTA");
 
-__device__ __forceinline__ int run_begin(int total, int cta, int used) {
-  return static_cast<int>(static_cast<int64_t>(total) * cta / used);
-}
-__device__ __forceinline__ int used_ctas(int total, int ctas) { return min(total, ctas); }
+// A run of a block's own pays for up to this many tiles more than an equal run
+// over all blocks: a run that crosses from one block to the next has queries to
+// wait for and sums to write twice.
+constexpr int kOwnRunTiles = 3;
 
 template <int DTYPE>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -316,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
 
   if (base & 1023u) {  // the swizzled layouts need it; the runtime places the window there
     if (tid == 0) {
-      pl.info[blockIdx.x].total = 0;
+      pl.info[blockIdx.x].item = -1;
       atomicOr(p.err, kErrTimeout);
     }
     return;
@@ -341,58 +349,99 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
     mbar_init(smem_u32(&ctl.mfree), kSoftmaxWarps);
     mbar_init(smem_u32(&ctl.drain), 2);
     ctl.abort = 0;
+    ctl.run_lo = ctl.run_hi = ctl.worst = 0;
     fence_barrier_init();
+  }
+  if (tid == 32 * kLoadWarp) {
+    prefetch_tmap(&maps.k);
+    prefetch_tmap(&maps.v);
   }
   if (warp == kMmaWarp) tmem_alloc<kTmemCols>(smem_u32(&ctl.tmem));
   __syncthreads();
   pdl_wait();  // everything below reads what earlier kernels wrote
 
-  // ---- this CTA's run of tiles and the block that it starts in
+  // ---- this CTA's run of tiles and the block that it begins in
   {
+    int* warp_sum = reinterpret_cast<int*>(smem);  // (the ring is not in use yet)
     const int per = (pl.blocks + kThreads - 1) / kThreads;
     const int first = min(pl.blocks, tid * per), last = min(pl.blocks, first + per);
+    Block own = {};
     int mine = 0;
-    for (int i = first; i < last; ++i) mine += pl.block_tiles[i];
+    if (per == 1) {
+      if (first < last) own = pl.block[first];
+      mine = own.tiles;
+    } else {
+      for (int i = first; i < last; ++i) mine += pl.block_tiles[i];
+    }
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += y;
     }
-    if (lane == 31) ctl.warp_sum[warp] = incl;
+    if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
     int before = incl - mine, per_head = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
-      const int v = ctl.warp_sum[w];
+      const int v = warp_sum[w];
       before += w < warp ? v : 0;
       per_head += v;
     }
-    const int total = per_head * p.num_kv_heads, used = used_ctas(total, pl.ctas), cta = blockIdx.x;
-    const int lo = cta < used ? run_begin(total, cta, used) : 0, hi = cta < used ? run_begin(total, cta + 1, used) : 0;
-    if (tid == 0) {
+    const int heads = p.num_kv_heads, total = per_head * heads, cta = blockIdx.x;
+    const int used = min(pl.ctas, (total + 1) / 2);  // (two tiles go through the two accumulators at a time)
+    // A block's own CTAs: [S used / total, (S + t) used / total) of a block of t
+    // tiles behind S others, at least t used / total of them.  (32 bits.)
+    const uint32_t all = total, n_all = used;
+    bool own_runs = per == 1 && static_cast<int64_t>(pl.blocks) * heads <= used && total < 1 << 22;
+    if (own_runs) {
+      const uint32_t least = mine * n_all / all;
+      const int worst = __reduce_max_sync(0xffffffffu, mine == 0 ? 0 : least == 0 ? INT32_MAX : static_cast<int>((mine + least - 1) / least));
+      if (lane == 0 && worst > 0) atomicMax(&ctl.worst, worst);
+      __syncthreads();
+      own_runs = ctl.worst <= static_cast<int>((all + n_all - 1) / n_all) + kOwnRunTiles;
+    }
+    // the thread whose blocks hold the run's first tile
+    int lo = 0, hi = 0, hk = -1;
+    if (cta >= used) {
+      if (tid == 0) pl.info[cta].item = -1;
+    } else if (own_runs) {
+      const uint32_t x = ((cta + 1) * all - 1) / n_all;  // the last tile that may be the first of CTA cta's block
+      const int h = x / per_head, at = x - h * per_head;
+      if (before <= at && at < before + mine) {
+        const uint32_t s = h * per_head + before, c0 = s * n_all / all, n = (s + mine) * n_all / all - c0;
+        hk = h;
+        lo = s + mine * (cta - c0) / n;
+        hi = s + mine * (cta + 1 - c0) / n;
+      }
+    } else {
+      lo = static_cast<int>(static_cast<int64_t>(total) * cta / used);
+      hi = static_cast<int>(static_cast<int64_t>(total) * (cta + 1) / used);
+      const int h = lo / per_head, at = lo - h * per_head;
+      if (before <= at && at < before + mine) hk = h;
+    }
+    if (hk >= 0) {
+      int i = first;
+      if (per > 1) {
+        while (hk * per_head + before + pl.block_tiles[i] <= lo) before += pl.block_tiles[i++];
+        own = pl.block[i];
+      }
+      const int start = hk * per_head + before;
+      ctl.first = own;
+      ctl.run_hk = hk;
+      ctl.run_block = i;
+      ctl.run_start = start;
       ctl.run_lo = lo;
       ctl.run_hi = hi;
       ctl.per_head = per_head;
-      pl.info[cta].total = total;
-    }
-    if (lo < hi) {
-      const int hk = lo / per_head, at = lo - hk * per_head;
-      if (before <= at && at < before + mine) {  // the thread whose blocks hold the first tile
-        int i = first;
-        while (before + pl.block_tiles[i] <= at) before += pl.block_tiles[i++];
-        ctl.run_hk = hk;
-        ctl.run_block = i;
-        ctl.run_start = hk * per_head + before;
-        const Block b = pl.block[i];
-        RunInfo& info = pl.info[cta];
-        info.item = hk * pl.blocks + i;
-        info.start = hk * per_head + before;
-        info.row0 = b.row0;
-        info.pair0 = b.pair0;
-        info.pairs = b.pairs;
-        info.hk = hk;
-      }
+      RunInfo info = {};
+      info.item = hk * pl.blocks + i;
+      info.inside = lo > start;
+      info.row0 = own.row0;
+      info.pair0 = own.pair0;
+      info.pairs = own.pairs;
+      info.hk = hk;
+      pl.info[cta] = info;
     }
   }
   __syncthreads();
@@ -406,8 +455,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
     bool ok = true;
     const int hi = ctl.run_hi, per_head = ctl.per_head;
     int at = ctl.run_lo, hk = ctl.run_hk, block = ctl.run_block, start = ctl.run_start;
+    Block b = ctl.first;
     while (ok && at < hi) {
-      const Block b = pl.block[block];
       const int from = at - start, to = min(b.tiles, hi - start);  // tiles of the block
       const bool two = b.pairs > kRows;
       const int segment = (two ? kTwo : 0) | (from == 0 && to == b.tiles ? kWhole : 0);
@@ -501,6 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
           break;
         }
       }
+      if (ok) b = pl.block[block];
     }
     if (ok) {
       const uint32_t slot = n % kChunks;
@@ -726,6 +776,37 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
     bool valid = false, ok = true;
     float m = -INFINITY;            // the row's reference, in powers of two
     float l = 0.0f;                 // this thread's share of the sum
+    // The 32 rows of this warp in its half of the queries' buffer: rows of 128
+    // bytes, 16-byte units swizzled.
+    uint8_t* const my_rows = smem + kOff_Q + acc * kQBytes + half * kPiece + (warp & 3) * 32 * 128;
+    const auto unit_at = [](int row, int unit) { return (unit ^ (row & 7)) << 4; };
+    // This warp's part of a segment's queries, and what its rows see.
+    const auto load_queries = [&](int row0, int pair0, int pairs, int hk, bool two) {
+      // (the products that read the queries before are done: this warp has
+      // waited for its own, and through mfull for the other issuer's)
+      const int off = two ? acc * kRows : 0, pair = pair0 + off + r, t = row0 + group_div(p, pair);
+      valid = off + r < pairs;
+      if (valid) vis = pl.row_vis[t];
+      if (acc == 0 || two) {
+        // eight lanes a row: a warp's load touches four lines (with a row a lane
+        // it touched 32, and 256 rows took 7,000 cycles)
+        const int h = hk * p.group + pair - group_div(p, pair) * p.group;
+        const int64_t from = valid ? t * p.q_row_stride + h * p.q_head_stride : -1;
+        uint4 q[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int64_t at = __shfl_sync(0xffffffffu, from, 4 * u + (lane >> 3));
+          q[u] = at < 0 ? make_uint4(0, 0, 0, 0) : __ldg(reinterpret_cast<const uint4*>(p.q + at) + half * 8 + (lane & 7));
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) *reinterpret_cast<uint4*>(my_rows + (4 * u + (lane >> 3)) * 128 + unit_at(4 * u + (lane >> 3), lane & 7)) = q[u];
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl.qfull[acc]));
+    };
+    // (the first segment's without waiting for the planner)
+    if (ctl.run_lo < ctl.run_hi) load_queries(ctl.first.row0, ctl.first.pair0, ctl.first.pairs, ctl.run_hk, ctl.first.pairs > kRows);
     for (uint32_t n = 0;; ++n) {
       const uint32_t slot = n % kChunks;
       ok = ok && warp_try(smem_u32(&ctl.cfull[slot]), (n / kChunks) & 1, abort_flag, p.err);
@@ -736,26 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
       const bool two = flags & kTwo;
       const int off = two ? acc * kRows : 0;  // first pair of this accumulator
       if (flags & kFirst) {
-        // (the products that read the queries before are done: this warp has
-        // waited for its own, and through mfull for the other issuer's)
-        const int pair = d.pair0 + off + r, t = d.row0 + group_div(p, pair);
-        valid = off + r < d.pairs;
-        if (valid) {
-          vis = pl.row_vis[t];
-          if (acc == 0 || two) {
-            const int h = d.hk * p.group + pair - group_div(p, pair) * p.group;
-            const uint4* src = reinterpret_cast<const uint4*>(p.q + t * p.q_row_stride + h * p.q_head_stride) + half * 8;
-            uint4 q[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) q[u] = __ldg(src + u);
-            uint8_t* dst = smem + kOff_Q + acc * kQBytes + half * kPiece + r * 128;
-#pragma unroll
-            for (int u = 0; u < 8; ++u) *reinterpret_cast<uint4*>(dst + ((u ^ (r & 7)) << 4)) = q[u];
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctl.qfull[acc]));
+        if (segs > 0) load_queries(d.row0, d.pair0, d.pairs, d.hk, two);
         // the other accumulator's warps have read this one's output and sums
         if (acc == 1 && merging) ok = warp_try(smem_u32(&ctl.mfree), (merged - 1) & 1, abort_flag, p.err);
         ++segs;
@@ -912,7 +974,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
             f1 *= inv;
           }
           const int row = off + r;  // of the block
-          uint4* out = reinterpret_cast<uint4*>(p.out + t * p.out_row_stride + static_cast<int64_t>(h) * kPagedDim + half * kHalf);
+          const int64_t to = valid && ok ? t * p.out_row_stride + static_cast<int64_t>(h) * kPagedDim + half * kHalf : -1;
           float4* part = pl.partial + (static_cast<int64_t>(d.part) * (kPagedDim / 4) + half * (kHalf / 4)) * kBlockPairs + row;
 #pragma unroll 1
           for (int c = 0; c < kHalf; c += 16) {
@@ -931,17 +993,27 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
 #pragma unroll
               for (int e = 0; e < 16; ++e) y[e] = f1 == 0.0f ? y[e] : fmaf(__uint_as_float(o[e]), f1, y[e]);
             }
-            if (valid && ok) {
-              if (whole) {
+            if (whole) {  // rounded, into the queries' place, which is free now
 #pragma unroll
-                for (int e = 0; e < 16; e += 8)
-                  out[(c + e) / 8] = make_uint4(pack2<DTYPE>(y[e], y[e + 1]), pack2<DTYPE>(y[e + 2], y[e + 3]),
-                                                pack2<DTYPE>(y[e + 4], y[e + 5]), pack2<DTYPE>(y[e + 6], y[e + 7]));
-              } else {
+              for (int e = 0; e < 16; e += 8)
+                *reinterpret_cast<uint4*>(my_rows + lane * 128 + unit_at(lane, (c + e) / 8)) =
+                    make_uint4(pack2<DTYPE>(y[e], y[e + 1]), pack2<DTYPE>(y[e + 2], y[e + 3]), pack2<DTYPE>(y[e + 4], y[e + 5]),
+                               pack2<DTYPE>(y[e + 6], y[e + 7]));
+            } else if (valid && ok) {
 #pragma unroll
-                for (int e = 0; e < 16; e += 4) part[(c + e) / 4 * kBlockPairs] = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
-              }
+              for (int e = 0; e < 16; e += 4) part[(c + e) / 4 * kBlockPairs] = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
             }
+          }
+          if (whole) {  // and out, eight lanes a row
+            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const int row_u = 4 * u + (lane >> 3);
+              const int64_t at = __shfl_sync(0xffffffffu, to, row_u);
+              const uint4 v = *reinterpret_cast<const uint4*>(my_rows + row_u * 128 + unit_at(row_u, lane & 7));
+              if (at >= 0) *(reinterpret_cast<uint4*>(p.out + at) + (lane & 7)) = v;
+            }
+            __syncwarp();
           }
           if (valid && ok && half == 0) {
             if (!whole) pl.stats[static_cast<int64_t>(d.part) * kBlockPairs + row] = make_float2(m, sum);
@@ -987,17 +1059,17 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // a CTA of the first kernel per thread (plan_shared)
   RunInfo info = {};
+  info.item = -1;
   if (tid < pl.ctas) info = pl.info[tid];
-  const int item = BY_ITEM ? blockIdx.x : pl.info[blockIdx.x + 1].item, total = pl.info[0].total;
+  const int item = BY_ITEM ? blockIdx.x : pl.info[blockIdx.x + 1].item;
   if (tid == 0) first_cta = INT32_MAX;
   __syncthreads();
   // the CTAs whose run begins inside the block: consecutive ones
-  const int used = used_ctas(total, pl.ctas);
-  const bool inside = tid > 0 && tid < used && info.item == item && info.start < run_begin(total, tid, used);
+  const bool inside = tid > 0 && info.item == item && info.inside;
   if (inside) atomicMin(&first_cta, tid);
   const int parts = 1 + __syncthreads_count(inside);
   const int c = first_cta;  // the first boundary; the part before it is the previous CTA's
-  if (parts == 1 || (!BY_ITEM && c != static_cast<int>(blockIdx.x) + 1)) return;
+  if (item < 0 || parts == 1 || (!BY_ITEM && c != static_cast<int>(blockIdx.x) + 1)) return;
   if (tid == c) its = info;
   __syncthreads();
   const int row = (BY_ITEM ? blockIdx.y : blockIdx.y * 2 + (warp >> 2)) * 32 + lane, cols = (BY_ITEM ? blockIdx.z : warp & 3) * kJoinCols;
