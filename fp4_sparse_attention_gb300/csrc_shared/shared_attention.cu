@@ -1051,6 +1051,7 @@ template <int DTYPE, bool BY_ITEM>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Plan pl) {
   __shared__ float4 sums[BY_ITEM ? kJoinWarps : 1][kJoinCols / 4][32];
   __shared__ float2 part[kJoinWarps][32];
+  __shared__ uint4 staged[BY_ITEM ? 1 : kJoinWarps][32 * 4];
   __shared__ RunInfo its;
   __shared__ int first_cta;
   pdl_wait();
@@ -1076,6 +1077,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   if (row - lane >= its.pairs) return;  // (BY_ITEM: the whole CTA)
   float4 acc[kJoinCols / 4] = {};
   float m = -INFINITY, l = 0.0f;
+#pragma unroll 2
   for (int i = BY_ITEM ? warp : 0; i < parts; i += BY_ITEM ? kJoinWarps : 1) {
     // part i is CTA c - 1 + i's; of the first one its last segment, of the others their first
     const int64_t at = 2 * (c - 1 + i) + (i == 0);
@@ -1119,15 +1121,35 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
       acc[0].w = fmaf(f, o.w, acc[0].w);
     }
   }
-  if (row >= its.pairs) return;
+  // Out by whole 32-byte sectors: a warp's 32 rows x 64 bytes (BY_ITEM: the
+  // CTA's), four lanes a row.  (Eight bytes a lane, as they come, took twice as
+  // long as all the rest.)
+  const bool have = row < its.pairs;
   const int pair = its.pair0 + row, t = its.row0 + group_div(p, pair);
   const int h = its.hk * p.group + pair - group_div(p, pair) * p.group;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  uint2* out = reinterpret_cast<uint2*>(p.out + t * p.out_row_stride + static_cast<int64_t>(h) * kPagedDim + cols);
+  const int64_t to = have ? t * p.out_row_stride + static_cast<int64_t>(h) * kPagedDim + cols : -1;
+  if (p.lse && have && cols == 0 && (!BY_ITEM || warp == 0)) p.lse[static_cast<int64_t>(t) * p.num_heads + h] = row_lse(m, l);
+  uint4* const rows = staged[BY_ITEM ? 0 : warp];
+  if constexpr (BY_ITEM) {
+    reinterpret_cast<uint2*>(rows)[lane * 8 + warp] = make_uint2(pack2<DTYPE>(acc[0].x * inv, acc[0].y * inv), pack2<DTYPE>(acc[0].z * inv, acc[0].w * inv));
+    __syncthreads();
+    if (warp > 0) return;
+  } else {
 #pragma unroll
-  for (int v = 0; v < (BY_ITEM ? 1 : kJoinCols / 4); ++v)
-    out[BY_ITEM ? warp : v] = make_uint2(pack2<DTYPE>(acc[v].x * inv, acc[v].y * inv), pack2<DTYPE>(acc[v].z * inv, acc[v].w * inv));
-  if (p.lse && cols == 0 && (!BY_ITEM || warp == 0)) p.lse[static_cast<int64_t>(t) * p.num_heads + h] = row_lse(m, l);
+    for (int v = 0; v < kJoinCols / 4; v += 2)
+      rows[lane * 4 + ((v / 2) ^ (lane >> 1 & 3))] =
+          make_uint4(pack2<DTYPE>(acc[v].x * inv, acc[v].y * inv), pack2<DTYPE>(acc[v].z * inv, acc[v].w * inv),
+                     pack2<DTYPE>(acc[v + 1].x * inv, acc[v + 1].y * inv), pack2<DTYPE>(acc[v + 1].z * inv, acc[v + 1].w * inv));
+    __syncwarp();
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row_i = 8 * i + (lane >> 2), unit = lane & 3;
+    const int64_t at = __shfl_sync(0xffffffffu, to, row_i);
+    const uint4 v = rows[row_i * 4 + (BY_ITEM ? unit : unit ^ (row_i >> 1 & 3))];
+    if (at >= 0) *(reinterpret_cast<uint4*>(p.out + at) + unit) = v;
+  }
 }
 
 // ---------------------------------------------------------------- host
