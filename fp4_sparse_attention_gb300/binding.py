@@ -36,6 +36,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libfp4idx.so")
 
 FP4IDX_OK = 0
+_EWORKSPACE = 3
 FP4IDX_TOPK_SORTED = 0x1
 FP4IDX_TOPK_STREAMING = 0x2
 ERR_PAGE_RANGE = 0x1
@@ -238,7 +239,7 @@ def load_library(path: str = LIB_PATH):
         lib.fp4idx_fork_requests.restype = i32
         lib.fp4idx_copy_pages.argtypes = [ctypes.POINTER(CPageSpan), i32, i64, vp, vp, i32, vp, vp]
         lib.fp4idx_copy_pages.restype = i32
-        lib.fp4idx_pages_workspace_bytes.argtypes = [i64]
+        lib.fp4idx_pages_workspace_bytes.argtypes = [i64, i32, i64]
         lib.fp4idx_pages_workspace_bytes.restype = sz
         lib.fp4idx_release_pages.argtypes = [vp, vp, i32, i32, i32, i64, vp, vp, i64, vp, vp, vp, sz, vp]
         lib.fp4idx_release_pages.restype = i32
@@ -854,42 +855,43 @@ def fp4idx_shared_prefix_attention(shared: DeviceSharedAttention, stream=None):
     return shared.out, shared.lse
 
 
-def _lists(named, device, dim=1):
-    """Contiguous int32 tensors of one number of dimensions on the current device, or a ValueError."""
-    for name, x in named:
-        if x is not None and (x.dtype != torch.int32 or x.dim() != dim or not x.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous {dim}-D int32 tensor")
-    for _, x in named:
-        if x is not None and (x.get_device() != device or device < 0):  # -1: host
-            raise ValueError(_ONE_DEVICE)
-    _on_current(device)
-
-
 def _on_current(device):
     """The library launches on the current device: another one's addresses mean nothing there."""
     if device != (torch.cuda.current_device() if _raw_device is None else _raw_device()):
         raise ValueError("the tensors must be on the current CUDA device")
 
 
-def _table(table, reqs, name="block_table"):
+def _list(x, name, device):
+    """Entries of a contiguous 1-D int32 tensor on `device`."""
+    if x.dtype != torch.int32 or x.dim() != 1 or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 1-D int32 tensor")
+    if x.get_device() != device or device < 0:  # -1: host
+        raise ValueError(_ONE_DEVICE)
+    return x.shape[0]
+
+
+def _table(table, reqs, device, name="block_table"):
     """Row width of a table [reqs, width] that may be written to or read up to its rows' ends."""
-    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != reqs or table.shape[1] < 1 or table.stride(1) != 1:
+    if table.dtype != torch.int32 or table.dim() != 2:
         raise ValueError(f"{name} must be int32 [B, stride] with dense rows")
-    if _step(table, 0, table.shape[1]) != table.shape[1]:
+    (rows, width), (step, one) = table.shape, table.stride()
+    if rows != reqs or width < 1 or one != 1:
+        raise ValueError(f"{name} must be int32 [B, stride] with dense rows")
+    if step != width and rows > 1:
         raise ValueError(f"{name} must not be a view of wider rows")
-    return int(table.shape[1])
+    if table.get_device() != device:
+        raise ValueError(_ONE_DEVICE)
+    return width
 
 
-def _outputs(out, named, device):
-    """The tensors of ``out``, judged, or new ones; named: (name, entries)."""
-    if out is None:
-        return [torch.empty((n,), dtype=torch.int32, device=device) for _, n in named]
+def _given(out, *named):
+    """The tensors of ``out``, judged: (name, entries, device)."""
     if len(out) != len(named):
-        raise ValueError("out: " + ", ".join(name for name, _ in named))
-    for x, (name, n) in zip(out, named):
-        if x.dtype != torch.int32 or x.numel() != n or not x.is_contiguous() or x.device != device:
+        raise ValueError("out: " + ", ".join(name for name, _, _ in named))
+    for x, (name, n, device) in zip(out, named):
+        if x.dtype != torch.int32 or x.numel() != n or not x.is_contiguous() or x.get_device() != device:
             raise ValueError(f"out: {name} must be a contiguous int32 tensor of {n} entries on the device of the table")
-    return list(out)
+    return out
 
 
 def fp4idx_fork_requests(parent: torch.Tensor, child: torch.Tensor, cached_len: torch.Tensor, block_table: torch.Tensor,
@@ -900,20 +902,23 @@ def fp4idx_fork_requests(parent: torch.Tensor, child: torch.Tensor, cached_len: 
     Returns (copy_src [N], copy_dst [N], pages_taken [1]): the unfinished pages to copy (fp4idx_copy_pages), -1 for none.
     ``num_pages`` bounds the page ids (default: any); ``out`` may give the three tensors."""
     dev = cached_len.get_device()
-    _lists((("parent", parent), ("child", child), ("cached_len", cached_len), ("free_pages", free_pages), ("fork_len", fork_len)), dev)
-    N, B = parent.shape[0], cached_len.shape[0]
-    if child.shape[0] != N or (fork_len is not None and fork_len.shape[0] != N):
+    B, N, F = _list(cached_len, "cached_len", dev), _list(parent, "parent", dev), _list(free_pages, "free_pages", dev)
+    if _list(child, "child", dev) != N or (fork_len is not None and _list(fork_len, "fork_len", dev) != N):
         raise ValueError("parent, child and fork_len must have one length")
-    width = _table(block_table, B)
-    if block_table.get_device() != dev:
-        raise ValueError(_ONE_DEVICE)
-    src, dst, taken = _outputs(out, (("copy_src", N), ("copy_dst", N), ("pages_taken", 1)), cached_len.device)
+    width = _table(block_table, B, dev)
+    _on_current(dev)
+    if out is None:
+        i32, where = torch.int32, cached_len.device
+        src, dst = torch.empty(N, dtype=i32, device=where), torch.empty(N, dtype=i32, device=where)
+        taken = torch.empty(1, dtype=i32, device=where)
+    else:
+        src, dst, taken = _given(out, ("copy_src", N, dev), ("copy_dst", N, dev), ("pages_taken", 1, dev))
     if num_pages is None:
         num_pages = (2 ** 31 - 1) // page_size if page_size > 0 else 1
     status = load_library().fp4idx_fork_requests(
         parent.data_ptr(), child.data_ptr(), None if fork_len is None else fork_len.data_ptr(), N, B, page_size, num_pages,
-        free_pages.data_ptr(), free_pages.shape[0], cached_len.data_ptr(), block_table.data_ptr(), width, src.data_ptr(),
-        dst.data_ptr(), taken.data_ptr(), _stream(stream))
+        free_pages.data_ptr(), F, cached_len.data_ptr(), block_table.data_ptr(), width, src.data_ptr(), dst.data_ptr(),
+        taken.data_ptr(), _stream(stream))
     if status:
         _check(status, "fp4idx_fork_requests")
     return src, dst, taken
@@ -937,55 +942,65 @@ class DevicePages:
                 raise ValueError(_ONE_DEVICE)
             size = x[0].numel() * x.element_size()
             span.base, span.page_bytes, span.page_stride = x.data_ptr(), size, _step(x, 0, x[0].numel()) * x.element_size()
-        self.spans = spans
+        self.spans, self.index = spans, self.caches[0].get_device()
 
 
 def fp4idx_copy_pages(pages: DevicePages, src: torch.Tensor, dst: torch.Tensor, count: Optional[torch.Tensor] = None,
                       stream=None) -> None:
     """Copy page src[i] to page dst[i] in every cache of ``pages`` (int32 lists; negative entries are skipped).
     ``count`` [1] int32: only that many entries, read on the device."""
-    if not pages.device.type == "cuda":
+    dev = pages.index
+    if dev < 0:
         raise ValueError("the tensors must be on a CUDA device")
-    _lists((("src", src), ("dst", dst), ("count", count)), pages.device.index or 0)
-    if src.shape != dst.shape or (count is not None and count.numel() != 1):
+    n = _list(src, "src", dev)
+    if _list(dst, "dst", dev) != n or (count is not None and _list(count, "count", dev) != 1):
         raise ValueError("src and dst must have one length and count one entry")
+    _on_current(dev)
     status = load_library().fp4idx_copy_pages(pages.spans, len(pages.caches), pages.num_pages, src.data_ptr(), dst.data_ptr(),
-                                              src.shape[0], None if count is None else count.data_ptr(), _stream(stream))
+                                              n, None if count is None else count.data_ptr(), _stream(stream))
     if status:
         _check(status, "fp4idx_copy_pages")
 
 
-def fp4idx_pages_workspace_bytes(num_pages: int) -> int:
-    return int(load_library().fp4idx_pages_workspace_bytes(int(num_pages)))
+def fp4idx_pages_workspace_bytes(num_pages: int, num_reqs: int, table_stride: int) -> int:
+    return int(load_library().fp4idx_pages_workspace_bytes(int(num_pages), int(num_reqs), int(table_stride)))
 
 
-def _pages_workspace(workspace, num_pages, device):
-    if workspace is None:
-        return torch.empty((max(1, fp4idx_pages_workspace_bytes(num_pages)),), dtype=torch.uint8, device=device)
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous, on the device of the table")
-    return workspace
+def _with_workspace(call, workspace, num_pages, num_reqs, width, where, stream):
+    """call(pointer, bytes) with the given workspace, without one where none is needed, or with a new one."""
+    if workspace is not None:
+        if workspace.device != where or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous, on the device of the table")
+        return call(workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    status = call(None, 0)
+    if status != _EWORKSPACE:
+        return status
+    workspace = torch.empty(fp4idx_pages_workspace_bytes(num_pages, num_reqs, width), dtype=torch.uint8, device=where)
+    if stream is not None:
+        workspace.record_stream(stream)  # it is freed on return, perhaps before that stream comes to it
+    return call(workspace.data_ptr(), workspace.numel())
 
 
 def fp4idx_release_pages(requests: Optional[torch.Tensor], cached_len: torch.Tensor, block_table: torch.Tensor, page_size: int,
                          num_pages: int, keep_len: Optional[torch.Tensor] = None, out=None, workspace=None, stream=None):
     """Requests [N] (None: none) keep their first keep_len [N] tokens (default 0; cached_len [B] in place); returns
     (free_pages [num_pages], num_free [1]): the pages that no held entry of block_table [B, stride] names, ascending, -1
-    behind them.  ``out`` may give the two tensors, ``workspace`` fp4idx_pages_workspace_bytes(num_pages) bytes."""
-    dev = cached_len.get_device()
-    _lists((("cached_len", cached_len), ("requests", requests), ("keep_len", keep_len)), dev)
-    B, N = cached_len.shape[0], 0 if requests is None else requests.shape[0]
-    if keep_len is not None and keep_len.shape[0] != N:
+    behind them.  ``out`` may give the two tensors, ``workspace`` fp4idx_pages_workspace_bytes(num_pages, B, stride) bytes."""
+    dev, where = cached_len.get_device(), cached_len.device
+    B, N = _list(cached_len, "cached_len", dev), 0 if requests is None else _list(requests, "requests", dev)
+    if keep_len is not None and _list(keep_len, "keep_len", dev) != N:
         raise ValueError("requests and keep_len must have one length")
-    width = _table(block_table, B)
-    if block_table.get_device() != dev:
-        raise ValueError(_ONE_DEVICE)
-    free, count = _outputs(out, (("free_pages", num_pages), ("num_free", 1)), cached_len.device)
-    workspace = _pages_workspace(workspace, num_pages, cached_len.device)
-    status = load_library().fp4idx_release_pages(
+    width = _table(block_table, B, dev)
+    _on_current(dev)
+    if out is None:
+        free, count = torch.empty(num_pages, dtype=torch.int32, device=where), torch.empty(1, dtype=torch.int32, device=where)
+    else:
+        free, count = _given(out, ("free_pages", num_pages, dev), ("num_free", 1, dev))
+    lib, at = load_library(), _stream(stream)
+    status = _with_workspace(lambda ws, size: lib.fp4idx_release_pages(
         None if N == 0 else requests.data_ptr(), None if keep_len is None else keep_len.data_ptr(), N, B, page_size, num_pages,
-        cached_len.data_ptr(), block_table.data_ptr(), width, free.data_ptr(), count.data_ptr(), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream(stream))
+        cached_len.data_ptr(), block_table.data_ptr(), width, free.data_ptr(), count.data_ptr(), ws, size, at),
+        workspace, num_pages, B, width, where, stream)
     if status:
         _check(status, "fp4idx_release_pages")
     return free, count
@@ -996,24 +1011,28 @@ def fp4idx_compact_pages(cached_len: torch.Tensor, block_table: torch.Tensor, pa
     """Up to max_moves moves of the highest pages in use into the lowest free ones: (new_table, copy_src [max_moves],
     copy_dst [max_moves], num_moves [1], extent [1]).  The rows go to ``out_table`` (default: block_table itself); the
     pages' contents are moved by fp4idx_copy_pages(pages, copy_src, copy_dst, count=num_moves).  ``out`` may give the
-    last four tensors, ``workspace`` fp4idx_pages_workspace_bytes(num_pages) bytes."""
-    dev = cached_len.get_device()
-    _lists((("cached_len", cached_len),), dev)
-    B = cached_len.shape[0]
-    width = _table(block_table, B)
-    to = block_table if out_table is None else out_table
-    new_width = _table(to, B, "out_table")
-    if block_table.get_device() != dev or to.get_device() != dev:
-        raise ValueError(_ONE_DEVICE)
-    if new_width < width:
-        raise ValueError("out_table must be at least as wide as block_table")
-    src, dst, moves, extent = _outputs(out, (("copy_src", max_moves), ("copy_dst", max_moves), ("num_moves", 1), ("extent", 1)),
-                                       cached_len.device)
-    workspace = _pages_workspace(workspace, num_pages, cached_len.device)
-    status = load_library().fp4idx_compact_pages(
+    last four tensors, ``workspace`` fp4idx_pages_workspace_bytes(num_pages, B, stride) bytes."""
+    dev, where = cached_len.get_device(), cached_len.device
+    B = _list(cached_len, "cached_len", dev)
+    width = new_width = _table(block_table, B, dev)
+    to = block_table
+    if out_table is not None:
+        to, new_width = out_table, _table(out_table, B, dev, "out_table")
+        if new_width < width:
+            raise ValueError("out_table must be at least as wide as block_table")
+    _on_current(dev)
+    if out is None:
+        i32 = torch.int32
+        src, dst = torch.empty(max_moves, dtype=i32, device=where), torch.empty(max_moves, dtype=i32, device=where)
+        moves, extent = torch.empty(1, dtype=i32, device=where), torch.empty(1, dtype=i32, device=where)
+    else:
+        src, dst, moves, extent = _given(out, ("copy_src", max_moves, dev), ("copy_dst", max_moves, dev), ("num_moves", 1, dev),
+                                         ("extent", 1, dev))
+    lib, at = load_library(), _stream(stream)
+    status = _with_workspace(lambda ws, size: lib.fp4idx_compact_pages(
         cached_len.data_ptr(), B, page_size, num_pages, block_table.data_ptr(), width, width, to.data_ptr(), new_width, max_moves,
-        src.data_ptr(), dst.data_ptr(), moves.data_ptr(), extent.data_ptr(), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream(stream))
+        src.data_ptr(), dst.data_ptr(), moves.data_ptr(), extent.data_ptr(), ws, size, at),
+        workspace, num_pages, B, width, where, stream)
     if status:
         _check(status, "fp4idx_compact_pages")
     return to, src, dst, moves, extent

@@ -42,6 +42,7 @@ fp4idx_status_t check_pool(int32_t num_reqs, int32_t page_size, int64_t num_page
 }
 
 fp4idx_status_t check_workspace(const void* workspace, size_t bytes, size_t need) {
+  if (need == 0) return FP4IDX_OK;
   if (!workspace || bytes < need)
     FAIL(FP4IDX_EWORKSPACE, "workspace of %zu bytes is smaller than %zu", workspace ? bytes : size_t{0}, need);
   if (!aligned(workspace, 16)) FAIL(FP4IDX_EINVAL, "workspace must be 16-byte aligned");
@@ -209,9 +210,9 @@ fp4idx_status_t fp4idx_copy_pages(const fp4idx_page_span_t* spans, int32_t num_s
   return cuda_status(launch_copy_pages(p, sms, static_cast<cudaStream_t>(stream)), "page copy launch");
 }
 
-size_t fp4idx_pages_workspace_bytes(int64_t num_pages) {
+size_t fp4idx_pages_workspace_bytes(int64_t num_pages, int32_t num_reqs, int64_t table_stride) {
   set_last_error("%s", "");
-  return num_pages < 1 || num_pages > INT32_MAX ? 0 : pool_workspace(num_pages);
+  return num_pages < 1 || num_pages > INT32_MAX || num_reqs < 1 || table_stride < 1 ? 0 : pool_workspace(num_pages, num_reqs, table_stride);
 }
 
 fp4idx_status_t fp4idx_release_pages(const int32_t* requests, const int32_t* keep_len, int32_t num_released,
@@ -227,7 +228,7 @@ fp4idx_status_t fp4idx_release_pages(const int32_t* requests, const int32_t* kee
     return s;
   if (num_released > 0 && (s = check_arrays("requests", requests)) != FP4IDX_OK) return s;
   if (!aligned(keep_len, 4)) FAIL(FP4IDX_EINVAL, "keep_len must be 4-byte aligned");
-  if ((s = check_workspace(workspace, workspace_bytes, pool_workspace(num_pages))) != FP4IDX_OK) return s;
+  if ((s = check_workspace(workspace, workspace_bytes, pool_workspace(num_pages, num_reqs, table_stride))) != FP4IDX_OK) return s;
   int sms = 0;
   uint32_t* err = nullptr;
   if ((s = call_device(&sms, &err)) != FP4IDX_OK) return s;
@@ -258,7 +259,7 @@ fp4idx_status_t fp4idx_compact_pages(const int32_t* cached_len, int32_t num_reqs
                         extent)) != FP4IDX_OK)
     return s;
   if (max_moves > 0 && (s = check_arrays("copy_src and copy_dst", copy_src, copy_dst)) != FP4IDX_OK) return s;
-  if ((s = check_workspace(workspace, workspace_bytes, pool_workspace(num_pages))) != FP4IDX_OK) return s;
+  if ((s = check_workspace(workspace, workspace_bytes, pool_workspace(num_pages, num_reqs, table_stride))) != FP4IDX_OK) return s;
   int sms = 0;
   uint32_t* err = nullptr;
   if ((s = call_device(&sms, &err)) != FP4IDX_OK) return s;

@@ -76,17 +76,28 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkParams p) 
   for (int k = 0; k < kForkWarps; ++k) mine[k] = child[k];
   int parts = 0;  // unfinished pages of forks before i0
   const bool last = i0 + kForkWarps >= p.num_forks;
-  for (int j = tid; j < p.num_forks; j += kForkThreads) {
-    const int32_t from = __ldg(p.parent + j), to = __ldg(p.child + j);
-    const bool valid = from >= 0 && to >= 0 && from < p.num_reqs && to < p.num_reqs;
-    if (!valid) continue;
+  constexpr int kBatch = 4;  // loads of so many forks under way
+  for (int j0 = tid; j0 < p.num_forks; j0 += kBatch * kForkThreads) {
+    int32_t from[kBatch], to[kBatch], len[kBatch];
 #pragma unroll
-    for (int k = 0; k < kForkWarps; ++k)
-      if (from == mine[k] || (to == mine[k] && j < i0 + k)) bad[k] = 1;
-    if (j < i0) {
-      const Fork g = fork_of(p, j);
-      parts += g.part && g.full + 1 <= p.table_stride;
+    for (int x = 0; x < kBatch; ++x) {
+      const int j = j0 + x * kForkThreads;
+      from[x] = j < p.num_forks ? __ldg(p.parent + j) : -1;
+      to[x] = j < p.num_forks ? __ldg(p.child + j) : -1;
+      len[x] = p.fork_len && j < i0 ? max(0, __ldg(p.fork_len + j)) : INT32_MAX;
     }
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) {
+      const int j = j0 + x * kForkThreads;
+      const bool valid = from[x] >= 0 && to[x] >= 0 && from[x] < p.num_reqs && to[x] < p.num_reqs;
+      len[x] = valid && j < i0 ? min(len[x], max(0, p.cached_len[from[x]])) : 0;
+      if (!valid) from[x] = to[x] = -2;
+#pragma unroll
+      for (int k = 0; k < kForkWarps; ++k)
+        if (from[x] == mine[k] || (to[x] == mine[k] && j < i0 + k)) bad[k] = 1;
+    }
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) parts += (len[x] & (p.page_size - 1)) != 0 && (len[x] >> p.page_shift) < p.table_stride;
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) parts += __shfl_xor_sync(0xffffffffu, parts, o);
@@ -114,7 +125,14 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkParams p) 
   if (f.valid && fits && !bad[wid]) {
     const int32_t* from = p.block_table + static_cast<int64_t>(f.parent) * p.table_stride;
     int32_t* to = p.block_table + static_cast<int64_t>(f.child) * p.table_stride;
-    for (int j = lane; j < f.full; j += 32) to[j] = from[j];
+    for (int j = lane; j < f.full; j += 8 * 32) {
+      int32_t page[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) page[k] = j + 32 * k < f.full ? from[j + 32 * k] : 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (j + 32 * k < f.full) to[j + 32 * k] = page[k];
+    }
     if (f.part) {
       if (before < p.num_free) dst = __ldg(p.free_pages + before);
       else err |= kErrLengths;
@@ -175,152 +193,78 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
   }
 }
 
-// ---------------------------------------------------------------- pool
+// ---------------------------------------------------------------- pool, any size
+// One launch clears the bitmap (and cuts the released requests), one marks, one
+// ranks and lists, and for a compaction one rewrites the table.
 constexpr int kPoolThreads = 256, kPoolWarps = kPoolThreads / 32;
+constexpr int kListThreads = 1024, kListWarps = kListThreads / 32;
+constexpr int kEntries = 8;  // table entries that a lane has under way
 
-__device__ __forceinline__ int pool_words(const PoolParams& p) { return static_cast<int>((p.num_pages + 31) >> 5); }
-// Held entries of request b inside its row.
-__device__ __forceinline__ int held_entries(const PoolParams& p, int b, bool* past) {
-  const int len = max(0, p.cached_len[b]);
-  const int64_t held = (static_cast<int64_t>(len) + (1 << p.page_shift) - 1) >> p.page_shift;
-  *past |= held > p.width;
+// Words of the bitmap, by fours.
+__host__ __device__ constexpr int64_t pool_words(int64_t num_pages) { return (num_pages + 127) / 128 * 4; }
+__device__ __forceinline__ int popc4(uint4 v) { return __popc(v.x) + __popc(v.y) + __popc(v.z) + __popc(v.w); }
+// Held entries of a row of `len` tokens, inside the row.
+__device__ __forceinline__ int held_entries(const PoolParams& p, int len, uint32_t* err) {
+  const int64_t held = (static_cast<int64_t>(max(0, len)) + (1 << p.page_shift) - 1) >> p.page_shift;
+  if (held > p.width) *err |= kErrLengths;
   return static_cast<int>(min(held, static_cast<int64_t>(p.width)));
 }
-
-__global__ void __launch_bounds__(kPoolThreads) pool_start_kernel(const PoolParams p) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int at = blockIdx.x * kPoolThreads + threadIdx.x, step = gridDim.x * kPoolThreads;
-  const int words = pool_words(p);
-  for (int w = at; w < words; w += step) p.bitmap[w] = 0;
-  for (int i = at; i < p.num_released; i += step) {
-    const int32_t b = __ldg(p.requests + i);
-    if (b < 0) continue;
-    if (b >= p.num_reqs) {
-      atomicOr(p.err, kErrRequests);
-      continue;
-    }
-    atomicMin(p.cached_len + b, p.keep_len ? max(0, __ldg(p.keep_len + i)) : 0);
+// Marks entries j0, j0 + 32, ... of a row.
+__device__ __forceinline__ void mark_entries(const PoolParams& p, const int32_t* row, int j0, int n, uint32_t* bits, uint32_t* err) {
+  int32_t page[kEntries];
+#pragma unroll
+  for (int x = 0; x < kEntries; ++x) page[x] = j0 + 32 * x < n ? row[j0 + 32 * x] : 0;
+#pragma unroll
+  for (int x = 0; x < kEntries; ++x) {
+    if (j0 + 32 * x >= n) continue;
+    if (page[x] < 0 || page[x] >= p.num_pages) *err |= kErrPageRange;
+    else atomicOr(bits + (page[x] >> 5), 1u << (page[x] & 31));
   }
 }
-
-// A warp marks up to 128 entries of a row.
-__global__ void __launch_bounds__(kPoolThreads) pool_mark_kernel(const PoolParams p) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  bool past = false, range = false;
-  const int parts = (p.width + 127) / 128;
-  const int64_t work = static_cast<int64_t>(p.num_reqs) * parts;
-  for (int64_t w = static_cast<int64_t>(blockIdx.x) * kPoolWarps + wid; w < work;
-       w += static_cast<int64_t>(gridDim.x) * kPoolWarps) {
-    const int b = static_cast<int>(w / parts), j0 = static_cast<int>(w - static_cast<int64_t>(b) * parts) * 128 + lane;
-    const int n = held_entries(p, b, &past);
-    const int32_t* row = p.block_table + b * p.table_stride;
-    int32_t page[4];
+// Entries of a row at their pages' new places; rank(page) = pages in use before it.
+template <class Rank>
+__device__ __forceinline__ void move_entries(const PoolParams& p, const int32_t* row, int32_t* to, int j0, int held, int n, int moves,
+                                             const Rank& rank) {
+  int32_t page[kEntries], move[kEntries];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) page[k] = j0 + 32 * k < n ? __ldg(row + j0 + 32 * k) : INT32_MIN;
+  for (int x = 0; x < kEntries; ++x) page[x] = j0 + 32 * x < p.width ? row[j0 + 32 * x] : -1;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (page[k] == INT32_MIN && j0 + 32 * k >= n) continue;
-      if (page[k] < 0 || page[k] >= p.num_pages) range = true;
-      else atomicOr(p.bitmap + (page[k] >> 5), 1u << (page[k] & 31));
-    }
-  }
-  if (past) atomicOr(p.err, kErrLengths);
-  if (range) atomicOr(p.err, kErrPageRange);
+  for (int x = 0; x < kEntries; ++x)
+    move[x] = j0 + 32 * x < held && page[x] >= n && page[x] < p.num_pages ? n - 1 - rank(page[x]) : moves;
+#pragma unroll
+  for (int x = 0; x < kEntries; ++x)
+    if (move[x] < moves) page[x] = __ldcg(p.copy_dst + move[x]);
+#pragma unroll
+  for (int x = 0; x < kEntries; ++x)
+    if (j0 + 32 * x < p.width) to[j0 + 32 * x] = page[x];
 }
-
-// Sum over the CTA of up to two counts; every thread gets them.
-__device__ __forceinline__ int2 cta_sum(int2 v, int2* part) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-  }
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-  __syncthreads();
-  int2 all = make_int2(0, 0);
-#pragma unroll
-  for (int w = 0; w < kPoolWarps; ++w) {
-    all.x += part[w].x;
-    all.y += part[w].y;
-  }
-  return all;
-}
-
-// The lists.  A CTA owns a run of words; it sums all words for the total and
-// those before its own for its first rank.
+// The lists' share of four words of the bitmap, a lane a page; `rank` pages are
+// in use before them.
 template <bool COMPACT>
-__global__ void __launch_bounds__(kPoolThreads) pool_list_kernel(const PoolParams p) {
-  __shared__ int2 part[kPoolWarps];
-  pdl_wait();
-  pdl_launch_dependents();
-  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  const int words = pool_words(p);
-  const int per = (words + gridDim.x - 1) / gridDim.x;
-  const int w0 = min(words, static_cast<int>(blockIdx.x) * per), w1 = min(words, w0 + per);
-  int2 sum = make_int2(0, 0);  // pages in use: all, before w0
-  for (int w = tid; w < words; w += kPoolThreads) {
-    const int c = __popc(p.bitmap[w]);
-    sum.x += c;
-    sum.y += w < w0 ? c : 0;
-  }
-  sum = cta_sum(sum, part);
-  const int n = sum.x;
-  int moves = 0, movers = 0;
-  if (COMPACT) {
-    int below = 0;  // pages in use below n
-    for (int w = tid; w <= (n >> 5) && w < words; w += kPoolThreads) {
-      const uint32_t bits = p.bitmap[w];
-      below += __popc(w == (n >> 5) ? bits & ((1u << (n & 31)) - 1) : bits);
-    }
-    movers = n - cta_sum(make_int2(below, 0), part).x;
-    moves = min(movers, p.max_moves);
-  }
-  int rank = sum.y;  // pages in use before this warp's words
-  for (int base = w0; base < w1; base += kPoolThreads) {
-    const int w = base + tid;
-    const uint32_t bits = w < w1 ? p.bitmap[w] : 0;
-    int incl = __popc(bits);
+__device__ __forceinline__ void list_words(const PoolParams& p, const uint32_t* bits, int group, int rank, int n, int moves) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    __syncthreads();
-    if (lane == 31) part[wid].x = incl;
-    __syncthreads();
-    int before = rank;
-#pragma unroll
-    for (int k = 0; k < kPoolWarps; ++k) {
-      if (k < wid) before += part[k].x;
-      rank += part[k].x;
-    }
-    before += incl - __popc(bits);
-    if (COMPACT && w < w1) p.rank[w] = before;
-    // a warp's 32 words, one at a time: lane = page of the word
-    const int w_first = base + wid * 32;
-    for (int k = 0; k < 32 && w_first + k < w1; ++k) {
-      const uint32_t word = __shfl_sync(0xffffffffu, bits, k);
-      const int upto = __shfl_sync(0xffffffffu, before, k) + __popc(word & ((1u << lane) - 1));
-      const int64_t page = static_cast<int64_t>(w_first + k) * 32 + lane;
-      const bool used = word >> lane & 1;
-      if (page >= p.num_pages) continue;
-      if (!COMPACT) {
-        if (!used) p.free_pages[page - upto] = static_cast<int32_t>(page);
-      } else if (used && page >= n) {
-        const int m = n - 1 - upto;
-        if (m < moves) p.copy_src[m] = static_cast<int32_t>(page);
-        if (m == moves) p.extent[0] = static_cast<int32_t>(page) + 1;  // the highest one that stays
-      } else if (!used && page < n && page - upto < moves) {
-        p.copy_dst[page - upto] = static_cast<int32_t>(page);
-      }
+  for (int x = 0; x < 4; ++x) {
+    const uint32_t word = bits[4 * group + x];
+    const int64_t page = (static_cast<int64_t>(4) * group + x) * 32 + lane;
+    const int r = rank + __popc(word & ((1u << lane) - 1));
+    rank += __popc(word);
+    if (page >= p.num_pages) continue;
+    const bool used = word >> lane & 1;
+    if (!COMPACT) {
+      if (!used) p.free_pages[page - r] = static_cast<int32_t>(page);
+    } else if (used && page >= n) {
+      const int m = n - 1 - r;
+      if (m < moves) p.copy_src[m] = static_cast<int32_t>(page);
+      if (m == moves) p.extent[0] = static_cast<int32_t>(page) + 1;  // the highest one that stays
+    } else if (!used && page < n && page - r < moves) {
+      p.copy_dst[page - r] = static_cast<int32_t>(page);
     }
   }
-  // what lies behind the lists
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * kPoolThreads + tid, step = static_cast<int64_t>(gridDim.x) * kPoolThreads;
+}
+// What lies behind the lists, and the counts; at, step: this thread of all.
+template <bool COMPACT>
+__device__ __forceinline__ void end_lists(const PoolParams& p, int n, int moves, int movers, int64_t at, int64_t step) {
   if (!COMPACT) {
     for (int64_t i = p.num_pages - n + at; i < p.num_pages; i += step) p.free_pages[i] = -1;
     if (at == 0) p.num_free[0] = static_cast<int32_t>(p.num_pages - n);
@@ -333,58 +277,323 @@ __global__ void __launch_bounds__(kPoolThreads) pool_list_kernel(const PoolParam
   }
 }
 
+__global__ void __launch_bounds__(kPoolThreads) pool_start_kernel(const PoolParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int at = blockIdx.x * kPoolThreads + threadIdx.x, step = gridDim.x * kPoolThreads;
+  const int groups = static_cast<int>(pool_words(p.num_pages) / 4);
+  for (int g = at; g < groups; g += step) reinterpret_cast<uint4*>(p.bitmap)[g] = make_uint4(0, 0, 0, 0);
+  for (int i = at; i < p.num_released; i += step) {
+    const int32_t b = __ldg(p.requests + i);
+    if (b < 0) continue;
+    if (b >= p.num_reqs) {
+      atomicOr(p.err, kErrRequests);
+      continue;
+    }
+    atomicMin(p.cached_len + b, p.keep_len ? max(0, __ldg(p.keep_len + i)) : 0);
+  }
+}
+
+// A warp marks, or rewrites, up to 256 entries of a row.
+__global__ void __launch_bounds__(kPoolThreads) pool_mark_kernel(const PoolParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  uint32_t err = 0;
+  const int parts = (p.width + 32 * kEntries - 1) / (32 * kEntries);
+  const int64_t work = static_cast<int64_t>(p.num_reqs) * parts;
+  for (int64_t w = static_cast<int64_t>(blockIdx.x) * kPoolWarps + wid; w < work;
+       w += static_cast<int64_t>(gridDim.x) * kPoolWarps) {
+    const int b = static_cast<int>(w / parts), j0 = static_cast<int>(w - static_cast<int64_t>(b) * parts) * 32 * kEntries + lane;
+    mark_entries(p, p.block_table + b * p.table_stride, j0, held_entries(p, p.cached_len[b], &err), p.bitmap, &err);
+  }
+  if (err) atomicOr(p.err, err);
+}
+
+// Sum of two counts over the CTA.
+__device__ __forceinline__ int2 list_sum(int2 v, int2* part) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+  }
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  int2 all = part[threadIdx.x & 31];
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    all.x += __shfl_xor_sync(0xffffffffu, all.x, o);
+    all.y += __shfl_xor_sync(0xffffffffu, all.y, o);
+  }
+  return all;
+}
+
+// The lists.  A CTA owns a run of words; it sums all words for the total and
+// those before its own for its first rank.
+template <bool COMPACT>
+__global__ void __launch_bounds__(kListThreads) pool_list_kernel(const PoolParams p) {
+  __shared__ int2 part[kListWarps];
+  __shared__ int ranks[kListThreads];
+  static_assert(kListWarps == 32, "a lane a warp");
+  pdl_wait();
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int groups = static_cast<int>(pool_words(p.num_pages) / 4);
+  const int per = (groups + gridDim.x - 1) / gridDim.x;
+  const int g0 = min(groups, static_cast<int>(blockIdx.x) * per), g1 = min(groups, g0 + per);
+  const uint4* fours = reinterpret_cast<const uint4*>(p.bitmap);
+  int2 sum = make_int2(0, 0);  // pages in use: all, before g0
+#pragma unroll 4
+  for (int g = tid; g < groups; g += kListThreads) {
+    const int c = popc4(fours[g]);
+    sum.x += c;
+    sum.y += g < g0 ? c : 0;
+  }
+  sum = list_sum(sum, part);
+  const int n = sum.x;
+  int moves = 0, movers = 0;
+  if (COMPACT) {
+    int below = 0;  // pages in use below n
+#pragma unroll 4
+    for (int w = tid; w < (n >> 5); w += kListThreads) below += __popc(p.bitmap[w]);
+    if (tid == 0 && n < p.num_pages) below += __popc(p.bitmap[n >> 5] & ((1u << (n & 31)) - 1));
+    movers = n - list_sum(make_int2(below, 0), part).x;
+    moves = min(movers, p.max_moves);
+  }
+  int rank = sum.y;  // pages in use before the next groups
+  for (int base = g0; base < g1; base += kListThreads) {
+    const int g = base + tid, mine = g < g1 ? popc4(fours[g]) : 0;
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    __syncthreads();
+    if (lane == 31) part[wid].x = incl;
+    __syncthreads();
+    int before = part[lane].x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += y;
+    }
+    const int all = __shfl_sync(0xffffffffu, before, 31);
+    before = wid > 0 ? __shfl_sync(0xffffffffu, before, wid - 1) : 0;
+    ranks[tid] = rank + before + incl - mine;
+    if (COMPACT && g < g1) p.rank[g] = ranks[tid];
+    __syncthreads();
+    for (int x = wid; x < kListThreads && base + x < g1; x += kListWarps) list_words<COMPACT>(p, p.bitmap, base + x, ranks[x], n, moves);
+    rank += all;
+  }
+  end_lists<COMPACT>(p, n, moves, movers, static_cast<int64_t>(blockIdx.x) * kListThreads + tid, static_cast<int64_t>(gridDim.x) * kListThreads);
+}
+
 // Table rows with the moved pages' new places; n comes with the moves: the
 // pages at or above n are the ones whose rank from the top is below `moves`.
 __global__ void __launch_bounds__(kPoolThreads) pool_rewrite_kernel(const PoolParams p) {
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  const int words = pool_words(p), moves = p.num_moves[0];
-  const int n = p.rank[words - 1] + __popc(p.bitmap[words - 1]);
-  const int parts = (p.width + 127) / 128;
+  const int groups = static_cast<int>(pool_words(p.num_pages) / 4), moves = p.num_moves[0];
+  const uint4* fours = reinterpret_cast<const uint4*>(p.bitmap);
+  const int n = p.rank[groups - 1] + popc4(fours[groups - 1]);
+  const auto rank = [&](int page) {
+    const int w = page >> 5, x = w & 3;
+    const uint4 v = fours[w >> 2];
+    const uint32_t mine = x == 0 ? v.x : x == 1 ? v.y : x == 2 ? v.z : v.w;
+    return p.rank[w >> 2] + (x > 0 ? __popc(v.x) : 0) + (x > 1 ? __popc(v.y) : 0) + (x > 2 ? __popc(v.z) : 0) +
+           __popc(mine & ((1u << (page & 31)) - 1));
+  };
+  uint32_t err = 0;  // (the marks have reported it)
+  const int parts = (p.width + 32 * kEntries - 1) / (32 * kEntries);
   const int64_t work = static_cast<int64_t>(p.num_reqs) * parts;
   for (int64_t w = static_cast<int64_t>(blockIdx.x) * kPoolWarps + wid; w < work;
        w += static_cast<int64_t>(gridDim.x) * kPoolWarps) {
-    const int b = static_cast<int>(w / parts), j0 = static_cast<int>(w - static_cast<int64_t>(b) * parts) * 128 + lane;
-    bool past = false;
-    const int held = held_entries(p, b, &past);
-    const int32_t* row = p.block_table + b * p.table_stride;
-    int32_t* to = p.new_table + b * p.new_stride;
-    int32_t page[4];
+    const int b = static_cast<int>(w / parts), j0 = static_cast<int>(w - static_cast<int64_t>(b) * parts) * 32 * kEntries + lane;
+    move_entries(p, p.block_table + b * p.table_stride, p.new_table + b * p.new_stride, j0, held_entries(p, p.cached_len[b], &err), n, moves, rank);
+  }
+}
+
+// ---------------------------------------------------------------- pool, one cluster
+// The same in one launch, for small pools: a cluster of CTAs marks its requests'
+// entries, each in a bitmap of its own in shared memory; CTA r ORs everyone's
+// slice r and hands it to everyone; then each CTA has the whole bitmap, ranks
+// it, lists its slice and rewrites its requests' rows.  No workspace, nothing to
+// clear in memory, two or three cluster barriers.
+constexpr int kClusterThreads = 1024, kClusterWarps = kClusterThreads / 32;
+// What one cluster takes: more is faster on all SMs, in more launches.  (256
+// requests of up to 256 pages: release 7.1 us, 8.0 in three launches; compaction
+// 15 us, 17 in four.  256 of up to 512: 8.7, 8.4; 17, 16.)
+constexpr int kClusterPages = 1 << 17;
+constexpr int kClusterRuns = 512;  // runs of 256 entries of a row
+constexpr int kClusterCtas = 8;    // (four: 5.6 and 11.8 us for 64 requests of up to 256 pages, eight 5.3 and 10.1)
+
+struct ClusterSmem {
+  int2 part[kClusterWarps];
+};
+static_assert(sizeof(ClusterSmem) % 16 == 0, "the bitmap behind it is read by 16 bytes");
+// bitmap, pages in use before each four words of it, lengths of the CTA's requests
+size_t cluster_smem(int64_t num_pages, int reqs_of_cta) {
+  return sizeof(ClusterSmem) + static_cast<size_t>(pool_words(num_pages)) * 5 + 4 * static_cast<size_t>(reqs_of_cta);
+}
+__device__ __forceinline__ uint4 dsmem_ld_v4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void dsmem_st_v4(uint32_t a, uint4 v) {
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+template <bool COMPACT>
+__global__ void __launch_bounds__(kClusterThreads, 1) pool_cluster_kernel(const PoolParams p) {
+  constexpr int ctas = kClusterCtas;
+  extern __shared__ __align__(16) uint8_t raw[];
+  ClusterSmem& sm = *reinterpret_cast<ClusterSmem*>(raw);
+  const int words = static_cast<int>(pool_words(p.num_pages)), groups = words / 4;
+  uint32_t* bits = reinterpret_cast<uint32_t*>(raw + sizeof(ClusterSmem));
+  uint32_t* ranks = bits + words;
+  int32_t* len = reinterpret_cast<int32_t*>(ranks + groups);
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int me = blockIdx.x;  // one cluster: the rank
+  const int reqs = (p.num_reqs - me + ctas - 1) / ctas;  // requests me, me + ctas, ...
+  for (int g = tid; g < groups; g += kClusterThreads) reinterpret_cast<uint4*>(bits)[g] = make_uint4(0, 0, 0, 0);
+  pdl_wait();
+  pdl_launch_dependents();
+  uint32_t err = 0;
+  // lengths, cut where a request is released
+  for (int k = tid; k < reqs; k += kClusterThreads) len[k] = p.cached_len[me + k * ctas];
+  __syncthreads();
+  for (int i = tid; i < p.num_released; i += kClusterThreads) {
+    const int32_t b = __ldg(p.requests + i);
+    if (b >= p.num_reqs) err |= kErrRequests;
+    else if (b >= 0 && b % ctas == me) atomicMin(len + b / ctas, p.keep_len ? max(0, __ldg(p.keep_len + i)) : 0);
+  }
+  __syncthreads();
+  if (p.num_released > 0)
+    for (int k = tid; k < reqs; k += kClusterThreads) p.cached_len[me + k * ctas] = len[k];
+  // marks: a warp takes up to 256 entries of a row
+  const int parts = (p.width + 32 * kEntries - 1) / (32 * kEntries);
+  for (int w = wid; w < reqs * parts; w += kClusterWarps) {
+    const int k = w / parts, j0 = (w - k * parts) * 32 * kEntries + lane;
+    mark_entries(p, p.block_table + static_cast<int64_t>(me + k * ctas) * p.table_stride, j0, held_entries(p, len[k], &err), bits, &err);
+  }
+  __syncwarp();
+  cluster_sync();
+  // everyone's slice of mine, to everyone
+  const int slice = (groups + ctas - 1) / ctas, g0 = min(groups, me * slice), g1 = min(groups, g0 + slice);
+  for (int g = g0 + tid; g < g1; g += kClusterThreads) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    for (int c = 0; c < ctas; ++c) {
+      const uint4 x = dsmem_ld_v4(dsmem_addr(bits + 4 * g, c));
+      v = make_uint4(v.x | x.x, v.y | x.y, v.z | x.z, v.w | x.w);
+    }
+    for (int c = 0; c < ctas; ++c) dsmem_st_v4(dsmem_addr(bits + 4 * g, c), v);
+  }
+  __syncwarp();
+  cluster_sync();
+  // ranks of all groups of four words: a thread has a run of them
+  int n = 0;
+  {
+    const int per = (groups + kClusterThreads - 1) / kClusterThreads, first = min(groups, tid * per), last = min(groups, first + per);
+    int mine = 0;
+    for (int g = first; g < last; ++g) {
+      mine += popc4(reinterpret_cast<const uint4*>(bits)[g]);
+    }
+    int incl = mine;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) page[k] = j0 + 32 * k < p.width ? row[j0 + 32 * k] : -1;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) sm.part[wid].x = incl;
+    __syncthreads();
+    if (wid == 0) {
+      int all = sm.part[lane].x;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int j = j0 + 32 * k;
-      if (j >= p.width) continue;
-      if (j < held && page[k] >= n && page[k] < p.num_pages) {
-        const int word = page[k] >> 5;
-        const int m = n - 1 - (p.rank[word] + __popc(p.bitmap[word] & ((1u << (page[k] & 31)) - 1)));
-        if (m < moves) page[k] = p.copy_dst[m];
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, all, o);
+        if (lane >= o) all += y;
       }
-      to[j] = page[k];
+      sm.part[lane].y = all;
+    }
+    __syncthreads();
+    n = sm.part[kClusterWarps - 1].y;
+    int before = incl - mine + (wid > 0 ? sm.part[wid - 1].y : 0);
+    for (int g = first; g < last; ++g) {
+      ranks[g] = before;
+      before += popc4(reinterpret_cast<const uint4*>(bits)[g]);
+    }
+    __syncthreads();
+  }
+  const auto rank_of = [&](int64_t page) {  // pages in use before it
+    const int w = static_cast<int>(page >> 5), g = w >> 2;
+    int r = ranks[g];
+    for (int x = 4 * g; x < w; ++x) r += __popc(bits[x]);
+    return r + __popc(bits[w] & ((1u << (page & 31)) - 1));
+  };
+  const int below = n < p.num_pages ? rank_of(n) : n, movers = n - below, moves = COMPACT ? min(movers, p.max_moves) : 0;
+  for (int g = g0 + wid; g < g1; g += kClusterWarps) list_words<COMPACT>(p, bits, g, ranks[g], n, moves);
+  end_lists<COMPACT>(p, n, moves, movers, static_cast<int64_t>(me) * kClusterThreads + tid, static_cast<int64_t>(ctas) * kClusterThreads);
+  if (COMPACT) {
+    __syncwarp();
+    cluster_sync();  // the targets are written
+    for (int w = wid; w < reqs * parts; w += kClusterWarps) {
+      const int k = w / parts, j0 = (w - k * parts) * 32 * kEntries + lane;
+      const int64_t b = me + static_cast<int64_t>(k) * ctas;
+      move_entries(p, p.block_table + b * p.table_stride, p.new_table + b * p.new_stride, j0, held_entries(p, len[k], &err), n, moves, rank_of);
     }
   }
+  if (err) atomicOr(p.err, err);
+}
+
+bool in_one_cluster(const PoolParams& p) {
+  return p.num_pages <= kClusterPages && static_cast<int64_t>(p.num_reqs) * ((p.width + 32 * kEntries - 1) / (32 * kEntries)) <= kClusterRuns;
+}
+
+template <bool COMPACT>
+cudaError_t launch_cluster(const PoolParams& p, cudaStream_t stream) {
+  constexpr int ctas = kClusterCtas;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kClusterThreads);
+  cfg.dynamicSmemBytes = cluster_smem(p.num_pages, (p.num_reqs + ctas - 1) / ctas);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, pool_cluster_kernel<COMPACT>, p);
 }
 
 int64_t round16(int64_t n) { return (n + 15) & ~int64_t{15}; }
 
-cudaError_t mark(PoolParams* p, int sms, void* workspace, cudaStream_t stream) {
-  const int64_t words = (p->num_pages + 31) / 32;
-  p->bitmap = static_cast<uint32_t*>(workspace);
-  p->rank = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + round16(words * 4));
-  const int64_t most = 8 * static_cast<int64_t>(sms);
-  const int64_t first = std::max<int64_t>(1, (std::max<int64_t>(words, p->num_released) + kPoolThreads - 1) / kPoolThreads);
-  cudaError_t e = launch_dependent(pool_start_kernel, dim3(static_cast<unsigned>(std::min(first, most))), kPoolThreads, stream, *p);
-  if (e != cudaSuccess) return e;
-  const int64_t parts = static_cast<int64_t>(p->num_reqs) * ((p->width + 127) / 128);
-  const int64_t ctas = std::min(most, (parts + kPoolWarps - 1) / kPoolWarps);
-  return launch_dependent(pool_mark_kernel, dim3(static_cast<unsigned>(ctas)), kPoolThreads, stream, *p);
+unsigned entry_ctas(const PoolParams& p, int sms) {
+  const int64_t parts = static_cast<int64_t>(p.num_reqs) * ((p.width + 32 * kEntries - 1) / (32 * kEntries));
+  return static_cast<unsigned>(std::min<int64_t>(8 * static_cast<int64_t>(sms), (parts + kPoolWarps - 1) / kPoolWarps));
 }
 
+cudaError_t mark(PoolParams* p, int sms, void* workspace, cudaStream_t stream) {
+  const int64_t words = pool_words(p->num_pages);
+  p->bitmap = static_cast<uint32_t*>(workspace);
+  p->rank = reinterpret_cast<int32_t*>(p->bitmap + words);
+  const int64_t most = 8 * static_cast<int64_t>(sms);
+  const int64_t first = std::max<int64_t>(1, (std::max<int64_t>(words / 4, p->num_released) + kPoolThreads - 1) / kPoolThreads);
+  cudaError_t e = launch_dependent(pool_start_kernel, dim3(static_cast<unsigned>(std::min(first, most))), kPoolThreads, stream, *p);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(pool_mark_kernel, dim3(entry_ctas(*p, sms)), kPoolThreads, stream, *p);
+}
+
+// A CTA sums the whole bitmap: one for each 256 groups of four words at most.
 unsigned list_ctas(const PoolParams& p, int sms) {
-  const int64_t words = (p.num_pages + 31) / 32;
-  return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(sms, words / 64)));
+  return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(sms, pool_words(p.num_pages) / 4 / 64)));
 }
 
 }  // namespace
@@ -405,23 +614,27 @@ cudaError_t launch_copy_pages(CopyParams p, int sms, cudaStream_t stream) {
   return launch_dependent(copy_kernel, dim3(static_cast<unsigned>(ctas)), kCopyThreads, stream, p);
 }
 
-size_t pool_workspace(int64_t num_pages) {
-  return static_cast<size_t>(2 * round16((num_pages + 31) / 32 * 4));
+size_t pool_workspace(int64_t num_pages, int32_t num_reqs, int64_t table_stride) {
+  PoolParams p = {};
+  p.num_pages = num_pages;
+  p.num_reqs = num_reqs;
+  p.width = static_cast<int32_t>(std::min<int64_t>(table_stride, INT32_MAX));
+  return in_one_cluster(p) ? 0 : static_cast<size_t>(round16(5 * pool_words(num_pages)));
 }
 
 cudaError_t launch_release(PoolParams p, int sms, void* workspace, cudaStream_t stream) {
+  if (in_one_cluster(p)) return launch_cluster<false>(p, stream);
   cudaError_t e = mark(&p, sms, workspace, stream);
   if (e != cudaSuccess) return e;
-  return launch_dependent(pool_list_kernel<false>, dim3(list_ctas(p, sms)), kPoolThreads, stream, p);
+  return launch_dependent(pool_list_kernel<false>, dim3(list_ctas(p, sms)), kListThreads, stream, p);
 }
 
 cudaError_t launch_compact(PoolParams p, int sms, void* workspace, cudaStream_t stream) {
+  if (in_one_cluster(p)) return launch_cluster<true>(p, stream);
   cudaError_t e = mark(&p, sms, workspace, stream);
   if (e != cudaSuccess) return e;
-  if ((e = launch_dependent(pool_list_kernel<true>, dim3(list_ctas(p, sms)), kPoolThreads, stream, p)) != cudaSuccess) return e;
-  const int64_t parts = static_cast<int64_t>(p.num_reqs) * ((p.width + 127) / 128);
-  const int64_t ctas = std::min<int64_t>(8 * sms, (parts + kPoolWarps - 1) / kPoolWarps);
-  return launch_dependent(pool_rewrite_kernel, dim3(static_cast<unsigned>(ctas)), kPoolThreads, stream, p);
+  if ((e = launch_dependent(pool_list_kernel<true>, dim3(list_ctas(p, sms)), kListThreads, stream, p)) != cudaSuccess) return e;
+  return launch_dependent(pool_rewrite_kernel, dim3(entry_ctas(p, sms)), kPoolThreads, stream, p);
 }
 
 }  // namespace fp4idx

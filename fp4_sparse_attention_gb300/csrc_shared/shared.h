@@ -96,7 +96,7 @@ cudaError_t launch_shared(SharedParams p, const AttnMaps& maps, int dtype, void*
 
 cudaError_t launch_fork(const ForkParams& p, cudaStream_t stream);
 cudaError_t launch_copy_pages(CopyParams p, int sms, cudaStream_t stream);
-size_t pool_workspace(int64_t num_pages);
+size_t pool_workspace(int64_t num_pages, int32_t num_reqs, int64_t table_stride);  // 0: none needed
 cudaError_t launch_release(PoolParams p, int sms, void* workspace, cudaStream_t stream);
 cudaError_t launch_compact(PoolParams p, int sms, void* workspace, cudaStream_t stream);
 

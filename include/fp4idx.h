@@ -701,11 +701,11 @@ fp4idx_status_t fp4idx_copy_pages(const fp4idx_page_span_t* spans, int32_t num_s
  * (num_released 0: the list alone.)  Table entries are not written.  A held
  * entry outside [0, num_pages), or behind table_stride, names no page and sets
  * FP4IDX_ERR_PAGE_RANGE (FP4IDX_ERR_LENGTHS).
- * Workspace: fp4idx_pages_workspace_bytes(num_pages), 16-byte aligned,
- * uninitialised, shared with fp4idx_compact_pages.  Graph-capturable, no
- * synchronisation.  Supported: page_size 64 or 128, num_pages * page_size < 2^31.
+ * Workspace: fp4idx_pages_workspace_bytes(), 16-byte aligned, uninitialised, as
+ * for fp4idx_compact_pages; 0 bytes (NULL allowed) for small tables and pools,
+ * which take one launch.  Graph-capturable, no synchronisation.  Supported: page_size 64 or 128, num_pages * page_size < 2^31.
  */
-size_t fp4idx_pages_workspace_bytes(int64_t num_pages);
+size_t fp4idx_pages_workspace_bytes(int64_t num_pages, int32_t num_reqs, int64_t table_stride);
 fp4idx_status_t fp4idx_release_pages(const int32_t* requests, const int32_t* keep_len, int32_t num_released,
                                      int32_t num_reqs, int32_t page_size, int64_t num_pages, int32_t* cached_len,
                                      const int32_t* block_table, int64_t table_stride, int32_t* free_pages,

@@ -165,7 +165,7 @@ def test_copies_beyond_two_to_the_31_bytes():
 def check_release(requests, keep, cached, table, page, num_pages):
     want = S.release(requests, keep, cached, table, page, num_pages)
     d_cached, d_table = i32(cached), i32(table)
-    ws = torch.full((B.fp4idx_pages_workspace_bytes(num_pages),), 0xA5, dtype=torch.uint8, device="cuda")
+    ws = torch.full((B.fp4idx_pages_workspace_bytes(num_pages, len(cached), len(table[0])),), 0xA5, dtype=torch.uint8, device="cuda")
     B.fp4idx_get_error(clear=True)
     for _ in range(2):
         free, count = B.fp4idx_release_pages(i32(requests).view(-1) if requests is not None else None, d_cached, d_table, page, num_pages,
@@ -209,7 +209,7 @@ def check_compact(cached, table, page, num_pages, max_moves, in_place=False):
     want = S.compact(cached, table, page, num_pages, max_moves)
     d_cached, d_table = i32(cached), i32(table)
     width = d_table.shape[1]
-    ws = torch.full((B.fp4idx_pages_workspace_bytes(num_pages),), 0xA5, dtype=torch.uint8, device="cuda")
+    ws = torch.full((B.fp4idx_pages_workspace_bytes(num_pages, len(cached), len(table[0])),), 0xA5, dtype=torch.uint8, device="cuda")
     out = [torch.full((max_moves,), 5, dtype=torch.int32, device="cuda") for _ in range(2)] + [i32([-3]), i32([-3])]
     to = None if in_place else torch.full((len(cached), width + 2), -77, dtype=torch.int32, device="cuda")
     B.fp4idx_get_error(clear=True)
@@ -264,6 +264,45 @@ def test_compactions_of_broken_tables():
     assert check_compact([0, -7, 0], table, 64, 9, 10)[4] == 0
 
 
+# ---------------------------------------------------------------- pools and tables past the one-launch kernel
+MANY = 1310720  # pages: more than it takes
+
+
+def many_requests(reqs, num_pages, longest, seed):
+    """Lengths and tables of many short requests (a list for the plain form)."""
+    g = torch.Generator().manual_seed(seed)
+    cached = torch.randint(0, longest * 64 + 1, (reqs,), generator=g).tolist()
+    return cached, torch.randint(0, num_pages, (reqs, longest), generator=g).tolist()
+
+
+@pytest.mark.parametrize("reqs,num_pages", [(50, 150000), (50, MANY), (50, 3000000), (32768, 90000), (40000, 200000), (3, 250000)])
+def test_large_pools_and_many_requests(reqs, num_pages):
+    cached, table = many_requests(reqs, num_pages, 5 if reqs > 1000 else 1500 if reqs > 3 else 3000, reqs)
+    gone = [(7 * i) % (reqs + 1) - 1 for i in range(0, reqs, 3)]  # with -1, none twice
+    check_release(gone, [i % 90 for i in range(len(gone))], cached, table, 64, num_pages)
+    for moves in (1000, num_pages // 2):
+        want = check_compact(cached, table, 64, num_pages, moves)
+    assert want[4] == len(S.in_use(cached, table, 64, num_pages)[0])
+
+
+def test_workspace_is_the_callers_or_made_for_the_call():
+    cached, table = many_requests(20, MANY + 100, 50, 3)
+    want = S.release([1], None, cached, table, 64, MANY + 100)
+    stream = torch.cuda.Stream()
+    d_cached, d_table, one = i32(cached), i32(table), i32([1])
+    torch.cuda.synchronize()
+    for s in (None, stream):
+        free, count = B.fp4idx_release_pages(one, d_cached, d_table, 64, MANY + 100, stream=s)
+        torch.cuda.synchronize()
+        assert free.tolist() == want[1] and count.tolist() == [want[2]]
+    short = torch.empty(B.fp4idx_pages_workspace_bytes(MANY + 100, 20, 50) - 1, dtype=torch.uint8, device="cuda")
+    for f in (lambda: B.fp4idx_release_pages(one, d_cached, d_table, 64, MANY + 100, workspace=short),
+              lambda: B.fp4idx_compact_pages(d_cached, d_table, 64, MANY + 100, 5, workspace=short)):
+        with pytest.raises(B.Fp4idxError) as e:
+            f()
+        assert e.value.status == 3
+
+
 # ---------------------------------------------------------------- streams and graphs
 def test_graph_replays_see_new_lengths_and_another_stream():
     rng = random.Random(9)
@@ -271,15 +310,14 @@ def test_graph_replays_see_new_lengths_and_another_stream():
     d_cached, d_table = i32(cached), i32(table)
     gone, keep = i32([3, 4, 5]), i32([0, 10, 20])
     moved = torch.empty_like(d_table)
-    ws = [torch.empty((B.fp4idx_pages_workspace_bytes(2000),), dtype=torch.uint8, device="cuda") for _ in range(1)][0]
     free = [torch.empty((2000,), dtype=torch.int32, device="cuda"), i32([0])]
     moves = [i32([0] * 64), i32([0] * 64), i32([0]), i32([0])]
     stream = torch.cuda.Stream()
     stream.wait_stream(torch.cuda.current_stream())
 
     def step(s=None):
-        B.fp4idx_release_pages(gone, d_cached, d_table, 64, 2000, keep_len=keep, out=free, workspace=ws, stream=s)
-        B.fp4idx_compact_pages(d_cached, d_table, 64, 2000, 64, out_table=moved, out=moves, workspace=ws, stream=s)
+        B.fp4idx_release_pages(gone, d_cached, d_table, 64, 2000, keep_len=keep, out=free, stream=s)
+        B.fp4idx_compact_pages(d_cached, d_table, 64, 2000, 64, out_table=moved, out=moves, stream=s)
 
     def right(lens):
         want = S.release(gone.tolist(), keep.tolist(), lens, table, 64, 2000)
