@@ -127,9 +127,17 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   if (i >= pl.blocks) return;
   const int g = i / pl.blocks_per_group;
   const int2 reqs = group_requests(sp, g);
+  const int n_reqs = reqs.y - reqs.x;
+  // (loads that need nothing from each other stand together: a block's plan is a
+  // chain of five of them)
+  const int step = (n_reqs + 31) >> 5;
+  const int probe = lane * step < n_reqs ? __ldg(p.cu_seqlens_q + reqs.x + lane * step) : INT32_MAX;
+  const int first_row = __ldg(p.cu_seqlens_q + reqs.x), end_row = __ldg(p.cu_seqlens_q + reqs.y);
+  const int prefix_len = __ldg(sp.prefix_len + g);
+  const int first_keys = reqs.x < sp.a.num_seqs ? __ldg(p.cu_seqlens_k + reqs.x + 1) - __ldg(p.cu_seqlens_k + reqs.x) : 0;
   Block blk = {};
-  blk.row0 = max(0, __ldg(p.cu_seqlens_q + reqs.x));
-  const int rows = min(max(min(__ldg(p.cu_seqlens_q + reqs.y), p.num_rows) - blk.row0, 0), sp.max_group_rows);
+  blk.row0 = max(0, first_row);
+  const int rows = min(max(min(end_row, p.num_rows) - blk.row0, 0), sp.max_group_rows);
   const int64_t pair0 = static_cast<int64_t>(i - g * pl.blocks_per_group) * kBlockPairs;
   const int64_t pairs = min(static_cast<int64_t>(rows) * p.group - pair0, static_cast<int64_t>(kBlockPairs));
   if (pairs <= 0) {
@@ -142,23 +150,22 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   blk.pair0 = static_cast<int>(pair0);
   blk.pairs = static_cast<int>(pairs);
   const int r0 = blk.row0 + group_div(p, pair0), r1 = blk.row0 + group_div(p, pair0 + pairs - 1) + 1;  // its rows
-  // the request of a row, 32 tests at a time
-  const auto request_of = [&](int row) {
-    int lo = reqs.x, n = reqs.y - reqs.x;
-    while (n > 1) {
-      const int step = (n + 31) >> 5, at = lane * step;
-      const uint32_t before = __ballot_sync(0xffffffffu, at < n && __ldg(p.cu_seqlens_q + lo + (at < n ? at : 0)) <= row);
-      const int skip = max(0, __popc(before) - 1) * step;
-      lo += skip;
-      n = min(step, n - skip);
-    }
-    return lo;
-  };
-  const int a0 = request_of(r0), a1 = request_of(r1 - 1);
+  // the requests of its first and last row: the last ones that begin at or
+  // before it, 32 tests at a time
+  int a0 = reqs.x + max(0, __popc(__ballot_sync(0xffffffffu, probe <= r0)) - 1) * step;
+  int a1 = reqs.x + max(0, __popc(__ballot_sync(0xffffffffu, probe <= r1 - 1)) - 1) * step;
+  for (int n = step; n > 1;) {
+    const int by = (n + 31) >> 5, at = lane * by;
+    const int x0 = at < n && a0 + at < reqs.y ? __ldg(p.cu_seqlens_q + a0 + at) : INT32_MAX;
+    const int x1 = at < n && a1 + at < reqs.y ? __ldg(p.cu_seqlens_q + a1 + at) : INT32_MAX;
+    a0 += max(0, __popc(__ballot_sync(0xffffffffu, x0 <= r0)) - 1) * by;
+    a1 += max(0, __popc(__ballot_sync(0xffffffffu, x1 <= r1 - 1)) - 1) * by;
+    n = by;
+  }
   const auto key_count = [&](int a) {
     return min(max(0, __ldg(p.cu_seqlens_k + a + 1) - __ldg(p.cu_seqlens_k + a)), p.max_seqlen_k);
   };
-  const int prefix = max(0, min(__ldg(sp.prefix_len + g), key_count(reqs.x)));
+  const int prefix = max(0, min(prefix_len, min(max(0, first_keys), p.max_seqlen_k)));
   // (a block has 1 + its requests spans at most, and the next block's first
   // request is not before this one's last)
   blk.span0 = 2 * i + a0;
@@ -878,9 +885,11 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
               bar_sync(pair_bar, 64);
               const float most = fmaxf(mine_top, ctl.row[acc][half ^ 1][r]);
               const float f = most > m ? ex2(m - most) : 1.0f;
+              // a row without a reference has weights and an output of zero so far
+              const bool grown = __any_sync(0xffffffffu, most > m && m != -INFINITY);
               if (most > m) m = most;
               l *= f;
-              if (steps_of_seg > 0) {  // (the score product came behind the last value product)
+              if (grown && steps_of_seg > 0) {  // (the score product came behind the last value product)
 #pragma unroll 1
                 for (int c = 0; c < kHalf; c += 16) {
                   uint32_t o[16];
