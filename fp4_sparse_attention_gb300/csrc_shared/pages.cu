@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kListThreads) pool_list_kernel(const PoolParam
     int below = 0;  // pages in use below n
 #pragma unroll 4
     for (int w = tid; w < (n >> 5); w += kListThreads) below += __popc(p.bitmap[w]);
-    if (tid == 0 && n < p.num_pages) below += __popc(p.bitmap[n >> 5] & ((1u << (n & 31)) - 1));
+    if (tid == 0 && (n & 31)) below += __popc(p.bitmap[n >> 5] & ((1u << (n & 31)) - 1));
     movers = n - list_sum(make_int2(below, 0), part).x;
     moves = min(movers, p.max_moves);
   }

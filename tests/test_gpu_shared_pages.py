@@ -285,6 +285,21 @@ def test_large_pools_and_many_requests(reqs, num_pages):
     assert want[4] == len(S.in_use(cached, table, 64, num_pages)[0])
 
 
+@pytest.mark.parametrize("num_pages", [65, 96, 127, 131, 131200, 131201, 131209, 160031])
+@pytest.mark.parametrize("free", [0, 1, 33])
+def test_compaction_of_pools_that_are_almost_full(num_pages, free):
+    # every page but `free` of them, which lie at the pool's start, middle and end
+    holes = {x for i in range(free) for x in [(0, num_pages // 2, num_pages - 1)[i % 3] + (i // 3 if i % 3 < 2 else -(i // 3))]}
+    pages = [x for x in range(num_pages) if x not in holes]
+    width = -(-len(pages) // 3)
+    table = [pages[i * width:(i + 1) * width] for i in range(3)]
+    cached = [64 * len(r) for r in table]
+    table = [r + [7] * (width - len(r)) for r in table]
+    want = check_compact(cached, table, 64, num_pages, 50)
+    assert want[4] == num_pages - len(holes) and (free > 0 or want[3] == 0)
+    assert check_release([], None, cached, table, 64, num_pages)[2] == len(holes)
+
+
 def test_workspace_is_the_callers_or_made_for_the_call():
     cached, table = many_requests(20, MANY + 100, 50, 3)
     want = S.release([1], None, cached, table, 64, MANY + 100)
