@@ -134,8 +134,8 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkParams p) 
         if (j + 32 * k < f.full) to[j + 32 * k] = page[k];
     }
     if (f.part) {
-      if (before < p.num_free) dst = __ldg(p.free_pages + before);
-      else err |= kErrLengths;
+      if (before < p.num_free) dst = max(-1, __ldg(p.free_pages + before));
+      if (dst < 0) err |= kErrLengths;
       if (lane == 0) to[f.full] = dst;
       src = from[f.full];
       if (src < 0 || src >= p.num_pages) {

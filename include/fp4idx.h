@@ -641,14 +641,15 @@ fp4idx_status_t fp4idx_shared_prefix_attention(const fp4idx_shared_attention_t* 
  *   cached_len  [num_reqs] int32, in place: entry child[i] becomes L.
  *   copy_src, copy_dst  [num_forks] int32: the unfinished page and the child's
  *             own one (fp4idx_copy_pages' input), or -1 and -1.
- *   pages_taken [1] the number of free pages used.
+ *   pages_taken [1] the number of entries of free_pages used.
  * The children's rows must hold nothing that is still wanted (release them
  * first).  A negative parent or child is no fork (padding of a fixed-size
  * call).  Refused, with -1 and -1 and the child left as it was:
  * FP4IDX_ERR_REQUESTS -- a number not below num_reqs; a child that an earlier
  * fork of the call names (counted as taking its page) or that is the parent of
- * any fork; FP4IDX_ERR_LENGTHS -- a parent longer than its table row.  Without a free page left the child's
- * unfinished page is entered as -1 and FP4IDX_ERR_LENGTHS is set.  A parent's
+ * any fork; FP4IDX_ERR_LENGTHS -- a parent longer than its table row.  Without a free page left (behind
+ * num_free, or a negative entry: what fp4idx_release_pages leaves behind its
+ * list) the child's unfinished page is entered as -1 and FP4IDX_ERR_LENGTHS is set.  A parent's
  * unfinished page outside [0, num_pages) gives -1 and -1 and
  * FP4IDX_ERR_PAGE_RANGE (full pages are shared as they are).  Negative lengths
  * count as 0.  A call repeated on its own results enters the same pages again.

@@ -42,7 +42,7 @@ def fork(parent, child, fork_len, cached, table, free, page, num_pages):
             err |= ERR_REQUESTS
         new = -1
         if fits and part:
-            new = free[used] if used < len(free) else -1
+            new = max(-1, free[used]) if used < len(free) else -1
             used += 1
         if refused or not fits:
             continue

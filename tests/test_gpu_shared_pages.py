@@ -85,6 +85,12 @@ def test_fork_without_pages_or_room():
     assert check_fork([0, 0], [1, 2], [100, 128], [130] * 6, table, [70, 71], 64, 100)[5] == S.ERR_PAGE_RANGE
 
 
+def test_forks_from_a_list_that_release_ended_with_negative_entries():
+    table = [[10 * b + j for j in range(3)] for b in range(6)]
+    want = check_fork([0, 0, 0, 0], [1, 2, 3, 4], None, [100] * 6, table, [70, -1, -7, -2 ** 31], 64, 100)
+    assert want[5] == S.ERR_LENGTHS and want[3] == [70, -1, -1, -1] and [want[1][b][1] for b in (1, 2, 3, 4)] == [70, -1, -1, -1]
+
+
 def test_no_forks():
     check_fork([], [], None, [3, 4], [[1], [2]], [5], 64, 10)
 
