@@ -109,6 +109,19 @@ def test_many_groups():
     run_case(11, groups, heads=4, kv_heads=4, page=128)
 
 
+def test_more_blocks_than_a_cta_has_threads():
+    # 800 blocks of a group: a row of 256 heads each; 900 groups, some without requests or rows
+    run_case(13, [(130, [(400, 400), (400, 430)])], heads=256, kv_heads=1)
+    groups = [((29 * i) % 300, [((i + j) % 3, 1 + (11 * i + 53 * j) % 70) for j in range((i // 2) % 3)]) for i in range(900)]
+    run_case(14, groups, heads=4, kv_heads=2)
+
+
+@pytest.mark.parametrize("reqs", [33, 300, 1023, 1025, 2500])
+def test_blocks_and_groups_of_many_requests(reqs):
+    # one head a K/V head: a block is 256 rows, so up to 256 requests and more where some have no rows
+    run_case(reqs, [(70, [((7 * i) % 5 % 3, 1 + (37 * i) % 40) for i in range(reqs)]), (0, [(1, 5)] * 40)], heads=2, kv_heads=2)
+
+
 def test_long_requests_without_a_prefix():
     run_case(12, [(0, [(1, 9000), (2, 3000), (1, 17)])], heads=8, kv_heads=2)
 
@@ -346,6 +359,28 @@ def test_another_stream_two_objects_and_graph_replay():
     g.replay()
     torch.cuda.synchronize()
     check(c, (a.out, a.lse))
+
+
+def test_graphs_of_different_calls_share_a_workspace():
+    cases = [S.make_shared(60 + i, groups, heads=16, kv_heads=4, device="cuda") for i, groups in
+             enumerate(([(5000, [(1, 40)] * 20)], [(64, [(1, 1)] * 3), (0, [(2, 900)])], [(300, [(70, 100), (50, 60)])]))]
+    shared = torch.empty(max(build(c).workspace.numel() for c in cases), dtype=torch.uint8, device="cuda")
+    calls = [build(c, workspace=shared) for c in cases]
+    want = [[x.clone() for x in B.fp4idx_shared_prefix_attention(a)] for a in calls]
+    graphs = []
+    for a in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            B.fp4idx_shared_prefix_attention(a)
+        graphs.append(g)
+    for order in ((0, 1, 2, 1, 0, 2), (2, 2, 0, 0, 1, 1)):
+        for a in calls:
+            a.out.fill_(math.nan)
+        for i in order:  # one behind another, no wait between
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for a, w in zip(calls, want) for x, y in zip((a.out, a.lse), w))
+    assert B.fp4idx_get_error(clear=True) == 0
 
 
 def test_workspace_too_small_is_refused():
