@@ -95,6 +95,7 @@ struct Plan {
   int32_t blocks;          // of one K/V head: num_groups x blocks_per_group
   int32_t blocks_per_group;
   int32_t ctas;
+  int32_t few;             // up to 32 blocks, tiles that 32 bits can be multiplied in
   Block* block;
   int32_t* block_tiles;
   Span* span;
@@ -272,7 +273,8 @@ struct Control {
   Chunk chunk[kChunks];
   float row[2][2][kRows];  // exchange between the threads of a row
   Block first;           // the block that this CTA's run begins in
-  int32_t run_hk, run_block, run_start, run_lo, run_hi, per_head, worst;
+  int32_t run_hk, run_block, run_start, run_lo, run_hi, per_head;
+  uint32_t worst;
   uint32_t tmem;
   int abort;
 };
@@ -284,6 +286,25 @@ static_assert(kSmem <= 232448, "227 KB per CTA");
 // over all blocks: a run that crosses from one block to the next has queries to
 // wait for and sums to write twice.
 constexpr int kOwnRunTiles = 3;
+// A block's own CTAs: [S used / all, (S + t) used / all) of a block of t tiles
+// behind S others, at least t used / all of them.  (32 bits: below kTiles32 tiles.)
+constexpr int kTiles32 = 1 << 22;
+static_assert(static_cast<uint64_t>(kTiles32) * 257 < uint64_t{1} << 32, "times the CTAs (a join's threads) and one");
+struct Split {
+  uint32_t worst, limit;  // tiles of a block's longest own run; what that may be
+};
+__device__ __forceinline__ Split split_of(uint32_t tiles, uint32_t all, uint32_t used) {
+  const uint32_t least = tiles * used / all;
+  return {tiles == 0 ? 0u : least == 0 ? UINT32_MAX : (tiles + least - 1) / least, (all + used - 1) / used + kOwnRunTiles};
+}
+// The last tile that may be the first of CTA cta's block.
+__device__ __forceinline__ uint32_t own_probe(uint32_t cta, uint32_t all, uint32_t used) { return ((cta + 1) * all - 1) / used; }
+// CTA cta's run of the block's tiles [start, start + tiles).
+__device__ __forceinline__ void own_run(uint32_t start, uint32_t tiles, uint32_t cta, uint32_t all, uint32_t used, uint32_t* lo, uint32_t* hi) {
+  const uint32_t c0 = start * used / all, n = (start + tiles) * used / all - c0;
+  *lo = start + tiles * (cta - c0) / n;
+  *hi = start + tiles * (cta + 1 - c0) / n;
+}
 
 template <int DTYPE>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -368,7 +389,53 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
   pdl_wait();  // everything below reads what earlier kernels wrote
 
   // ---- this CTA's run of tiles and the block that it begins in
-  {
+  const auto begin_run = [&](const Block& b, int i, int hk, int start, int lo, int hi, int per_head) {
+    ctl.first = b;
+    ctl.run_hk = hk;
+    ctl.run_block = i;
+    ctl.run_start = start;
+    ctl.run_lo = lo;
+    ctl.run_hi = hi;
+    ctl.per_head = per_head;
+    RunInfo info = {};
+    info.item = hk * pl.blocks + i;
+    info.inside = lo > start;
+    info.row0 = b.row0;
+    info.pair0 = b.pair0;
+    info.pairs = b.pairs;
+    info.hk = hk;
+    pl.info[blockIdx.x] = info;
+  };
+  if (pl.few) {
+    // a block a lane of one warp
+    if (warp == kPlanWarp) {
+      Block own = {};
+      if (lane < pl.blocks) own = pl.block[lane];
+      const uint32_t mine = own.tiles, cta = blockIdx.x;
+      uint32_t incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const uint32_t before = incl - mine, per_head = __shfl_sync(0xffffffffu, incl, 31), all = per_head * p.num_kv_heads;
+      const uint32_t used = min(static_cast<uint32_t>(pl.ctas), (all + 1) / 2);
+      if (cta >= used) {
+        if (lane == 0) pl.info[cta].item = -1;
+      } else {
+        const Split split = split_of(mine, all, used);
+        const bool own_runs = static_cast<uint32_t>(pl.blocks * p.num_kv_heads) <= used &&
+                              __reduce_max_sync(0xffffffffu, split.worst) <= split.limit;
+        const uint32_t x = own_runs ? own_probe(cta, all, used) : cta * all / used, h = x / per_head, at = x - h * per_head;
+        if (before <= at && at < before + mine) {
+          const uint32_t start = h * per_head + before;
+          uint32_t lo = x, hi = (cta + 1) * all / used;
+          if (own_runs) own_run(start, mine, cta, all, used, &lo, &hi);
+          begin_run(own, lane, h, start, lo, hi, per_head);
+        }
+      }
+    }
+  } else {
     int* warp_sum = reinterpret_cast<int*>(smem);  // (the ring is not in use yet)
     const int per = (pl.blocks + kThreads - 1) / kThreads;
     const int first = min(pl.blocks, tid * per), last = min(pl.blocks, first + per);
@@ -397,29 +464,26 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
     }
     const int heads = p.num_kv_heads, total = per_head * heads, cta = blockIdx.x;
     const int used = min(pl.ctas, (total + 1) / 2);  // (two tiles go through the two accumulators at a time)
-    // A block's own CTAs: [S used / total, (S + t) used / total) of a block of t
-    // tiles behind S others, at least t used / total of them.  (32 bits.)
-    const uint32_t all = total, n_all = used;
-    bool own_runs = per == 1 && static_cast<int64_t>(pl.blocks) * heads <= used && total < 1 << 22;
+    bool own_runs = per == 1 && static_cast<int64_t>(pl.blocks) * heads <= used && total < kTiles32;
     if (own_runs) {
-      const uint32_t least = mine * n_all / all;
-      const int worst = __reduce_max_sync(0xffffffffu, mine == 0 ? 0 : least == 0 ? INT32_MAX : static_cast<int>((mine + least - 1) / least));
+      const Split split = split_of(mine, total, used);
+      const uint32_t worst = __reduce_max_sync(0xffffffffu, split.worst);
       if (lane == 0 && worst > 0) atomicMax(&ctl.worst, worst);
       __syncthreads();
-      own_runs = ctl.worst <= static_cast<int>((all + n_all - 1) / n_all) + kOwnRunTiles;
+      own_runs = ctl.worst <= split.limit;
     }
     // the thread whose blocks hold the run's first tile
     int lo = 0, hi = 0, hk = -1;
     if (cta >= used) {
       if (tid == 0) pl.info[cta].item = -1;
     } else if (own_runs) {
-      const uint32_t x = ((cta + 1) * all - 1) / n_all;  // the last tile that may be the first of CTA cta's block
-      const int h = x / per_head, at = x - h * per_head;
+      const int x = own_probe(cta, total, used), h = x / per_head, at = x - h * per_head;
       if (before <= at && at < before + mine) {
-        const uint32_t s = h * per_head + before, c0 = s * n_all / all, n = (s + mine) * n_all / all - c0;
+        uint32_t from, to;
+        own_run(h * per_head + before, mine, cta, total, used, &from, &to);
         hk = h;
-        lo = s + mine * (cta - c0) / n;
-        hi = s + mine * (cta + 1 - c0) / n;
+        lo = from;
+        hi = to;
       }
     } else {
       lo = static_cast<int>(static_cast<int64_t>(total) * cta / used);
@@ -433,22 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
         while (hk * per_head + before + pl.block_tiles[i] <= lo) before += pl.block_tiles[i++];
         own = pl.block[i];
       }
-      const int start = hk * per_head + before;
-      ctl.first = own;
-      ctl.run_hk = hk;
-      ctl.run_block = i;
-      ctl.run_start = start;
-      ctl.run_lo = lo;
-      ctl.run_hi = hi;
-      ctl.per_head = per_head;
-      RunInfo info = {};
-      info.item = hk * pl.blocks + i;
-      info.inside = lo > start;
-      info.row0 = own.row0;
-      info.pair0 = own.pair0;
-      info.pairs = own.pairs;
-      info.hk = hk;
-      pl.info[cta] = info;
+      begin_run(own, i, hk, hk * per_head + before, lo, hi, per_head);
     }
   }
   __syncthreads();
@@ -1164,6 +1213,14 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 // ---------------------------------------------------------------- host
 int64_t round16(int64_t n) { return (n + 15) & ~int64_t{15}; }
 
+// Tiles that a call can have over all K/V heads: a span is what a block has of
+// one request or of the prefix.
+int64_t most_tiles(const SharedParams& p) {
+  const int64_t tiles = (static_cast<int64_t>(p.a.max_seqlen_k) + 63) / kTile + 1;
+  const int64_t of_head = tiles * (2 * static_cast<int64_t>(p.blocks_per_group) * p.num_groups + p.a.num_seqs);
+  return of_head > INT32_MAX ? of_head : of_head * p.a.num_kv_heads;
+}
+
 // The workspace's parts; returns its size.
 size_t lay_out(Plan* pl, char* w) {
   char* const begin = w;
@@ -1190,6 +1247,7 @@ Plan plan_of(const SharedParams& p) {
   pl.blocks_per_group = p.blocks_per_group;
   pl.blocks = p.num_groups * p.blocks_per_group;
   pl.ctas = p.ctas;
+  pl.few = pl.blocks <= 32 && most_tiles(p) < kTiles32;
   return pl;
 }
 
@@ -1244,13 +1302,11 @@ bool plan_shared(SharedParams* p, int sms) {
   const int64_t pairs = static_cast<int64_t>(p->max_group_rows) * a.group;
   const int64_t per = (pairs + kBlockPairs - 1) / kBlockPairs, blocks = per * p->num_groups;
   if (blocks > 1 << 20) return false;
-  // A span is what a block has of one request or of the prefix.
-  const int64_t tiles = (static_cast<int64_t>(a.max_seqlen_k) + 63) / kTile + 1;
-  const int64_t spans = 2 * blocks + a.num_seqs;
-  if (tiles * spans > INT32_MAX / a.num_kv_heads) return false;
   p->blocks_per_group = static_cast<int32_t>(per);
+  const int64_t tiles = most_tiles(*p);
+  if (tiles > INT32_MAX) return false;
   // (the join looks at one CTA per thread)
-  p->ctas = static_cast<int32_t>(std::min<int64_t>(std::min(sms, kJoinThreads), tiles * spans * a.num_kv_heads));
+  p->ctas = static_cast<int32_t>(std::min<int64_t>(std::min(sms, kJoinThreads), tiles));
   return true;
 }
 
