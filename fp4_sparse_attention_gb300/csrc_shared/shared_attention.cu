@@ -1134,19 +1134,22 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
 
 // ---------------------------------------------------------------- join
 // out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over the partial sums of
-// a block that crosses run boundaries, in the order of its tiles.  A warp takes
-// 32 rows (a lane a row) and 32 columns.  With few parts (BY_ITEM false:
-// blockIdx.x counts run boundaries, the first one inside a block does its work)
-// it adds all of them, and a CTA's warps take 64 rows; with many (BY_ITEM:
-// blockIdx.x is the block of a K/V head) the CTA's warps take parts in turn and
-// are added in order.
-constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinCols = 32;
+// a block that crosses run boundaries, in the order of its tiles.  A lane has a
+// row.  With few parts (BY_ITEM false: blockIdx.x counts run boundaries, the
+// first one inside a block does its work) a warp adds all of them for 32 columns;
+// with many (BY_ITEM: blockIdx.x is the block of a K/V head) a CTA's warps take
+// parts in turn for 16 columns, several parts' loads together, and are added in
+// order.  Bound by the round trips to L2: with a part of 32 columns at a time a
+// block of 25 parts took 42.0 us in all, in this way 37.2; in 16 columns calls of
+// two or three parts only have more CTAs (82.1 for 81.6, 35.6 for 34.4 us).
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 
 template <int DTYPE, bool BY_ITEM>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Plan pl) {
-  __shared__ float4 sums[BY_ITEM ? kJoinWarps : 1][kJoinCols / 4][32];
+  constexpr int kCols = BY_ITEM ? 16 : 32, kFours = kCols / 4, kUnits = kCols / 8, kParts = BY_ITEM ? 4 : 1;
+  __shared__ float4 sums[BY_ITEM ? kJoinWarps : 1][kFours][32];
   __shared__ float2 part[kJoinWarps][32];
-  __shared__ uint4 staged[BY_ITEM ? 1 : kJoinWarps][32 * 4];
+  __shared__ uint4 staged[BY_ITEM ? 1 : kJoinWarps][32 * kUnits];
   __shared__ RunInfo its;
   __shared__ int first_cta;
   pdl_wait();
@@ -1168,37 +1171,47 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   if (item < 0 || parts == 1 || (!BY_ITEM && c != static_cast<int>(blockIdx.x) + 1)) return;
   if (tid == c) its = info;
   __syncthreads();
-  const int row = (BY_ITEM ? blockIdx.y : blockIdx.y * 2 + (warp >> 2)) * 32 + lane, cols = (BY_ITEM ? blockIdx.z : warp & 3) * kJoinCols;
+  const int row = (BY_ITEM ? blockIdx.y : blockIdx.y * 2 + (warp >> 2)) * 32 + lane, cols = (BY_ITEM ? blockIdx.z : warp & 3) * kCols;
   if (row - lane >= its.pairs) return;  // (BY_ITEM: the whole CTA)
-  float4 acc[kJoinCols / 4] = {};
+  float4 acc[kFours] = {};
   float m = -INFINITY, l = 0.0f;
-#pragma unroll 2
-  for (int i = BY_ITEM ? warp : 0; i < parts; i += BY_ITEM ? kJoinWarps : 1) {
-    // part i is CTA c - 1 + i's; of the first one its last segment, of the others their first
-    const int64_t at = 2 * (c - 1 + i) + (i == 0);
-    const float2 s = pl.stats[at * kBlockPairs + row];
-    float4 o[kJoinCols / 4];
+  constexpr int step = BY_ITEM ? kJoinWarps : 1;
+#pragma unroll (BY_ITEM ? 1 : 2)
+  for (int i0 = BY_ITEM ? warp : 0; i0 < parts; i0 += kParts * step) {
+    float2 s[kParts];
+    float4 o[kParts][kFours];
 #pragma unroll
-    for (int v = 0; v < kJoinCols / 4; ++v) o[v] = pl.partial[(at * (kPagedDim / 4) + cols / 4 + v) * kBlockPairs + row];
-    const float top = fmaxf(m, s.x), ref = top == -INFINITY ? 0.0f : top;
-    const float keep = ex2(m - ref), w = ex2(s.x - ref);
-    m = top;
-    l = l * keep + w * s.y;
+    for (int b = 0; b < kParts; ++b) {
+      // part i is CTA c - 1 + i's; of the first one its last segment, of the others
+      // their first (behind the last part: the last one, which does not count)
+      const int i = min(i0 + b * step, parts - 1);
+      const int64_t at = 2 * (c - 1 + i) + (i == 0);
+      s[b] = pl.stats[at * kBlockPairs + row];
 #pragma unroll
-    for (int v = 0; v < kJoinCols / 4; ++v) {
-      acc[v].x = acc[v].x * keep + w * o[v].x;
-      acc[v].y = acc[v].y * keep + w * o[v].y;
-      acc[v].z = acc[v].z * keep + w * o[v].z;
-      acc[v].w = acc[v].w * keep + w * o[v].w;
+      for (int v = 0; v < kFours; ++v) o[b][v] = pl.partial[(at * (kPagedDim / 4) + cols / 4 + v) * kBlockPairs + row];
+    }
+#pragma unroll
+    for (int b = 0; b < kParts; ++b) {
+      if (i0 + b * step >= parts) break;
+      const float top = fmaxf(m, s[b].x), ref = top == -INFINITY ? 0.0f : top;
+      const float keep = ex2(m - ref), w = ex2(s[b].x - ref);
+      m = top;
+      l = l * keep + w * s[b].y;
+#pragma unroll
+      for (int v = 0; v < kFours; ++v) {
+        acc[v].x = acc[v].x * keep + w * o[b][v].x;
+        acc[v].y = acc[v].y * keep + w * o[b][v].y;
+        acc[v].z = acc[v].z * keep + w * o[b][v].z;
+        acc[v].w = acc[v].w * keep + w * o[b][v].w;
+      }
     }
   }
   if constexpr (BY_ITEM) {
 #pragma unroll
-    for (int v = 0; v < kJoinCols / 4; ++v) sums[warp][v][lane] = acc[v];
+    for (int v = 0; v < kFours; ++v) sums[warp][v][lane] = acc[v];
     part[warp][lane] = make_float2(m, l);
     __syncthreads();
     // warp v adds the warps' shares of four columns
-    static_assert(kJoinWarps == kJoinCols / 4, "four columns a warp");
     m = part[0][lane].x;
 #pragma unroll
     for (int w = 1; w < kJoinWarps; ++w) m = fmaxf(m, part[w][lane].x);
@@ -1207,7 +1220,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     acc[0] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) {
-      const float4 o = sums[w][warp][lane];
+      const float4 o = sums[w][warp % kFours][lane];
       const float f = ex2(part[w][lane].x - ref);
       l = fmaf(f, part[w][lane].y, l);
       acc[0].x = fmaf(f, o.x, acc[0].x);
@@ -1217,8 +1230,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     }
   }
   // Out by whole 32-byte sectors: a warp's 32 rows x 64 bytes (BY_ITEM: the
-  // CTA's), four lanes a row.  (Eight bytes a lane, as they come, took twice as
-  // long as all the rest.)
+  // CTA's 32 rows x 32).  (Eight bytes a lane, as they come, took twice as long
+  // as all the rest.)
   const bool have = row < its.pairs;
   const int pair = its.pair0 + row, t = its.row0 + group_div(p, pair);
   const int h = its.hk * p.group + pair - group_div(p, pair) * p.group;
@@ -1227,22 +1240,23 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   if (p.lse && have && cols == 0 && (!BY_ITEM || warp == 0)) p.lse[static_cast<int64_t>(t) * p.num_heads + h] = row_lse(m, l);
   uint4* const rows = staged[BY_ITEM ? 0 : warp];
   if constexpr (BY_ITEM) {
-    reinterpret_cast<uint2*>(rows)[lane * 8 + warp] = make_uint2(pack2<DTYPE>(acc[0].x * inv, acc[0].y * inv), pack2<DTYPE>(acc[0].z * inv, acc[0].w * inv));
+    if (warp < kFours)
+      reinterpret_cast<uint2*>(rows)[lane * 4 + warp] = make_uint2(pack2<DTYPE>(acc[0].x * inv, acc[0].y * inv), pack2<DTYPE>(acc[0].z * inv, acc[0].w * inv));
     __syncthreads();
     if (warp > 0) return;
   } else {
 #pragma unroll
-    for (int v = 0; v < kJoinCols / 4; v += 2)
-      rows[lane * 4 + ((v / 2) ^ (lane >> 1 & 3))] =
+    for (int v = 0; v < kFours; v += 2)
+      rows[lane * kUnits + ((v / 2) ^ (lane >> 1 & 3))] =
           make_uint4(pack2<DTYPE>(acc[v].x * inv, acc[v].y * inv), pack2<DTYPE>(acc[v].z * inv, acc[v].w * inv),
                      pack2<DTYPE>(acc[v + 1].x * inv, acc[v + 1].y * inv), pack2<DTYPE>(acc[v + 1].z * inv, acc[v + 1].w * inv));
     __syncwarp();
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row_i = 8 * i + (lane >> 2), unit = lane & 3;
+  for (int i = 0; i < kUnits; ++i) {
+    const int row_i = (i * 32 + lane) / kUnits, unit = lane % kUnits;
     const int64_t at = __shfl_sync(0xffffffffu, to, row_i);
-    const uint4 v = rows[row_i * 4 + (BY_ITEM ? unit : unit ^ (row_i >> 1 & 3))];
+    const uint4 v = rows[row_i * kUnits + (BY_ITEM ? unit : unit ^ (row_i >> 1 & 3))];
     if (at >= 0) *(reinterpret_cast<uint4*>(p.out + at) + unit) = v;
   }
 }
@@ -1323,7 +1337,7 @@ cudaError_t launch(const Plan& pl, const AttnMaps& maps, cudaStream_t stream) {
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   if (pl.ctas > 4 * items) {
-    cfg.gridDim = dim3(static_cast<unsigned>(items), (rows + 31) / 32, kPagedDim / kJoinCols);
+    cfg.gridDim = dim3(static_cast<unsigned>(items), (rows + 31) / 32, kPagedDim / 16);
     return cudaLaunchKernelEx(&cfg, join_kernel<DTYPE, true>, pl);
   }
   cfg.gridDim = dim3(static_cast<unsigned>(pl.ctas - 1), (rows + 63) / 64);
