@@ -76,15 +76,14 @@ SharedParams shared_params(const fp4idx_shared_attention_t* s) {
   return p;
 }
 
-// The caches as {64 values, (K/V head, offset), piece of 64 values, page}:
-// boxes of 64 keys of one page, a piece of the keys and both of the values.
-fp4idx_status_t shared_maps(const fp4idx_attention_t* a, AttnMaps* maps) {
+fp4idx_status_t shared_maps(const fp4idx_attention_t* a, SharedMaps* maps) {
   const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(a->num_kv_heads) * a->page_size, kPagedDim / 64,
                               static_cast<cuuint64_t>(a->num_pages)};
   const cuuint64_t strides[3] = {kPagedDim * 2, 128, static_cast<cuuint64_t>(a->page_stride) * 2};
-  const cuuint32_t k_box[4] = {64, 64, 1, 1}, v_box[4] = {64, 64, 2, 1};
-  const fp4idx_status_t s = call_tensor_map16(&maps->k, a->k, 4, dims, strides, k_box);
-  return s != FP4IDX_OK ? s : call_tensor_map16(&maps->v, a->v, 4, dims, strides, v_box);
+  const cuuint32_t k_box[4] = {64, 64, 1, 1}, v_box[4] = {64, 64, 2, 1}, part_box[4] = {64, 16, 1, 1};
+  fp4idx_status_t s = call_tensor_map16(&maps->k, a->k, 4, dims, strides, k_box);
+  if (s == FP4IDX_OK) s = call_tensor_map16(&maps->v, a->v, 4, dims, strides, v_box);
+  return s != FP4IDX_OK ? s : call_tensor_map16(&maps->v_part, a->v, 4, dims, strides, part_box);
 }
 
 PoolParams pool_params(int32_t num_reqs, int32_t page_size, int64_t num_pages, const int32_t* block_table,
@@ -129,7 +128,7 @@ fp4idx_status_t fp4idx_shared_prefix_attention(const fp4idx_shared_attention_t* 
   if (!plan_shared(&p, sms))
     FAIL(FP4IDX_EUNSUPPORTED, "more than 2^20 blocks of 256 (row, head) pairs over all groups, or 2^31 key tiles");
   if ((s = check_workspace(workspace, workspace_bytes, shared_workspace(p))) != FP4IDX_OK) return s;
-  AttnMaps maps;
+  SharedMaps maps;
   if ((s = shared_maps(&shared->attention, &maps)) != FP4IDX_OK) return s;
   return cuda_status(launch_shared(p, maps, shared->attention.dtype, workspace, static_cast<cudaStream_t>(stream)),
                      "shared-prefix attention launch");

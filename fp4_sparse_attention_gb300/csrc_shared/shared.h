@@ -89,10 +89,17 @@ struct SharedParams {
   int32_t ctas;
 };
 
+// The caches as {64 values, (K/V head, offset), piece of 64 values, page}: boxes of
+// 64 keys of one page, a piece of the keys and both of the values, and of 16 keys,
+// a piece of the values.
+struct SharedMaps {
+  CUtensorMap k, v, v_part;
+};
+
 // Fills the work split; false if it does not fit the counters.
 bool plan_shared(SharedParams* p, int sms);
 size_t shared_workspace(const SharedParams& p);
-cudaError_t launch_shared(SharedParams p, const AttnMaps& maps, int dtype, void* workspace, cudaStream_t stream);
+cudaError_t launch_shared(SharedParams p, const SharedMaps& maps, int dtype, void* workspace, cudaStream_t stream);
 
 cudaError_t launch_fork(const ForkParams& p, cudaStream_t stream);
 cudaError_t launch_copy_pages(CopyParams p, int sms, cudaStream_t stream);

@@ -30,8 +30,8 @@
 // Roles: warps 0-7 and 8-15 softmax of the two accumulators, queries and output
 // (four of a lane quarter, by halves of the keys); warps 16 and 17 issue the
 // products of one accumulator each; warp 18 loader (TMA; 16-byte copies, which
-// can leave zeros where a value may be anything, for the values of a run that
-// ends inside); warp 19 planner, which looks up the tiles' pages ahead of all
+// can leave zeros where a value may be anything, for the last values of a run
+// that ends inside); warp 19 planner, which looks up the tiles' pages ahead of all
 // of them and hands them out in chunks.
 #include <algorithm>
 #include <atomic>
@@ -390,7 +390,7 @@ __device__ __forceinline__ void clear_other_rows(const SharedParams& sp, int lan
 }
 
 template <int DTYPE>
-__global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_constant__ Plan pl, const __grid_constant__ AttnMaps maps) {
+__global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_constant__ Plan pl, const __grid_constant__ SharedMaps maps) {
   extern __shared__ __align__(1024) uint8_t smem[];
   Control& ctl = *reinterpret_cast<Control*>(smem + kOff_Ctl);
   const SharedParams& sp = pl.sp;
@@ -432,6 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
   if (tid == 32 * kLoadWarp) {
     prefetch_tmap(&maps.k);
     prefetch_tmap(&maps.v);
+    prefetch_tmap(&maps.v_part);
   }
   if (warp == kMmaWarp) tmem_alloc<kTmemCols>(smem_u32(&ctl.tmem));
   __syncthreads();
@@ -711,21 +712,37 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
             __syncwarp();
             if (lane < 4) tma_load_4d(dst + (lane >> 1) * kPiece + r * kRun, &maps.k, 0, row, lane >> 1, page, bar);
           } else {
-            // a run that ends inside is copied, with zeros behind the end
-            const int tail = tails ? (hi - pos) >> 6 : -1;
+            // Of a run that ends inside 16 keys at a time, as the products take
+            // them: the whole ones by TMA, the last by copies with zeros behind
+            // the end.  (All 64 by copies kept the loader for 1,850 cycles: 15.0
+            // for 13.7 us with two requests, 96.3 for 94.7 with 486 ends of requests.)
+            int tail = tails ? (hi - pos) >> 6 : -1, whole = 0;
             if (tail >= 0) {
               const int32_t its = __shfl_sync(0xffffffffu, here, tail), at = __shfl_sync(0xffffffffu, row, tail);
-              const int keys = its < 0 ? 0 : hi - pos - 64 * tail;
-              const uint16_t* src = p.v + (its < 0 ? 0 : its) * p.page_stride + static_cast<int64_t>(at) * kPagedDim;
-              const int u = lane & 7, piece = (lane >> 3) & 1;  // 16-byte unit
-#pragma unroll 4
-              for (int k = lane >> 4; k < 64; k += 2)
-                cp_async_16_or_zero(dst + tail * 2 * kRun + piece * kRun + k * 128 + ((u ^ (k & 7)) << 4),
-                                    src + (k < keys ? k : 0) * kPagedDim + piece * 64 + u * 8, k < keys);
-              cp_async_arrive_extra(bar);
-              __syncwarp();
+              if (its < 0) {
+                tail = -1;  // zeros, like any page that is not there
+              } else {
+                const int keys = hi - pos - 64 * tail;
+                const uint32_t to = dst + tail * 2 * kRun;
+                whole = keys >> 4;
+                if (keys & 15) {
+                  const int u = lane & 7, piece = (lane >> 3) & 1, k0 = 16 * whole + (lane >> 4);  // 16-byte unit; row
+                  const uint16_t* src = p.v + its * p.page_stride + static_cast<int64_t>(at) * kPagedDim + piece * 64 + u * 8;
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) {
+                    const int k = k0 + 2 * j;
+                    cp_async_16_or_zero(to + piece * kRun + k * 128 + ((u ^ (k & 7)) << 4), src + (k < keys ? k : 0) * kPagedDim, k < keys);
+                  }
+                  cp_async_arrive_extra(bar);
+                  __syncwarp();
+                }
+                if (lane == 0) mbar_arrive_expect_tx(bar, kStage / 2 + whole * (16 * 2 * 128));
+                __syncwarp();
+                if (lane < 2 * whole)
+                  tma_load_4d(to + (lane & 1) * kRun + (lane >> 1) * (16 * 128), &maps.v_part, 0, at + (lane >> 1) * 16, lane & 1, its, bar);
+              }
             }
-            if (lane == 0) mbar_arrive_expect_tx(bar, tail >= 0 ? kStage / 2 : kStage);
+            if (tail < 0 && lane == 0) mbar_arrive_expect_tx(bar, kStage);
             __syncwarp();
             if (lane < 2 && lane != tail) tma_load_4d(dst + lane * 2 * kRun, &maps.v, 0, row, 0, page, bar);
           }
@@ -761,15 +778,22 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
     uint32_t turns = 0;
     bool ok = true;
     // A tile whose value product is to come: its number, its values' stage,
-    // whether copies filled it and whether its product adds to the output.
+    // whether copies filled it, its keys by 16 (what lies behind them may be
+    // anything) and whether its product adds to the output.
     bool open = false;
-    uint32_t open_tile = 0, v_st = 0, v_use = 0, v_tail = 0, more = 0;
+    uint32_t open_tile = 0, v_st = 0, v_use = 0, v_tail = 0, v_steps = 0, more = 0;
     uint32_t begun = 0;                      // this accumulator has had a tile of the segment
     const auto values = [&] {
       const uint64_t v = desc_sw128(base + v_st * kStage, kRun);
+      if (v_steps == 8) {  // (a test in front of each product instead took 2 % of a long prefill)
 #pragma unroll
-      for (int x = 0; x < 8; ++x)
-        tc_mma_f16_tmem(o_tmem, s_tmem + (x >> 2) * kHalf + (x & 3) * 8, v + (x >> 2) * (2 * kRun >> 4) + (x & 3) * 128, o_idesc, x > 0 ? 1u : more);
+        for (int x = 0; x < 8; ++x)
+          tc_mma_f16_tmem(o_tmem, s_tmem + (x >> 2) * kHalf + (x & 3) * 8, v + (x >> 2) * (2 * kRun >> 4) + (x & 3) * 128, o_idesc, x > 0 ? 1u : more);
+      } else {
+#pragma unroll 1
+        for (uint32_t x = 0; x < v_steps; ++x)
+          tc_mma_f16_tmem(o_tmem, s_tmem + (x >> 2) * kHalf + (x & 3) * 8, v + (x >> 2) * (2 * kRun >> 4) + (x & 3) * 128, o_idesc, x > 0 ? 1u : more);
+      }
       tc_commit(smem_u32(&ctl.kempty[v_st]));
     };
     const auto wait_weights = [&] {  // of the open tile, and its values
@@ -792,6 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
       ok = warp_try(smem_u32(&ctl.cfull[slot]), (n / kChunks) & 1, abort_flag, p.err);
       if (!ok) break;
       const uint32_t flags = uniform(ctl.chunk[slot].flags), tiles = uniform(ctl.chunk[slot].tiles);
+      const int chunk_keys = uniform(ctl.chunk[slot].hi - ctl.chunk[slot].pos0);
       __syncwarp();
       if (flags & kEnd) break;
       if (lane == 0) mbar_arrive(smem_u32(&ctl.cempty[slot]));
@@ -861,6 +886,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
         v_st = next_v;
         v_use = next_use;
         v_tail = flags & kTail;
+        v_steps = min(max(chunk_keys - static_cast<int>(i) * kTile + 15, 16) >> 4, 8);
       }
       if (ok && (flags & kLast)) {
         const bool was_open = open;
@@ -1333,7 +1359,7 @@ Plan plan_of(const SharedParams& p) {
 }
 
 template <int DTYPE>
-cudaError_t launch(const Plan& pl, const AttnMaps& maps, cudaStream_t stream) {
+cudaError_t launch(const Plan& pl, const SharedMaps& maps, cudaStream_t stream) {
   static std::atomic<uint64_t> ready{0};  // devices whose kernel has its shared memory limit (a call costs 1 us)
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1398,7 +1424,7 @@ size_t shared_workspace(const SharedParams& p) {
   return lay_out(&pl, nullptr);
 }
 
-cudaError_t launch_shared(SharedParams p, const AttnMaps& maps, int dtype, void* workspace, cudaStream_t stream) {
+cudaError_t launch_shared(SharedParams p, const SharedMaps& maps, int dtype, void* workspace, cudaStream_t stream) {
   Plan pl = plan_of(p);
   lay_out(&pl, static_cast<char*>(workspace));
   return dtype == FP4IDX_BF16 ? launch<FP4IDX_BF16>(pl, maps, stream) : launch<FP4IDX_FP16>(pl, maps, stream);
