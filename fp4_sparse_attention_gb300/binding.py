@@ -26,6 +26,7 @@ The functions keep the C names:
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional
@@ -36,7 +37,6 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libfp4idx.so")
 
 FP4IDX_OK = 0
-_EWORKSPACE = 3
 FP4IDX_TOPK_SORTED = 0x1
 FP4IDX_TOPK_STREAMING = 0x2
 ERR_PAGE_RANGE = 0x1
@@ -966,16 +966,19 @@ def fp4idx_pages_workspace_bytes(num_pages: int, num_reqs: int, table_stride: in
     return int(load_library().fp4idx_pages_workspace_bytes(int(num_pages), int(num_reqs), int(table_stride)))
 
 
+_pages_workspace = functools.lru_cache(maxsize=64)(fp4idx_pages_workspace_bytes)  # of three numbers alone
+
+
 def _with_workspace(call, workspace, num_pages, num_reqs, width, where, stream):
     """call(pointer, bytes) with the given workspace, without one where none is needed, or with a new one."""
     if workspace is not None:
         if workspace.device != where or not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous, on the device of the table")
         return call(workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    status = call(None, 0)
-    if status != _EWORKSPACE:
-        return status
-    workspace = torch.empty(fp4idx_pages_workspace_bytes(num_pages, num_reqs, width), dtype=torch.uint8, device=where)
+    need = _pages_workspace(num_pages, num_reqs, width)
+    if need == 0:
+        return call(None, 0)
+    workspace = torch.empty(need, dtype=torch.uint8, device=where)
     if stream is not None:
         workspace.record_stream(stream)  # it is freed on return, perhaps before that stream comes to it
     return call(workspace.data_ptr(), workspace.numel())
