@@ -54,7 +54,9 @@ __device__ __forceinline__ Fork fork_of(const ForkParams& p, int i) {
 
 // A warp writes a fork's table row.  Every CTA first passes over all forks, a
 // thread each: it counts the unfinished pages of the ones before its own and
-// looks for one that names an own child.
+// looks for one that names an own child.  That is forks^2 / 8 reads from L2, but
+// no second launch and no wait for another CTA: bound by latency, 4 forks 2.9 us
+// on the device, 1,984 forks of up to 512 pages 5.7 us.
 __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkParams p) {
   __shared__ int32_t child[kForkWarps];
   __shared__ int bad[kForkWarps];
@@ -155,7 +157,9 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkParams p) 
 
 // ---------------------------------------------------------------- copy
 // A warp copies a piece of one page of one span: up to 4 KB, eight 16-byte
-// loads a lane before the first store.
+// loads a lane before the first store, so that an SM has 256 KB under way.  Bound
+// by HBM: 1,500 pages of four layers' latent and index caches, 937 MB, 145.7 us,
+// 6.43 TB/s, 96 % of a plain copy; 8 pages of one layer 2.4 us on the device.
 constexpr int kCopyThreads = 256, kCopyWarps = kCopyThreads / 32;
 constexpr int kCopyLoads = 8, kPieceUnits = 32 * kCopyLoads;
 
@@ -195,7 +199,10 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
 
 // ---------------------------------------------------------------- pool, any size
 // One launch clears the bitmap (and cuts the released requests), one marks, one
-// ranks and lists, and for a compaction one rewrites the table.
+// ranks and lists, and for a compaction one rewrites the table.  Bound by the
+// launches' latency and the marks' atomics: 2,048 requests of up to 512 pages in
+// a pool of 482,000 (4 MB) 12.4 us for a release, 21 us for a compaction in a
+// pool of 682,000, on the device.
 constexpr int kPoolThreads = 256, kPoolWarps = kPoolThreads / 32;
 constexpr int kListThreads = 1024, kListWarps = kListThreads / 32;
 constexpr int kEntries = 8;  // table entries that a lane has under way
@@ -421,7 +428,9 @@ __global__ void __launch_bounds__(kPoolThreads) pool_rewrite_kernel(const PoolPa
 // entries, each in a bitmap of its own in shared memory; CTA r ORs everyone's
 // slice r and hands it to everyone; then each CTA has the whole bitmap, ranks
 // it, lists its slice and rewrites its requests' rows.  No workspace, nothing to
-// clear in memory, two or three cluster barriers.
+// clear in memory, two or three cluster barriers.  64 requests of up to 256 pages
+// 4.9 us for a release; 32 of up to 16 pages 6.2 us for a compaction, on the
+// device: latency.
 constexpr int kClusterThreads = 1024, kClusterWarps = kClusterThreads / 32;
 // What one cluster takes: more is faster on all SMs, in more launches.  (256
 // requests of up to 256 pages: release 7.1 us, 8.0 in three launches; compaction
