@@ -122,6 +122,21 @@ def test_blocks_and_groups_of_many_requests(reqs):
     run_case(reqs, [(70, [((7 * i) % 5 % 3, 1 + (37 * i) % 40) for i in range(reqs)]), (0, [(1, 5)] * 40)], heads=2, kv_heads=2)
 
 
+def test_long_runs():
+    # 16 tiles a CTA and more: equal runs over blocks of other lengths, and a block's own, with many requests
+    groups = [(1001 + 1143 * i, [(4, 5 + (331 * (6 * i + j)) % 700) for j in range(3)]) for i in range(8)]
+    run_case(17, groups, heads=40, kv_heads=8)
+    run_case(18, [(16000, [(1, 1 + (53 * i) % 300) for i in range(40)])], heads=32, kv_heads=4, page=128)
+    run_case(19, [(30000, [(1, 1)] * 33)], heads=32, kv_heads=2, dtype=FP16)
+
+
+@pytest.mark.parametrize("groups", [33, 76, 152, 153])
+def test_blocks_of_alike_lengths(groups):
+    # as many CTAs as blocks, or a whole number of them each
+    run_case(groups, [(64, [(1, 200 + i % 3)]) for i in range(groups)], heads=4, kv_heads=1)
+    run_case(groups, [(0, [(1, 1)]) for i in range(groups)], heads=1, kv_heads=1)
+
+
 def test_long_requests_without_a_prefix():
     run_case(12, [(0, [(1, 9000), (2, 3000), (1, 17)])], heads=8, kv_heads=2)
 
