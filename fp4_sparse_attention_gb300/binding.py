@@ -908,9 +908,8 @@ def fp4idx_fork_requests(parent: torch.Tensor, child: torch.Tensor, cached_len: 
     width = _table(block_table, B, dev)
     _on_current(dev)
     if out is None:
-        i32, where = torch.int32, cached_len.device
-        src, dst = torch.empty(N, dtype=i32, device=where), torch.empty(N, dtype=i32, device=where)
-        taken = torch.empty(1, dtype=i32, device=where)
+        src, dst = torch.empty_like(parent), torch.empty_like(parent)
+        taken = torch.empty(1, dtype=torch.int32, device=cached_len.device)
     else:
         src, dst, taken = _given(out, ("copy_src", N, dev), ("copy_dst", N, dev), ("pages_taken", 1, dev))
     if num_pages is None:
@@ -1025,9 +1024,8 @@ def fp4idx_compact_pages(cached_len: torch.Tensor, block_table: torch.Tensor, pa
             raise ValueError("out_table must be at least as wide as block_table")
     _on_current(dev)
     if out is None:
-        i32 = torch.int32
-        src, dst = torch.empty(max_moves, dtype=i32, device=where), torch.empty(max_moves, dtype=i32, device=where)
-        moves, extent = torch.empty(1, dtype=i32, device=where), torch.empty(1, dtype=i32, device=where)
+        src, moves = torch.empty(max_moves, dtype=torch.int32, device=where), torch.empty(1, dtype=torch.int32, device=where)
+        dst, extent = torch.empty_like(src), torch.empty_like(moves)
     else:
         src, dst, moves, extent = _given(out, ("copy_src", max_moves, dev), ("copy_dst", max_moves, dev), ("num_moves", 1, dev),
                                          ("extent", 1, dev))
