@@ -121,12 +121,13 @@ __device__ __forceinline__ int group_div(const AttnParams& p, int64_t x) {
 }
 
 // Requests [first, second) of a group.
-__device__ __forceinline__ int2 group_requests(const SharedParams& sp, int g) {
-  const int lo = min(max(__ldg(sp.group_offsets + g), 0), sp.a.num_seqs);
-  return make_int2(lo, min(max(__ldg(sp.group_offsets + g + 1), lo), sp.a.num_seqs));
+__device__ __forceinline__ int2 group_requests(const int32_t* offsets, int g, int num_seqs) {
+  const int lo = min(max(offsets[g], 0), num_seqs);
+  return make_int2(lo, min(max(offsets[g + 1], lo), num_seqs));
 }
 
 constexpr int kPlanThreads = 256, kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanReqs = 512, kPlanRows = 2048;  // requests (and groups), rows that a CTA's shared memory has room for
 
 // A warp, or with many requests a group (WIDE) a CTA, plans a block: its spans,
 // its tiles and what its rows see: a warp takes 32 requests at a time, 1.4 us.
@@ -139,19 +140,38 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   pdl_launch_dependents();
   const SharedParams& sp = pl.sp;
   const AttnParams& p = sp.a;
+  // What a small call gives comes to shared memory in one round trip: read where
+  // it is needed, it is a chain of five.  (48 requests: 81.5 -> 80.7 us; 16: 35.8
+  // -> 35.1; two, whose arrays are a line each: 13.9 -> 14.1.)
+  __shared__ int32_t cu_q_s[kPlanReqs + 1], cu_k_s[kPlanReqs + 1], qo_s[kPlanReqs], groups_s[kPlanReqs + 1], prefix_s[kPlanReqs], seen_s[kPlanRows];
+  const int32_t *cu_q = p.cu_seqlens_q, *cu_k = p.cu_seqlens_k, *qo = p.qo_offset, *groups = sp.group_offsets, *prefix_lens = sp.prefix_len;
+  const int32_t* visible = p.visible_len;
+  if (p.num_seqs <= kPlanReqs && sp.num_groups <= kPlanReqs) {
+    const auto stage = [&](int32_t* to, const int32_t*& from, int n) {
+      for (int x = threadIdx.x; x < n; x += kPlanThreads) cp_async_4(smem_u32(to + x), from + x);
+      from = to;
+    };
+    stage(groups_s, groups, sp.num_groups + 1);
+    stage(prefix_s, prefix_lens, sp.num_groups);
+    stage(cu_q_s, cu_q, p.num_seqs + 1);
+    stage(cu_k_s, cu_k, p.num_seqs + 1);
+    if (qo) stage(qo_s, qo, p.num_seqs);
+    if (visible && p.num_rows <= kPlanRows) stage(seen_s, visible, p.num_rows);
+    cp_async_wait_all();
+    __syncthreads();
+  }
   const int lane = threadIdx.x & 31;
   const int warp = WIDE ? threadIdx.x >> 5 : 0, i = WIDE ? blockIdx.x : blockIdx.x * kPlanWarps + (threadIdx.x >> 5);
   if (i >= pl.blocks) return;
   const int g = i / pl.blocks_per_group;
-  const int2 reqs = group_requests(sp, g);
+  const int2 reqs = group_requests(groups, g, p.num_seqs);
   const int n_reqs = reqs.y - reqs.x;
-  // (loads that need nothing from each other stand together: a block's plan is a
-  // chain of five of them)
+  // (loads that need nothing from each other stand together)
   const int step = (n_reqs + 31) >> 5;
-  const int probe = lane * step < n_reqs ? __ldg(p.cu_seqlens_q + reqs.x + lane * step) : INT32_MAX;
-  const int first_row = __ldg(p.cu_seqlens_q + reqs.x), end_row = __ldg(p.cu_seqlens_q + reqs.y);
-  const int prefix_len = __ldg(sp.prefix_len + g);
-  const int first_keys = reqs.x < sp.a.num_seqs ? __ldg(p.cu_seqlens_k + reqs.x + 1) - __ldg(p.cu_seqlens_k + reqs.x) : 0;
+  const int probe = lane * step < n_reqs ? cu_q[reqs.x + lane * step] : INT32_MAX;
+  const int first_row = cu_q[reqs.x], end_row = cu_q[reqs.y];
+  const int prefix_len = prefix_lens[g];
+  const int first_keys = reqs.x < sp.a.num_seqs ? cu_k[reqs.x + 1] - cu_k[reqs.x] : 0;
   Block blk = {};
   blk.row0 = max(0, first_row);
   const int rows = min(max(min(end_row, p.num_rows) - blk.row0, 0), sp.max_group_rows);
@@ -173,14 +193,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   int a1 = reqs.x + max(0, __popc(__ballot_sync(0xffffffffu, probe <= r1 - 1)) - 1) * step;
   for (int n = step; n > 1;) {
     const int by = (n + 31) >> 5, at = lane * by;
-    const int x0 = at < n && a0 + at < reqs.y ? __ldg(p.cu_seqlens_q + a0 + at) : INT32_MAX;
-    const int x1 = at < n && a1 + at < reqs.y ? __ldg(p.cu_seqlens_q + a1 + at) : INT32_MAX;
+    const int x0 = at < n && a0 + at < reqs.y ? cu_q[a0 + at] : INT32_MAX;
+    const int x1 = at < n && a1 + at < reqs.y ? cu_q[a1 + at] : INT32_MAX;
     a0 += max(0, __popc(__ballot_sync(0xffffffffu, x0 <= r0)) - 1) * by;
     a1 += max(0, __popc(__ballot_sync(0xffffffffu, x1 <= r1 - 1)) - 1) * by;
     n = by;
   }
   const auto key_count = [&](int a) {
-    return min(max(0, __ldg(p.cu_seqlens_k + a + 1) - __ldg(p.cu_seqlens_k + a)), p.max_seqlen_k);
+    return min(max(0, cu_k[a + 1] - cu_k[a]), p.max_seqlen_k);
   };
   const int prefix = max(0, min(prefix_len, min(max(0, first_keys), p.max_seqlen_k)));
   // (a block has 1 + its requests spans at most, and the next block's first
@@ -228,15 +248,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     int from = 0, to = 0, k_len = 0, hi = 0;  // its rows of the block, its keys, the most that a row sees
     int64_t off = 0;                          // causal: row t sees t + off
     if (a <= a1) {
-      const int q0 = __ldg(p.cu_seqlens_q + a), q1 = __ldg(p.cu_seqlens_q + a + 1);
+      const int q0 = cu_q[a], q1 = cu_q[a + 1];
       from = max(q0, r0);
       to = min(q1, r1);
       k_len = key_count(a);
-      off = (p.qo_offset ? static_cast<int64_t>(__ldg(p.qo_offset + a)) : static_cast<int64_t>(k_len) - (q1 - q0)) + 1 - q0;
+      off = (qo ? static_cast<int64_t>(qo[a]) : static_cast<int64_t>(k_len) - (q1 - q0)) + 1 - q0;
     }
     const auto sees = [&](int t, int n, int64_t o) {
       int64_t v = n;
-      if (p.visible_len) v = __ldg(p.visible_len + t);
+      if (visible) v = visible[t];
       else if (p.causal) v = t + o;
       return static_cast<int>(v < 0 ? 0 : v > n ? n : v);
     };
@@ -387,8 +407,8 @@ __device__ __forceinline__ void cp_async_arrive_extra(uint32_t bar) {
 // Rows that no group holds: zeros and -inf, a (row, head) pair of a CTA at a time.
 __device__ __forceinline__ void clear_other_rows(const SharedParams& sp, int lane) {
   const AttnParams& p = sp.a;
-  const int first = min(max(0, __ldg(p.cu_seqlens_q + group_requests(sp, 0).x)), p.num_rows);
-  const int last = min(max(first, __ldg(p.cu_seqlens_q + group_requests(sp, sp.num_groups - 1).y)), p.num_rows);
+  const int first = min(max(0, __ldg(p.cu_seqlens_q + group_requests(sp.group_offsets, 0, p.num_seqs).x)), p.num_rows);
+  const int last = min(max(first, __ldg(p.cu_seqlens_q + group_requests(sp.group_offsets, sp.num_groups - 1, p.num_seqs).y)), p.num_rows);
   const int64_t rows = first + (p.num_rows - last), pairs = rows * p.num_heads;
 #pragma unroll 1
   for (int64_t x = blockIdx.x; x < pairs; x += gridDim.x) {
