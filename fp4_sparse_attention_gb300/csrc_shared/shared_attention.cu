@@ -37,13 +37,13 @@
 // Bounds and figures (bf16, cold caches).  A tile of a full block is 16.8 MFLOP for
 // 64 KB: with every row of 256 pairs on the same keys the tensor pipe and the
 // softmax beside it bound it (2,048 rows x 32/8 heads on 8,191 + 512..640 keys:
-// 195.5 us, 1,460 TFLOP/s, 76 % of a burst of large library products; a tile takes
+// 195.2 us, 1,463 TFLOP/s, 76 % of a burst of large library products; a tile takes
 // 2,700 cycles, of which its products need 2,180); with keys of a request's own or
-// few rows a group HBM does (8 groups x 24 rows x 40/8 heads, 365 MB: 81.5 us,
+// few rows a group HBM does (8 groups x 24 rows x 40/8 heads, 365 MB: 80.7 us,
 // 6.4 TB/s while the runs last; no prefix, 64 requests x 8,192 keys, 1,075 MB:
 // 171 us, 6.3 TB/s, 94 % of a copy).  What a short call pays: 2 us plan, 2 us until a
 // run is known, 2 us for the first pages and keys, 2 us output, 4-7 us join (2
-// requests on 200 keys 13.7 us, 64 samples of 32,768 keys 54 us).
+// requests on 200 keys 13.8 us, 64 samples of 32,768 keys 53 us).
 #include <algorithm>
 #include <atomic>
 #include <cstddef>
