@@ -611,7 +611,8 @@ fp4idx_status_t fp4idx_build_tables(const int32_t* cached_len, const int32_t* ne
  * Everything else as for fp4idx_attention_t: visibility of each row, rows
  * behind the requests', page errors, values that nobody may see.  A position
  * below prefix_len that some row of the group sees must hold finite values for
- * all of them.
+ * all of them; what a request has behind it is used for that request's rows
+ * alone, and infinite or NaN values there change no other request's result.
  * Workspace: fp4idx_shared_attention_workspace_bytes(), 16-byte aligned,
  * uninitialised.  The result is the same from call to call.  No allocation, no
  * synchronisation; graph-capturable; replays see updated device metadata.
