@@ -22,9 +22,14 @@ The functions keep the C names:
     fp4idx_release_pages(...) -> (free_pages, num_free)
     fp4idx_compact_pages(...) -> (new_table, copy_src, copy_dst, num_moves, extent)
     fp4idx_get_error(clear=True, stream=None) -> int
+
+A call runs on `stream` (default: the current one).  Tensors that it makes
+itself, outputs and scratch, are made there; the ones that it is given must be
+ready for that stream, as for any work that is moved to another stream.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -281,6 +286,27 @@ def _stream(stream):
     return _raw_stream(_raw_device())
 
 
+def _made_on(stream):
+    """Context in which tensors are made for a call on `stream` (None: the current one).  The caching allocator hands a
+    block out again as soon as it is freed, to work that is ordered behind its last use on the block's own stream only."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream.cuda_stream))
+
+
+def _on_stream(stream, call, *args, given=()):
+    """call(*args), which makes tensors, with `stream` as the current one.  The new ones are recorded for the stream that
+    was current, where the caller goes on with them; `given` were there before."""
+    here = torch.cuda.current_stream()
+    with _made_on(stream):
+        got = call(*args)
+    given = [x.data_ptr() for x in given if x is not None]
+    for x in got if isinstance(got, tuple) else (got,):
+        if isinstance(x, torch.Tensor) and x.data_ptr() not in given:
+            x.record_stream(here)
+    return got
+
+
 class DeviceProblem:
     """Device tensors of one scorer problem plus its fp4idx_problem_t.
 
@@ -381,6 +407,8 @@ def fp4idx_logits(problem: DeviceProblem, w: torch.Tensor, ld: Optional[int] = N
     lib = load_library()
     if ld is None:
         ld = out.stride(0) if out is not None else (problem.max_seqlen_k + 3) // 4 * 4
+    if out is None and stream is not None:
+        return _on_stream(stream, fp4idx_logits, problem, w, ld)
     if out is None:
         out = torch.empty((problem.num_rows, ld), dtype=torch.float32, device=w.device)
     _check(lib.fp4idx_logits(ctypes.byref(problem.c), _ptr(w), w.stride(0), _ptr(out), ld, _stream(stream)),
@@ -391,6 +419,8 @@ def fp4idx_logits(problem: DeviceProblem, w: torch.Tensor, ld: Optional[int] = N
 def fp4idx_block_scores(problem: DeviceProblem, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Per-128-key block max of the unweighted dot: [Hq, ceil(max_seqlen_k/128), T] fp32."""
     lib = load_library()
+    if out is None and stream is not None:
+        return _on_stream(stream, fp4idx_block_scores, problem)
     if out is None:
         out = torch.empty((problem.num_heads, problem.ktiles, problem.num_rows), dtype=torch.float32,
                           device=problem.q.device)
@@ -408,6 +438,9 @@ def fp4idx_block_topk(scores: torch.Tensor, k: int, indices: Optional[torch.Tens
         raise ValueError("scores must be a contiguous [Hq, Ktiles, T] float32 tensor")
     H, Kt, T = scores.shape
     dev = scores.device
+    if stream is not None and (indices is None or values is None or valid_count is None):
+        return _on_stream(stream, fp4idx_block_topk, scores, k, indices, values, valid_count,
+                          given=(indices, values, valid_count))
     if indices is None:
         indices = torch.empty((H, T, k), dtype=torch.int32, device=dev)
     if values is None:
@@ -429,6 +462,8 @@ def fp4idx_topk_slots(problem: DeviceProblem, indices: torch.Tensor, ncols: Opti
         raise ValueError("indices must be a contiguous [T, k] int32 tensor")
     T, k = indices.shape
     ncols = k if ncols is None else ncols
+    if slots is None and stream is not None:
+        return _on_stream(stream, fp4idx_topk_slots, problem, indices, ncols)
     if slots is None:
         slots = torch.empty((T, ncols), dtype=torch.int32, device=indices.device)
     bits = ctypes.c_int32(0)
@@ -466,6 +501,8 @@ def fp4idx_quantize_q(q: torch.Tensor, codes: Optional[torch.Tensor] = None,
     T, H, D = q.shape
     if q.dtype != torch.bfloat16 or D != 128 or q.stride(2) != 1 or q.stride(1) != 128:
         raise ValueError("q must be bfloat16 [T, H, 128] with dense heads")
+    if stream is not None and (codes is None or scales is None):
+        return _on_stream(stream, fp4idx_quantize_q, q, codes, scales, given=(codes, scales))
     if codes is None:
         codes = torch.empty((T, H, 64), dtype=torch.uint8, device=q.device)
     if scales is None:
@@ -486,6 +523,8 @@ def fp4idx_pages_from_token_table(req: torch.Tensor, req_table: torch.Tensor, pa
     lib = load_library()
     B, cap = req_table.shape
     dev = req_table.device
+    if out is None and stream is not None:
+        return _on_stream(stream, fp4idx_pages_from_token_table, req, req_table, page_size, num_pages)
     if out is None:
         cu_q = torch.empty((B + 1,), dtype=torch.int32, device=dev)
         cu_k = torch.empty((B + 1,), dtype=torch.int32, device=dev)
@@ -514,13 +553,17 @@ def fp4idx_topk(problem: DeviceProblem, w: torch.Tensor, k: int, sorted: bool = 
     lib = load_library()
     dev = w.device
     T = problem.num_rows
+    need = fp4idx_topk_workspace_bytes(problem, k)
+    if stream is not None and (indices is None or (values is None and want_values) or valid_count is None or
+                               workspace is None or workspace.numel() < need):
+        return _on_stream(stream, fp4idx_topk, problem, w, k, sorted, indices, values, valid_count, workspace,
+                          want_values, streaming, given=(indices, values, valid_count))
     if indices is None:
         indices = torch.empty((T, k), dtype=torch.int32, device=dev)
     if values is None and want_values:
         values = torch.empty((T, k), dtype=torch.float32, device=dev)
     if valid_count is None:
         valid_count = torch.empty((T,), dtype=torch.int32, device=dev)
-    need = fp4idx_topk_workspace_bytes(problem, k)
     if workspace is None or workspace.numel() < need:
         workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=dev)
     flags = (FP4IDX_TOPK_SORTED if sorted else 0) | (FP4IDX_TOPK_STREAMING if streaming else 0)
@@ -538,6 +581,9 @@ def fp4idx_logits_topk(problem: DeviceProblem, w: torch.Tensor, k: int, sorted: 
     lib = load_library()
     dev = w.device
     T = problem.num_rows
+    if stream is not None and (logits is None or indices is None or values is None or valid_count is None):
+        return _on_stream(stream, fp4idx_logits_topk, problem, w, k, sorted, logits, ld, indices, values, valid_count,
+                          given=(logits, indices, values, valid_count))
     if logits is None:
         ld = ld or (problem.max_seqlen_k + 3) // 4 * 4
         logits = torch.empty((T, ld), dtype=torch.float32, device=dev)
@@ -594,6 +640,8 @@ class DeviceAttention:
     tensors again.  The object holds pointers: rebuild it when a tensor moves.
     Calls on one object use its one workspace and must be ordered (one stream, or
     events between streams); streams that run at the same time need an object each.
+    What is allocated here belongs to the stream that is current here: a call on
+    another one must be ordered behind it.
     """
 
     def __init__(self, *, q, k, cu_seqlens_q, cu_seqlens_k, block_table, max_seqlen_q: int, max_seqlen_k: int,
@@ -789,6 +837,8 @@ def fp4idx_build_tables(cached_len: torch.Tensor, new_len: torch.Tensor, block_t
         raise ValueError("block_table must not be a view of wider rows: new pages are bounded by the rows' distance")
     if not (cached_len.get_device() == new_len.get_device() == block_table.get_device() == free_pages.get_device() >= 0):
         raise ValueError(_ONE_DEVICE)  # -1: host
+    if out is None and stream is not None:
+        return _on_stream(stream, fp4idx_build_tables, cached_len, new_len, block_table, free_pages, page_size, num_rows, num_pages)
     if out is None:
         dev = cached_len.device
         cu_q = torch.empty((B + 1,), dtype=i32, device=dev)
@@ -907,6 +957,8 @@ def fp4idx_fork_requests(parent: torch.Tensor, child: torch.Tensor, cached_len: 
         raise ValueError("parent, child and fork_len must have one length")
     width = _table(block_table, B, dev)
     _on_current(dev)
+    if out is None and stream is not None:
+        return _on_stream(stream, fp4idx_fork_requests, parent, child, cached_len, block_table, free_pages, page_size, fork_len, num_pages)
     if out is None:
         src, dst = torch.empty_like(parent), torch.empty_like(parent)
         taken = torch.empty(1, dtype=torch.int32, device=cached_len.device)
@@ -977,9 +1029,9 @@ def _with_workspace(call, workspace, num_pages, num_reqs, width, where, stream):
     need = _pages_workspace(num_pages, num_reqs, width)
     if need == 0:
         return call(None, 0)
-    workspace = torch.empty(need, dtype=torch.uint8, device=where)
-    if stream is not None:
-        workspace.record_stream(stream)  # it is freed on return, perhaps before that stream comes to it
+    # (made on the stream of the call, where whatever gets it next is ordered behind)
+    with _made_on(stream):
+        workspace = torch.empty(need, dtype=torch.uint8, device=where)
     return call(workspace.data_ptr(), workspace.numel())
 
 
@@ -994,6 +1046,8 @@ def fp4idx_release_pages(requests: Optional[torch.Tensor], cached_len: torch.Ten
         raise ValueError("requests and keep_len must have one length")
     width = _table(block_table, B, dev)
     _on_current(dev)
+    if out is None and stream is not None:
+        return _on_stream(stream, fp4idx_release_pages, requests, cached_len, block_table, page_size, num_pages, keep_len, None, workspace)
     if out is None:
         free, count = torch.empty(num_pages, dtype=torch.int32, device=where), torch.empty(1, dtype=torch.int32, device=where)
     else:
@@ -1023,6 +1077,9 @@ def fp4idx_compact_pages(cached_len: torch.Tensor, block_table: torch.Tensor, pa
         if new_width < width:
             raise ValueError("out_table must be at least as wide as block_table")
     _on_current(dev)
+    if out is None and stream is not None:
+        return _on_stream(stream, fp4idx_compact_pages, cached_len, block_table, page_size, num_pages, max_moves, out_table, None, workspace,
+                          given=(to,))
     if out is None:
         src, moves = torch.empty(max_moves, dtype=torch.int32, device=where), torch.empty(1, dtype=torch.int32, device=where)
         dst, extent = torch.empty_like(src), torch.empty_like(moves)
