@@ -206,6 +206,11 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
 constexpr int kPoolThreads = 256, kPoolWarps = kPoolThreads / 32;
 constexpr int kListThreads = 1024, kListWarps = kListThreads / 32;
 constexpr int kEntries = 8;  // table entries that a lane has under way
+// Runs of 32 x kEntries entries of a row, which may be as wide as 32 bits allow.
+// (An entry's number then stays below 2^31, too: a run begins at a multiple of 256.)
+__host__ __device__ constexpr int row_runs(int32_t width) {
+  return static_cast<int>((static_cast<int64_t>(width) + 32 * kEntries - 1) / (32 * kEntries));
+}
 
 // Words of the bitmap, by fours.
 __host__ __device__ constexpr int64_t pool_words(int64_t num_pages) { return (num_pages + 127) / 128 * 4; }
@@ -307,7 +312,7 @@ __global__ void __launch_bounds__(kPoolThreads) pool_mark_kernel(const PoolParam
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   uint32_t err = 0;
-  const int parts = (p.width + 32 * kEntries - 1) / (32 * kEntries);
+  const int parts = row_runs(p.width);
   const int64_t work = static_cast<int64_t>(p.num_reqs) * parts;
   for (int64_t w = static_cast<int64_t>(blockIdx.x) * kPoolWarps + wid; w < work;
        w += static_cast<int64_t>(gridDim.x) * kPoolWarps) {
@@ -414,7 +419,7 @@ __global__ void __launch_bounds__(kPoolThreads) pool_rewrite_kernel(const PoolPa
            __popc(mine & ((1u << (page & 31)) - 1));
   };
   uint32_t err = 0;  // (the marks have reported it)
-  const int parts = (p.width + 32 * kEntries - 1) / (32 * kEntries);
+  const int parts = row_runs(p.width);
   const int64_t work = static_cast<int64_t>(p.num_reqs) * parts;
   for (int64_t w = static_cast<int64_t>(blockIdx.x) * kPoolWarps + wid; w < work;
        w += static_cast<int64_t>(gridDim.x) * kPoolWarps) {
@@ -484,7 +489,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) pool_cluster_kernel(const 
   if (p.num_released > 0)
     for (int k = tid; k < reqs; k += kClusterThreads) p.cached_len[me + k * ctas] = len[k];
   // marks: a warp takes up to 256 entries of a row
-  const int parts = (p.width + 32 * kEntries - 1) / (32 * kEntries);
+  const int parts = row_runs(p.width);
   for (int w = wid; w < reqs * parts; w += kClusterWarps) {
     const int k = w / parts, j0 = (w - k * parts) * 32 * kEntries + lane;
     mark_entries(p, p.block_table + static_cast<int64_t>(me + k * ctas) * p.table_stride, j0, held_entries(p, len[k], &err), bits, &err);
@@ -559,7 +564,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) pool_cluster_kernel(const 
 }
 
 bool in_one_cluster(const PoolParams& p) {
-  return p.num_pages <= kClusterPages && static_cast<int64_t>(p.num_reqs) * ((p.width + 32 * kEntries - 1) / (32 * kEntries)) <= kClusterRuns;
+  return p.num_pages <= kClusterPages && static_cast<int64_t>(p.num_reqs) * (row_runs(p.width)) <= kClusterRuns;
 }
 
 template <bool COMPACT>
@@ -585,7 +590,7 @@ cudaError_t launch_cluster(const PoolParams& p, cudaStream_t stream) {
 int64_t round16(int64_t n) { return (n + 15) & ~int64_t{15}; }
 
 unsigned entry_ctas(const PoolParams& p, int sms) {
-  const int64_t parts = static_cast<int64_t>(p.num_reqs) * ((p.width + 32 * kEntries - 1) / (32 * kEntries));
+  const int64_t parts = static_cast<int64_t>(p.num_reqs) * (row_runs(p.width));
   return static_cast<unsigned>(std::min<int64_t>(8 * static_cast<int64_t>(sms), (parts + kPoolWarps - 1) / kPoolWarps));
 }
 
