@@ -137,7 +137,12 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkParams p) 
     }
     if (f.part) {
       if (before < p.num_free) dst = max(-1, __ldg(p.free_pages + before));
-      if (dst < 0) err |= kErrLengths;
+      if (dst < 0) {
+        err |= kErrLengths;
+      } else if (dst >= p.num_pages) {
+        err |= kErrPageRange;
+        dst = -1;
+      }
       if (lane == 0) to[f.full] = dst;
       src = from[f.full];
       if (src < 0 || src >= p.num_pages) {

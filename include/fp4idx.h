@@ -648,10 +648,12 @@ fp4idx_status_t fp4idx_shared_prefix_attention(const fp4idx_shared_attention_t* 
  * call).  Refused, with -1 and -1 and the child left as it was:
  * FP4IDX_ERR_REQUESTS -- a number not below num_reqs; a child that an earlier
  * fork of the call names (counted as taking its page) or that is the parent of
- * any fork; FP4IDX_ERR_LENGTHS -- a parent longer than its table row.  Without a free page left (behind
- * num_free, or a negative entry: what fp4idx_release_pages leaves behind its
- * list) the child's unfinished page is entered as -1 and FP4IDX_ERR_LENGTHS is set.  A parent's
- * unfinished page outside [0, num_pages) gives -1 and -1 and
+ * any fork; FP4IDX_ERR_LENGTHS -- a parent longer than its table row.
+ * Without a free page left (behind num_free, or a negative entry: what
+ * fp4idx_release_pages leaves behind its list) the child's unfinished page is
+ * entered as -1 and FP4IDX_ERR_LENGTHS is set; with an entry of free_pages that
+ * is not below num_pages it is entered as -1, too, and FP4IDX_ERR_PAGE_RANGE is
+ * set.  A parent's unfinished page outside [0, num_pages) gives -1 and -1 and
  * FP4IDX_ERR_PAGE_RANGE (full pages are shared as they are).  Negative lengths
  * count as 0.  A call repeated on its own results enters the same pages again.
  * One launch, no workspace, graph-capturable.  Supported: page_size 64 or 128,
