@@ -174,7 +174,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   const int first_keys = reqs.x < sp.a.num_seqs ? cu_k[reqs.x + 1] - cu_k[reqs.x] : 0;
   Block blk = {};
   blk.row0 = max(0, first_row);
-  const int rows = min(max(min(end_row, p.num_rows) - blk.row0, 0), sp.max_group_rows);
+  const int group_rows = max(min(end_row, p.num_rows) - blk.row0, 0), rows = min(group_rows, sp.max_group_rows);
+  if (group_rows > rows && i == g * pl.blocks_per_group && warp == 0 && lane == 0) atomicOr(p.err, kErrLengths);
   const int64_t pair0 = static_cast<int64_t>(i - g * pl.blocks_per_group) * kBlockPairs;
   const int64_t pairs = min(static_cast<int64_t>(rows) * p.group - pair0, static_cast<int64_t>(kBlockPairs));
   if (pairs <= 0) {

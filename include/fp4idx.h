@@ -81,7 +81,9 @@ typedef enum fp4idx_status {
                                        non-decreasing                            */
 #define FP4IDX_ERR_LENGTHS 0x8u     /* fp4idx_build_tables: a negative length, more rows
                                        than the caller's row count, a request longer than
-                                       its table row, or too few free pages         */
+                                       its table row, or too few free pages; the same of
+                                       the page operations; fp4idx_shared_prefix_attention:
+                                       a group with more than max_group_rows rows   */
 #define FP4IDX_ERR_REQUESTS 0x10u   /* fp4idx_fork_requests, fp4idx_release_pages: a request
                                        number past the table; a fork's child that an earlier
                                        fork names or that is some fork's parent     */
@@ -607,7 +609,8 @@ fp4idx_status_t fp4idx_build_tables(const int32_t* cached_len, const int32_t* ne
  *             own entries below it are read only for the 64 positions that it
  *             ends in and must be valid there.
  *   max_group_rows  host upper bound of a group's query rows; it must hold for
- *             the device data.
+ *             the device data.  The rows of a group past it are not computed and
+ *             their outputs not written, which FP4IDX_ERR_LENGTHS reports.
  * Everything else as for fp4idx_attention_t: visibility of each row, rows
  * behind the requests', page errors, values that nobody may see.  A position
  * below prefix_len that some row of the group sees must hold finite values for
