@@ -171,7 +171,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   const int probe = lane * step < n_reqs ? cu_q[reqs.x + lane * step] : INT32_MAX;
   const int first_row = cu_q[reqs.x], end_row = cu_q[reqs.y];
   const int prefix_len = prefix_lens[g];
-  const int first_keys = reqs.x < sp.a.num_seqs ? cu_k[reqs.x + 1] - cu_k[reqs.x] : 0;
+  const auto key_count = [&](int a) {
+    return min(max(0, cu_k[a + 1] - cu_k[a]), p.max_seqlen_k);
+  };
+  int keys = lane < n_reqs ? key_count(reqs.x + lane) : -1;  // of the group's first requests
   Block blk = {};
   blk.row0 = max(0, first_row);
   const int group_rows = max(min(end_row, p.num_rows) - blk.row0, 0), rows = min(group_rows, sp.max_group_rows);
@@ -200,10 +203,24 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     a1 += max(0, __popc(__ballot_sync(0xffffffffu, x1 <= r1 - 1)) - 1) * by;
     n = by;
   }
-  const auto key_count = [&](int a) {
-    return min(max(0, cu_k[a + 1] - cu_k[a]), p.max_seqlen_k);
-  };
-  const int prefix = max(0, min(prefix_len, min(max(0, first_keys), p.max_seqlen_k)));
+  // The prefix is read through the first request whose keys reach its end, or
+  // else the first of the longest ones: requests that have ended, the group's
+  // first one among them, leave it shared.
+  const int wanted = max(0, min(prefix_len, p.max_seqlen_k));
+  uint32_t reach = __ballot_sync(0xffffffffu, keys >= wanted);
+  int through = reqs.x + __ffs(reach) - 1, prefix = wanted;
+  if (reach == 0) {
+    prefix = -1;
+    for (int x = 0; reach == 0 && x < n_reqs; x += 32) {
+      if (x > 0) keys = x + lane < n_reqs ? key_count(reqs.x + x + lane) : -1;
+      const int most = min(wanted, __reduce_max_sync(0xffffffffu, keys));
+      reach = __ballot_sync(0xffffffffu, keys >= wanted);
+      if (most > prefix) {
+        prefix = most;
+        through = reqs.x + x + __ffs(__ballot_sync(0xffffffffu, keys >= most)) - 1;
+      }
+    }
+  }
   // (a block has 1 + its requests spans at most, and the next block's first
   // request is not before this one's last)
   blk.span0 = 2 * i + a0;
@@ -302,7 +319,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     for (int w = 0; w < warps; ++w) top = max(top, sums[w][2]);
   }
   Span s = {};
-  s.req = reqs.x;
+  s.req = through;
   s.hi = min(prefix, top);
   s.tiles = (s.hi + kTile - 1) / kTile;
   if (s.tiles == 0 && blk.tiles == 0) s.tiles = 1;  // rows without keys are written, too

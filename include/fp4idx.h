@@ -603,11 +603,13 @@ fp4idx_status_t fp4idx_build_tables(const int32_t* cached_len, const int32_t* ne
  *             nearer end.  Requests before the first or behind the last group
  *             are in none: their rows get out = 0 and lse = -inf.)
  *   prefix_len    [num_groups] int32, device: the first prefix_len[g] positions
- *             are the same keys and values for every request of the group, and
- *             are read through the table row of its first request, whose key
- *             count bounds them (negative: 0).  Any length; the other requests'
- *             own entries below it are read only for the 64 positions that it
- *             ends in and must be valid there.
+ *             are the same keys and values for every request of the group, as
+ *             far as it has them (negative: 0).  They are read through the table
+ *             row of the first request whose keys reach that far, or else of the
+ *             longest one (the first of several), whose key count then bounds
+ *             them: requests that have ended (0 keys) may stay in their group.
+ *             Any length; the other requests' own entries below it are read only
+ *             for the 64 positions that it ends in and must be valid there.
  *   max_group_rows  host upper bound of a group's query rows; it must hold for
  *             the device data.  The rows of a group past it are not computed and
  *             their outputs not written, which FP4IDX_ERR_LENGTHS reports.
