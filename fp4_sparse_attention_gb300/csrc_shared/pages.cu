@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) pool_cluster_kernel(const 
 }
 
 bool in_one_cluster(const PoolParams& p) {
-  return p.num_pages <= kClusterPages && static_cast<int64_t>(p.num_reqs) * (row_runs(p.width)) <= kClusterRuns;
+  return p.num_pages <= kClusterPages && static_cast<int64_t>(p.num_reqs) * row_runs(p.width) <= kClusterRuns;
 }
 
 template <bool COMPACT>
@@ -595,7 +595,7 @@ cudaError_t launch_cluster(const PoolParams& p, cudaStream_t stream) {
 int64_t round16(int64_t n) { return (n + 15) & ~int64_t{15}; }
 
 unsigned entry_ctas(const PoolParams& p, int sms) {
-  const int64_t parts = static_cast<int64_t>(p.num_reqs) * (row_runs(p.width));
+  const int64_t parts = static_cast<int64_t>(p.num_reqs) * row_runs(p.width);
   return static_cast<unsigned>(std::min<int64_t>(8 * static_cast<int64_t>(sms), (parts + kPoolWarps - 1) / kPoolWarps));
 }
 
@@ -610,7 +610,7 @@ cudaError_t mark(PoolParams* p, int sms, void* workspace, cudaStream_t stream) {
   return launch_dependent(pool_mark_kernel, dim3(entry_ctas(*p, sms)), kPoolThreads, stream, *p);
 }
 
-// A CTA sums the whole bitmap: one for each 256 groups of four words at most.
+// A CTA sums the whole bitmap: one for each 64 groups of four words at most.
 unsigned list_ctas(const PoolParams& p, int sms) {
   return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(sms, pool_words(p.num_pages) / 4 / 64)));
 }

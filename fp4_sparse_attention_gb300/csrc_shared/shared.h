@@ -62,7 +62,7 @@ struct PoolParams {
   int64_t table_stride;
   int32_t width;             // entries of a row
   uint32_t* bitmap;          // workspace: a bit per page, in whole words
-  int32_t* rank;             // workspace: pages in use before each word
+  int32_t* rank;             // workspace: pages in use before each four words
   // release
   int32_t* free_pages;
   int32_t* num_free;

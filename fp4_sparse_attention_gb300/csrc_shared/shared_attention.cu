@@ -37,13 +37,15 @@
 // Bounds and figures (bf16, cold caches).  A tile of a full block is 16.8 MFLOP for
 // 64 KB: with every row of 256 pairs on the same keys the tensor pipe and the
 // softmax beside it bound it (2,048 rows x 32/8 heads on 8,191 + 512..640 keys:
-// 195.2 us, 1,463 TFLOP/s, 76 % of a burst of large library products; a tile takes
+// 196 us, 1,459 TFLOP/s, 76 % of a burst of large library products, and 205 us
+// where long runs of calls bring the clock to the power limit; a tile takes
 // 2,700 cycles, of which its products need 2,180); with keys of a request's own or
-// few rows a group HBM does (8 groups x 24 rows x 40/8 heads, 365 MB: 80.7 us,
+// few rows a group HBM does (8 groups x 24 rows x 40/8 heads, 365 MB: 82.7 us,
 // 6.4 TB/s while the runs last; no prefix, 64 requests x 8,192 keys, 1,075 MB:
-// 171 us, 6.3 TB/s, 94 % of a copy).  What a short call pays: 2 us plan, 2 us until a
+// 172 us, 6.3 TB/s, 93 % of a copy, and 189 us as one group, whose 32 requests a
+// block each have tiles of their own).  What a short call pays: 2 us plan, 2 us until a
 // run is known, 2 us for the first pages and keys, 2 us output, 4-7 us join (2
-// requests on 200 keys 13.8 us, 64 samples of 32,768 keys 53 us).
+// requests on 200 keys 13.9 us, 64 samples of 32,768 keys 53.4 us).
 #include <algorithm>
 #include <atomic>
 #include <cstddef>
@@ -141,8 +143,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   const SharedParams& sp = pl.sp;
   const AttnParams& p = sp.a;
   // What a small call gives comes to shared memory in one round trip: read where
-  // it is needed, it is a chain of five.  (48 requests: 81.5 -> 80.7 us; 16: 35.8
-  // -> 35.1; two, whose arrays are a line each: 13.9 -> 14.1.)
+  // it is needed, it is a chain of five.  (48 requests: 0.8 us less; 16: 0.7; two,
+  // whose arrays are a line each: 0.2 more.)
   __shared__ int32_t cu_q_s[kPlanReqs + 1], cu_k_s[kPlanReqs + 1], qo_s[kPlanReqs], groups_s[kPlanReqs + 1], prefix_s[kPlanReqs], seen_s[kPlanRows];
   const int32_t *cu_q = p.cu_seqlens_q, *cu_k = p.cu_seqlens_k, *qo = p.qo_offset, *groups = sp.group_offsets, *prefix_lens = sp.prefix_len;
   const int32_t* visible = p.visible_len;
@@ -429,8 +431,9 @@ __device__ __forceinline__ void cp_async_arrive_extra(uint32_t bar) {
 // request's own tile is multiplied with the weights of all rows of an
 // accumulator: the other requests' are zeros, but its values may be infinite or
 // NaN, which concerns nobody else.  (With the zeros that their output then has
-// to begin with, 64 samples take 53.9 for 53.2 us, 8 groups 82.1 for 80.5, rows
-// of one request what they took.)
+// to begin with, 64 samples take 53.9 for 53.2 us, 8 groups 82.1 for 80.5, 64
+// requests of 8,192 keys without a prefix 189 for 182, rows of one request what
+// they took.  Masks made once a tile and eight products in a row were no faster.)
 __device__ __forceinline__ void tc_mma_f16_tmem_lanes(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate,
                                                       int from, int to) {
   uint32_t off[4];

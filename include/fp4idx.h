@@ -591,6 +591,13 @@ fp4idx_status_t fp4idx_build_tables(const int32_t* cached_len, const int32_t* ne
  * counts are kept: the held entries of the tables -- the first
  * ceil(cached_len[b] / page_size) of row b -- are all that says which pages
  * are in use, so the calls can be repeated and nothing can drift.
+ *
+ * fp4idx_fork_requests and fp4idx_build_tables both take pages from the head of
+ * free_pages, and how many is known on the device only.  To run one behind the
+ * other without reading the number back, list the free pages again in between:
+ * fp4idx_release_pages of no request (num_released 0), once the lengths in
+ * cached_len cover the pages that were taken (a fork's do; after
+ * fp4idx_build_tables, once the new tokens are added to them).
  * ---------------------------------------------------------------------- */
 
 /*
@@ -622,7 +629,9 @@ fp4idx_status_t fp4idx_build_tables(const int32_t* cached_len, const int32_t* ne
  * uninitialised.  The result is the same from call to call.  No allocation, no
  * synchronisation; graph-capturable; replays see updated device metadata.
  * Supported: as fp4idx_paged_attention, up to 2^20 groups and at most 2^20 rows
- * a group; num_groups * ceil(max_group_rows * H / Hkv / 256) at most 2^20.
+ * a group; at most 2^20 blocks, num_groups * ceil(max_group_rows * H / Hkv / 256),
+ * and fewer than 2^31 tiles of 128 keys in all, counting max_seqlen_k keys for
+ * every request and twice for every block, of every K/V head.
  */
 typedef struct fp4idx_shared_attention {
   fp4idx_attention_t attention;
